@@ -1,7 +1,8 @@
 /*
- * hisparse.h -- C ABI of libhisparse: the HiSparse decode-time KV-row swap-in
- * and the indexed KV-row movers, as hand-written CUDA kernels for GB300
- * (sm_103a).
+ * hisparse.h -- C ABI of libhisparse: the HiSparse decode-time KV-row swap-in,
+ * the indexed KV-row movers and the operators around a paged KV cache (slot
+ * assignment, query/key norm with rotation and cache write, attention), as
+ * hand-written CUDA kernels for GB300 (sm_103a).
  *
  * Conventions shared by every entry point
  *  - All calls are asynchronous and stream-ordered on `stream` (a CUDA runtime
@@ -17,7 +18,8 @@
  *  - On any non-HS_OK return, hs_last_error() holds a message for the calling
  *    thread.  Empty work (batch == 0, top_k == 0, n == 0) returns HS_OK and
  *    launches nothing.
- *  - No floating point is involved: rows are opaque bytes.
+ *  - Rows are opaque bytes and no floating point is involved, except in
+ *    hs_fp8_store_kv, hs_qk_norm_rope_store and hs_paged_attention.
  */
 #ifndef HISPARSE_H
 #define HISPARSE_H
@@ -46,6 +48,7 @@ typedef enum hs_err {
 #define HS_ST_TIMEOUT 16      /* a bounded wait inside a kernel gave up (see hs_swap_in) */
 #define HS_ST_BAD_STATE 32    /* req_state[b] >= num_states: row emitted -1 */
 #define HS_ST_BAD_INDEX 64    /* a mover index was out of range: that row was skipped */
+#define HS_ST_NO_BLOCK 128    /* hs_assign_slots: the free blocks ran out before this row */
 
 /* hs_swap_in_args.flags */
 #define HS_SEQ_LENS_I64 1  /* seq_lens is int64 (else int32) */
@@ -421,6 +424,209 @@ hs_err hs_gather_misses(const uint64_t* pool_ptrs, const uint64_t* hot_ptrs, int
                         int32_t top_k, int32_t* status, hs_stream_t stream);
 
 /*
+ * hs_assign_slots -- block tables and slot maps from the requests' lengths:
+ * every request of the batch gets new_lens[b] more tokens behind the
+ * ctx_lens[b] it has, opens the cache blocks they need and learns the slot of
+ * each.  With r = req_state[b], c = ctx_lens[b], n = new_lens[b] (0 for a
+ * padding row, req_state[b] < 0) and bs = block_size:
+ *   cu_new[0] = 0, cu_new[b+1] = cu_new[b] + n;   seq_lens[b] = c + n
+ *   the row holds ceil(c / bs) blocks and opens ceil((c + n) / bs) - ceil(c / bs)
+ *   more; the j-th block that the batch opens (rows in order, a row's blocks in
+ *   order) is free_blocks[*free_top - 1 - j], written to block_table[r]
+ *   *free_top_out = *free_top - blocks opened
+ *   token t = cu_new[b] + i (i < n) has position p = c + i:
+ *   cache_loc[t] = block_table[r][p / bs] * bs + p % bs, positions[t] = p,
+ *   token_row[t] = b
+ * Entries from cu_new[batch] to max_tokens get -1 in all three.  cache_loc is
+ * what hs_store_kv, hs_fp8_store_kv and hs_qk_norm_rope_store take, cu_new and
+ * seq_lens what hs_paged_attention takes.  Defined by this library (the pages
+ * leave block allocation to the caller).
+ *
+ * Rows that cannot be served open no block, keep seq_lens[b] = c and get
+ * cache_loc -1 for their tokens (which still have their place in cu_new):
+ *   HS_ST_BAD_STATE  req_state[b] >= num_states, c < 0, n < 0 (counts as 0),
+ *                    n > max_tokens (counts as 0), or c + n beyond the
+ *                    table's table_blocks * bs positions
+ *   HS_ST_BAD_INDEX  cu_new[b+1] > max_tokens (entries behind it do not exist)
+ *   HS_ST_NO_BLOCK   fewer free blocks than the batch needs up to and with this
+ *                    row (rows behind it that open none are still served)
+ * HS_ST_BAD_INDEX is also set, and that token's cache_loc is -1, when the entry
+ * of a token's block is negative.
+ *
+ *  ctx_lens    int32/int64 [batch] (flags & HS_SEQ_LENS_I64); a value above
+ *              INT32_MAX is HS_ST_BAD_STATE
+ *  new_lens    int32 [batch]
+ *  req_state   int32/int64 [batch] (flags & HS_REQ_STATE_I64)
+ *  block_table int32 [num_states, >=table_blocks] in/out, stride in elements
+ *  free_blocks int32 [num_free], a stack; free_top int32 [1], its height (taken
+ *              as within [0, num_free]); free_top_out int32 [1]
+ *  cu_new      int32 [batch + 1]; seq_lens like ctx_lens [batch]
+ *  cache_loc   int64 [max_tokens]; positions int64 [max_tokens] or NULL;
+ *              token_row int32 [max_tokens] or NULL
+ *  status      int32 [batch] or NULL, overwritten (a set of HS_ST_* bits)
+ * seq_lens may be ctx_lens and free_top_out may be free_top: a captured call
+ * then carries the lengths and the stack from one replay to the next.
+ * Preconditions (not checked): distinct req_state values among the real rows;
+ * the buffers overlap in no other way.  Limits: batch <= 4096, max_tokens and
+ * num_free <= INT32_MAX (else HS_ERR_UNSUPPORTED).
+ */
+hs_err hs_assign_slots(const void* ctx_lens, const int32_t* new_lens, const void* req_state,
+                       int32_t batch, int32_t flags, int32_t* block_table,
+                       int64_t block_table_stride, int64_t num_states, int32_t table_blocks,
+                       int32_t block_size, const int32_t* free_blocks, int64_t num_free,
+                       const int32_t* free_top, int32_t* free_top_out, int32_t* cu_new,
+                       void* seq_lens, int64_t* cache_loc, int64_t* positions,
+                       int32_t* token_row, int64_t max_tokens, int32_t* status,
+                       hs_stream_t stream);
+
+/* Element types of a cache that hs_qk_norm_rope_store writes and
+ * hs_paged_attention reads: HS_DT_F32 / F16 / BF16, or FP8 E4M3 as
+ * hs_fp8_store_kv describes it. */
+#define HS_DT_E4M3 3
+
+/* hs_qk_norm_rope_args.flags */
+#define HS_ROPE_INTERLEAVED 1 /* rotate pairs (2i, 2i+1); else (i, i + rot_dim/2) */
+
+/*
+ * hs_qk_norm_rope_store -- root-mean-square norm of every query and key head,
+ * rotary positions, and the K/V write into a paged cache, in one pass.  For
+ * token t, head x[0..D) of q or k, with weight w and position p = positions[t]:
+ *   y[d] = x[d] / sqrt(mean(x^2) + eps) * w[d]      (y = x where w is NULL)
+ *   for i < rot_dim / 2, (a, b) = (i, i + rot_dim/2), or (2i, 2i+1) with
+ *   HS_ROPE_INTERLEAVED, cos = cos_sin[p][i], sin = cos_sin[p][rot_dim/2 + i]:
+ *   z[a] = y[a] * cos - y[b] * sin,  z[b] = y[b] * cos + y[a] * sin
+ *   z[d] = y[d] for d >= rot_dim
+ * q's z goes to q_out, k's z to k_cache and v (as it is) to v_cache at slot
+ * cache_loc[t], with the slots, layouts and FP8 scaling of hs_fp8_store_kv
+ * (HS_DT_E4M3: e4m3(fp32(z * fp32(1 / scale))), saturated; otherwise rounded to
+ * the cache's type).  Everything is computed in fp32 and rounded once.
+ * Defined by this library, beside tokenspeed tokenspeed_kernel/ops/kvcache/
+ * triton.py, fused_fp8_set_kv_buffer (the cache write).
+ *
+ *  q [n_tokens, num_heads, head_dim], k and v [n_tokens, num_kv_heads,
+ *              head_dim] of in_dtype, token and head strides in elements, dims
+ *              contiguous (views of one projection's output are fine)
+ *  q_weight, k_weight  in_dtype [head_dim] or NULL (no norm)
+ *  cos_sin     fp32 [max_pos, rot_dim] contiguous; may be NULL when rot_dim is 0
+ *  positions   int64 [n_tokens]; may be NULL when rot_dim is 0
+ *  q_out       in_dtype, strides in elements; may be q itself (same strides)
+ *  k_cache, v_cache  cache_dtype (in_dtype or HS_DT_E4M3); strides in bytes
+ *  cache_loc   int64 [n_tokens]
+ *  k_scale, v_scale  device fp32 [1] or NULL (HS_DT_E4M3 only)
+ *  status      int32 [1] or NULL: HS_ST_BAD_INDEX is OR-ed in when a token's
+ *              slot is outside [0, num_slots) (its K and V are skipped) or its
+ *              position outside [0, max_pos) (its q and K are skipped)
+ * A token of length 0 head (x all zero) stays zero.  Limits: head_dim <= 1024,
+ * rot_dim even and <= head_dim, num_slots < 2^32, (num_heads + 2 *
+ * num_kv_heads) * head_dim < 2^31 (else HS_ERR_UNSUPPORTED).
+ * Preconditions (not checked): cache_loc values in range are distinct; no
+ * buffer overlaps another, but for q_out = q.
+ */
+typedef struct hs_qk_norm_rope_args {
+  int64_t n_tokens;
+  int32_t num_heads, num_kv_heads, head_dim, rot_dim;
+  int32_t in_dtype, cache_dtype;
+  int32_t flags, page_size;
+  float eps;
+  int32_t reserved; /* 0 */
+  const void* q; int64_t q_stride_token; int64_t q_stride_head;
+  const void* k; int64_t k_stride_token; int64_t k_stride_head;
+  const void* v; int64_t v_stride_token; int64_t v_stride_head;
+  const void* q_weight; const void* k_weight;
+  const float* cos_sin; int64_t max_pos;
+  const int64_t* positions;
+  void* q_out; int64_t out_stride_token; int64_t out_stride_head;
+  void* k_cache; void* v_cache;
+  int64_t cache_stride_page; int64_t cache_stride_offset; int64_t cache_stride_head;
+  int64_t num_slots;
+  const int64_t* cache_loc;
+  const float* k_scale; const float* v_scale;
+  int32_t* status;
+} hs_qk_norm_rope_args;
+
+hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t stream);
+
+/*
+ * hs_paged_attention -- causal attention of a chunk of new tokens of every
+ * request over its paged KV cache (which holds the new tokens' keys and values
+ * already).  Request b with r = req_state[b] has the queries t in
+ * [cu_q[b], cu_q[b+1]), n of them, the last n of its L = seq_lens[b] tokens:
+ * query t has position p = L - n + (t - cu_q[b]) and sees the keys j with
+ *   0 <= j <= p, and p - window < j where window > 0.
+ * Key j of the request is in slot block_table[r][j / page_size] * page_size +
+ * j % page_size.  For query head h, with kv head g = h / (num_heads /
+ * num_kv_heads) and s_j = scale * k_scale * (q[t][h] . k_j[g]):
+ *   out[t][h] = sum_j exp(s_j - lse) * v_scale * v_j[g],
+ *   lse[t][h] = log(sum_j exp(s_j))     (natural logarithm)
+ * A query that sees no key (p < 0) gives zeros and lse = -inf.  Chunks of one
+ * token are a decode step, chunks as long as the sequence a whole prompt, and
+ * one call mixes them freely.  Defined by this library: it reads the caches
+ * that hs_store_kv, hs_fp8_store_kv and hs_qk_norm_rope_store write.
+ *
+ *  q, out      in_dtype [n_tokens, num_heads, head_dim], token and head strides
+ *              in elements, dims contiguous
+ *  lse         fp32 [n_tokens, num_heads] contiguous, or NULL
+ *  k_cache, v_cache  cache_dtype (in_dtype or HS_DT_E4M3) [num_pages,
+ *              page_size, num_kv_heads, head_dim], strides in bytes, dims
+ *              contiguous, as in hs_fp8_store_kv
+ *  block_table int32 [num_states, >=table_blocks], stride in elements
+ *  req_state   int32/int64 [batch] (flags & HS_REQ_STATE_I64), negative = padding
+ *  cu_q        int32 [batch + 1], increasing; seq_lens int32/int64 [batch]
+ *              (flags & HS_SEQ_LENS_I64)
+ *  k_scale, v_scale  device fp32 [1] or NULL (HS_DT_E4M3 only)
+ *  max_q_len   a bound on every request's n (host value; it sizes the launch)
+ *  status      int32 [batch] or NULL, overwritten
+ *  workspace   device memory, 256-byte aligned, of at least
+ *              hs_paged_attention_workspace_bytes(args) bytes (NULL if that is
+ *              0).  Its contents need not be set and mean nothing afterwards;
+ *              calls that may run at the same time (two streams, two graphs)
+ *              need one each.
+ * Padding rows and rows whose queries lie outside [0, n_tokens) or number less
+ * than 0 write nothing (status 0 / HS_ST_BAD_STATE); rows with r >= num_states,
+ * n > max_q_len or L beyond table_blocks * page_size write nothing and report
+ * HS_ST_BAD_STATE.  Rows of q that belong to no request are left as they were
+ * in out and lse.  A block index outside [0, num_pages) that a query of the row
+ * can see stands for keys and values that are zero, and sets HS_ST_BAD_INDEX.
+ * Cache bytes of positions that no query of a request sees have no effect,
+ * whatever they hold; a NaN or infinity in the value row of a position that
+ * some of its queries see and others do not may make either kind NaN.
+ * Scores, sums and outputs are accumulated in fp32.  For 16-bit inputs with
+ * head_dim 64 or 128 the products run on the tensor cores, with the softmax
+ * weights rounded to the cache's compute type (in_dtype, fp16 for HS_DT_E4M3);
+ * with HS_DT_E4M3 bf16 queries are multiplied by a power of two per row and
+ * taken as fp16.  Results do not depend on what else is in the batch, except
+ * through the order of fp32 sums.
+ * Limits: head_dim <= 512, num_heads a multiple of num_kv_heads, batch <= 4096,
+ * L <= INT32_MAX (else HS_ERR_UNSUPPORTED, or HS_ST_BAD_STATE for L).
+ */
+typedef struct hs_paged_attention_args {
+  int32_t batch, num_heads, num_kv_heads, head_dim;
+  int32_t in_dtype, cache_dtype;
+  int32_t flags, page_size;
+  int32_t max_q_len, window;
+  float scale;
+  int32_t table_blocks;
+  int64_t n_tokens;
+  const void* q; int64_t q_stride_token; int64_t q_stride_head;
+  void* out; int64_t out_stride_token; int64_t out_stride_head;
+  float* lse;
+  const void* k_cache; const void* v_cache;
+  int64_t cache_stride_page; int64_t cache_stride_offset; int64_t cache_stride_head;
+  int64_t num_pages;
+  const int32_t* block_table; int64_t block_table_stride; int64_t num_states;
+  const void* req_state; const int32_t* cu_q; const void* seq_lens;
+  const float* k_scale; const float* v_scale;
+  int32_t* status;
+  void* workspace; int64_t workspace_bytes;
+} hs_paged_attention_args;
+
+/* Bytes of workspace that this call needs on the current device (0 for none,
+ * negative hs_err on bad arguments).  It depends on sizes and types only. */
+int64_t hs_paged_attention_workspace_bytes(const hs_paged_attention_args* args);
+
+hs_err hs_paged_attention(const hs_paged_attention_args* args, hs_stream_t stream);
+
+/*
  * hs_probe_read -- measurement utility, not part of the method: stream-read
  * `bytes` bytes (16-byte aligned pointer, bytes % 16 == 0) from device or
  * pinned host memory with every SM, folding them into *sink (device uint64
@@ -455,7 +661,7 @@ const char* hs_last_error(void);
  */
 hs_err hs_wait_selftest(int32_t max_polls, int32_t* status, hs_stream_t stream);
 
-#define HS_ABI_VERSION 8
+#define HS_ABI_VERSION 9
 int32_t hs_abi_version(void);
 
 #ifdef __cplusplus

@@ -1,4 +1,4 @@
-"""HiSparse decode-time KV-row swap-in and indexed KV-row movers for GB300.
+"""HiSparse decode-time KV-row swap-in, indexed KV-row movers and paged-cache operators for GB300.
 
 Thin PyTorch binding over libhisparse (include/hisparse.h): it checks tensor
 dtypes/shapes and passes raw pointers, strides and the current CUDA stream;
@@ -12,6 +12,9 @@ Entry points (same names as the C ABI):
   store_kv(...)      hs_store_kv     -- k_dst[loc] = k_src, v_dst[loc] = v_src
   transfer_kv(...)   hs_transfer_kv  -- per-layer / all-layer indexed row copy
   probe_read(...)    hs_probe_read   -- streaming-read bandwidth probe
+  assign_slots(...)        hs_assign_slots       -- block tables and slot maps from lengths
+  qk_norm_rope_store(...)  hs_qk_norm_rope_store -- q/k norm, rotary positions, cache write
+  paged_attention(...)     hs_paged_attention    -- new tokens' attention over the paged cache
 """
 from __future__ import annotations
 
@@ -21,13 +24,15 @@ import torch
 
 from . import _capi
 from ._capi import (HisparseError, SwapInArgs, ST_BAD_HOT_ROW, ST_BAD_INDEX,  # noqa: F401
-                    ST_BAD_LRU_SLOT, ST_BAD_POOL_ROW, ST_BAD_STATE, ST_DUP_ID, ST_TIMEOUT)
+                    ST_BAD_LRU_SLOT, ST_BAD_POOL_ROW, ST_BAD_STATE, ST_DUP_ID, ST_NO_BLOCK,
+                    ST_TIMEOUT)
 
 __all__ = ["swap_in", "swap_in_args", "make_swap_in_args", "gather_misses", "fp8_store_kv",
            "invalidate_tokens", "wait_selftest", "swap_in_timeout_selftest",
            "swap_in_layers", "swap_in_layers_timeout_selftest", "layer_args_array",
            "store_kv", "transfer_kv",
-           "transfer_kv_layers", "probe_read", "swap_in_smem_bytes", "library_path",
+           "transfer_kv_layers", "probe_read", "assign_slots", "qk_norm_rope_store",
+           "paged_attention", "paged_attention_workspace_bytes", "swap_in_smem_bytes", "library_path",
            "HisparseError", "SwapInArgs"]
 
 
@@ -311,6 +316,7 @@ def gather_misses(pool_layers, hot_layers, miss_src, miss_dst, miss_count, *, ha
 
 
 _FP8_IN = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_FP8_CACHE = (torch.uint8, torch.float8_e4m3fn)
 
 
 def fp8_store_kv(k, v, k_cache, v_cache, cache_loc, *, k_scale=None, v_scale=None,
@@ -432,3 +438,247 @@ def probe_read(src, sink, stream=None) -> None:
     ptr, n, rb, pitch = _byte_rows(src.view(-1), "src")
     _capi.check(_lib().hs_probe_read(ptr, n * rb, _ptr(sink), C.c_void_p(_stream(stream))),
                 "hs_probe_read")
+
+
+def _on_device(device, **tensors):
+    """Every given tensor is on the same CUDA device; returns its device guard."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    return torch.cuda.device(device)
+
+
+def _lens_flags(lens, req_state, batch, name):
+    """(seq, req) width flags of int32 or int64 [batch] lengths and state rows."""
+    for t, what in ((lens, name), (req_state, "req_state")):
+        if t.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
+        _need(t, t.dtype, what, 1)
+        if t.numel() != batch:
+            raise ValueError(f"{what} needs one entry per batch row ({batch}), got {t.numel()}")
+    return (_capi.SEQ_LENS_I64 if lens.dtype == torch.int64 else 0) | (
+        _capi.REQ_STATE_I64 if req_state.dtype == torch.int64 else 0)
+
+
+def assign_slots(ctx_lens, new_lens, req_state, block_table, free_blocks, free_top, *, block_size,
+                 cu_new, seq_lens, cache_loc, positions=None, token_row=None, free_top_out=None,
+                 status=None, stream=None) -> None:
+    """Give new_lens[b] more tokens to every request and fill in their places (see
+    include/hisparse.h): opened blocks come from the top of the stack ``free_blocks`` [N]
+    (height ``free_top`` [1]) into ``block_table`` [R, blocks]; ``cu_new`` [B + 1] and
+    ``seq_lens`` [B] get the running token count and the new lengths, ``cache_loc`` /
+    ``positions`` / ``token_row`` [max_tokens] each token's slot, position and batch row (-1
+    behind the last token).  Lengths and state rows are int32 or int64 (``seq_lens`` as
+    ``ctx_lens``); ``cache_loc`` and ``positions`` int64; the rest int32.  ``free_top_out``
+    (default ``free_top`` itself) gets the new height, and ``seq_lens`` may be ``ctx_lens``:
+    a captured call then carries both from one replay to the next."""
+    batch = new_lens.numel()
+    _need(new_lens, torch.int32, "new_lens", 1)
+    flags = _lens_flags(ctx_lens, req_state, batch, "ctx_lens")
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(free_blocks, torch.int32, "free_blocks", 1)
+    if free_top_out is None:
+        free_top_out = free_top
+    for t, name, n in ((free_top, "free_top", 1), (free_top_out, "free_top_out", 1),
+                       (cu_new, "cu_new", batch + 1)):
+        _need(t, torch.int32, name, 1)
+        if t.numel() != n:
+            raise ValueError(f"{name} needs {n} entries, got {t.numel()}")
+    _need(seq_lens, ctx_lens.dtype, "seq_lens", 1)
+    _need(cache_loc, torch.int64, "cache_loc", 1)
+    if seq_lens.numel() != batch:
+        raise ValueError("seq_lens needs one entry per batch row")
+    for t, dtype, name, n in ((positions, torch.int64, "positions", cache_loc.numel()),
+                              (token_row, torch.int32, "token_row", cache_loc.numel()),
+                              (status, torch.int32, "status", batch)):
+        if t is not None:
+            _need(t, dtype, name, 1)
+            if t.numel() != n:
+                raise ValueError(f"{name} needs {n} entries, got {t.numel()}")
+    with _on_device(ctx_lens.device, new_lens=new_lens, req_state=req_state,
+                    block_table=block_table, free_blocks=free_blocks, free_top=free_top,
+                    free_top_out=free_top_out, cu_new=cu_new, seq_lens=seq_lens,
+                    cache_loc=cache_loc, positions=positions, token_row=token_row, status=status):
+        _capi.check(_lib().hs_assign_slots(
+            _ptr(ctx_lens), _ptr(new_lens), _ptr(req_state), batch, flags, _ptr(block_table),
+            block_table.stride(0), block_table.shape[0], block_table.shape[1], int(block_size),
+            _ptr(free_blocks), free_blocks.numel(), _ptr(free_top), _ptr(free_top_out),
+            _ptr(cu_new), _ptr(seq_lens), _ptr(cache_loc), _ptr(positions), _ptr(token_row),
+            cache_loc.numel(), _ptr(status), C.c_void_p(_stream(stream))), "hs_assign_slots")
+
+
+def _paged_cache(k_cache, v_cache, dtype, page_size):
+    """(cache dtype code, kv heads, dim, page / offset / head strides in bytes, pages) of a
+    paged cache [pages, page_size, heads, dim] or [slots, heads, dim] of ``dtype`` or FP8."""
+    if k_cache.dtype != v_cache.dtype or (k_cache.dtype != dtype
+                                          and k_cache.dtype not in _FP8_CACHE):
+        raise TypeError(f"caches must both be {dtype}, float8_e4m3fn or uint8 (E4M3 codes)")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache need the same shape and layout")
+    strides, shape = k_cache.stride(), k_cache.shape
+    if k_cache.dim() == 4:
+        if shape[1] != page_size:
+            raise ValueError(f"page_size mismatch: cache has {shape[1]}, expected {page_size}")
+        pages, (page, off, head) = shape[0], strides[:3]
+    elif k_cache.dim() == 3:
+        pages, page, (off, head) = shape[0] // page_size, strides[0] * page_size, strides[:2]
+    else:
+        raise ValueError("caches must be 3-D or 4-D")
+    if shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError("caches need contiguous dims")
+    size = k_cache.element_size()
+    code = _capi.DT_E4M3 if k_cache.dtype in _FP8_CACHE and dtype != k_cache.dtype else _FP8_IN[dtype]
+    return code, shape[-2], shape[-1], page * size, off * size, head * size, pages
+
+
+def _heads(t, dtype, name, shape):
+    """Token and head strides of [tokens, heads, dim] with contiguous dims."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or (shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be {list(shape)} with a contiguous last dim, got "
+                         f"{list(t.shape)}")
+    return t.stride(0), t.stride(1)
+
+
+def _cache_scales(code, k_scale, v_scale):
+    for sc, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if sc is not None:
+            _need(sc, torch.float32, name)
+            if code != _capi.DT_E4M3 or sc.numel() != 1:
+                raise ValueError(f"{name}: one element, with an FP8 cache only")
+
+
+def qk_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k_cache, v_cache,
+                       cache_loc, *, eps=1e-6, interleaved=False, k_scale=None, v_scale=None,
+                       page_size=16, status=None, stream=None) -> None:
+    """Norm every q and k head [T, heads, dim] (root mean square, times ``q_weight`` /
+    ``k_weight`` [dim]; None = no norm), rotate its first rot_dim dims by the angles
+    ``cos_sin`` [max_pos, rot_dim] (fp32, cosines then sines) of ``positions`` [T], write q to
+    ``q_out`` (may be q) and k and v to slot cache_loc[t] of a paged cache (see
+    include/hisparse.h; layouts and FP8 scales as in ``fp8_store_kv``).  float32, float16 or
+    bfloat16; the cache has the same type or is FP8.  ``cos_sin`` None = no rotation."""
+    if q.dtype not in _FP8_IN:
+        raise TypeError("q must be float32, float16 or bfloat16")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, dim], got {list(q.shape)}")
+    code, kv_heads, dim, c_page, c_off, c_head, pages = _paged_cache(k_cache, v_cache, q.dtype,
+                                                                     page_size)
+    T, heads = q.shape[0], q.shape[1]
+    qs = _heads(q, q.dtype, "q", (T, heads, dim))
+    ks = _heads(k, q.dtype, "k", (T, kv_heads, dim))
+    vs = _heads(v, q.dtype, "v", (T, kv_heads, dim))
+    os = _heads(q_out, q.dtype, "q_out", (T, heads, dim))
+    if q_out.data_ptr() == q.data_ptr() and os != qs:
+        raise ValueError("q_out may be q itself, not another view of its memory")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, q.dtype, name, 1)
+            if w.numel() != dim:
+                raise ValueError(f"{name} needs {dim} entries")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin", 2)
+        _need(positions, torch.int64, "positions", 1)
+        if not cos_sin.is_contiguous() or positions.numel() != T:
+            raise ValueError("cos_sin must be contiguous and positions have one entry per token")
+        max_pos, rot = cos_sin.shape
+    else:
+        positions = None
+    _need(cache_loc, torch.int64, "cache_loc", 1)
+    if cache_loc.numel() != T:
+        raise ValueError("cache_loc needs one entry per token")
+    _cache_scales(code, k_scale, v_scale)
+    if status is not None:
+        _need(status, torch.int32, "status", 1)
+    with _on_device(q.device, k=k, v=v, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+                    positions=positions, q_out=q_out, k_cache=k_cache, v_cache=v_cache,
+                    cache_loc=cache_loc, k_scale=k_scale, v_scale=v_scale, status=status):
+        args = _capi.QkNormRopeArgs(
+            T, heads, kv_heads, dim, rot, _FP8_IN[q.dtype], code,
+            _capi.ROPE_INTERLEAVED if interleaved else 0, page_size, eps, 0, _ptr(q), *qs, _ptr(k),
+            *ks, _ptr(v), *vs, _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), max_pos,
+            _ptr(positions), _ptr(q_out), *os, _ptr(k_cache), _ptr(v_cache), c_page, c_off, c_head,
+            pages * page_size, _ptr(cache_loc), _ptr(k_scale), _ptr(v_scale), _ptr(status))
+        _capi.check(_lib().hs_qk_norm_rope_store(C.byref(args), C.c_void_p(_stream(stream))),
+                    "hs_qk_norm_rope_store")
+
+
+def _paged_attention_args(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, *,
+                          max_q_len, scale, window, k_scale, v_scale, page_size, lse, status):
+    if q.dtype not in _FP8_IN:
+        raise TypeError("q must be float32, float16 or bfloat16")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, dim], got {list(q.shape)}")
+    code, kv_heads, dim, c_page, c_off, c_head, pages = _paged_cache(k_cache, v_cache, q.dtype,
+                                                                     page_size)
+    T, heads = q.shape[0], q.shape[1]
+    qs = _heads(q, q.dtype, "q", (T, heads, dim))
+    os = _heads(out, q.dtype, "out", (T, heads, dim))
+    _need(cu_q, torch.int32, "cu_q", 1)
+    batch = cu_q.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_q needs batch + 1 entries")
+    flags = _lens_flags(seq_lens, req_state, batch, "seq_lens")
+    _need(block_table, torch.int32, "block_table", 2)
+    if lse is not None:
+        _need(lse, torch.float32, "lse", 2)
+        if tuple(lse.shape) != (T, heads) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous [{T}, {heads}]")
+    if status is not None:
+        _need(status, torch.int32, "status", 1)
+        if status.numel() != batch:
+            raise ValueError("status needs one entry per batch row")
+    _cache_scales(code, k_scale, v_scale)
+    return _capi.PagedAttentionArgs(
+        batch, heads, kv_heads, dim, _FP8_IN[q.dtype], code, flags, page_size, max_q_len, window,
+        dim ** -0.5 if scale is None else scale, block_table.shape[1], T, _ptr(q), *qs, _ptr(out),
+        *os, _ptr(lse), _ptr(k_cache), _ptr(v_cache), c_page, c_off, c_head, pages,
+        _ptr(block_table), block_table.stride(0), block_table.shape[0], _ptr(req_state),
+        _ptr(cu_q), _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale), _ptr(status), None, 0)
+
+
+def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
+                                    out, *, max_q_len, window=0, page_size=16) -> int:
+    """Bytes of workspace that ``paged_attention`` needs for tensors of these shapes and types."""
+    args = _paged_attention_args(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out,
+                                 max_q_len=max_q_len, scale=None, window=window, k_scale=None,
+                                 v_scale=None, page_size=page_size, lse=None, status=None)
+    with _on_device(q.device):
+        n = int(_lib().hs_paged_attention_workspace_bytes(C.byref(args)))
+    _capi.check(max(0, -n), "hs_paged_attention_workspace_bytes")
+    return n
+
+
+def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, *, max_q_len,
+                    scale=None, window=0, k_scale=None, v_scale=None, page_size=16, lse=None,
+                    status=None, workspace=None, stream=None) -> None:
+    """Causal attention of the new tokens q [T, heads, dim] over each request's keys and values
+    in a paged cache (see include/hisparse.h).  Request b has the queries cu_q[b] to cu_q[b + 1]
+    (at most ``max_q_len``), the last of its seq_lens[b] tokens, in the blocks of block_table
+    row req_state[b].  ``scale`` defaults to dim ** -0.5; ``window`` > 0 lets a query see the
+    last ``window`` keys only; ``lse`` [T, heads] gets the softmax's log-sum-exp.  ``workspace``
+    (uint8, 256-byte aligned, ``paged_attention_workspace_bytes`` of it) may be passed to keep
+    one for a captured graph; otherwise one is allocated for the call."""
+    args = _paged_attention_args(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out,
+                                 max_q_len=max_q_len, scale=scale, window=window, k_scale=k_scale,
+                                 v_scale=v_scale, page_size=page_size, lse=lse, status=status)
+    lib = _lib()
+    with _on_device(q.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                    req_state=req_state, cu_q=cu_q, seq_lens=seq_lens, out=out, lse=lse,
+                    k_scale=k_scale, v_scale=v_scale, status=status, workspace=workspace):
+        stream = _stream(stream)
+        if workspace is None:
+            n = int(lib.hs_paged_attention_workspace_bytes(C.byref(args)))
+            if n > 0:
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+                if stream != torch.cuda.current_stream().cuda_stream:
+                    # the allocator must not hand it out again before that stream is done
+                    workspace.record_stream(torch.cuda.ExternalStream(stream))
+        if workspace is not None:
+            _need(workspace, torch.uint8, "workspace", 1)
+            args.workspace, args.workspace_bytes = _ptr(workspace), workspace.numel()
+        _capi.check(lib.hs_paged_attention(C.byref(args), C.c_void_p(stream)),
+                    "hs_paged_attention")

@@ -20,18 +20,21 @@ ST_BAD_HOT_ROW = 8
 ST_TIMEOUT = 16
 ST_BAD_STATE = 32
 ST_BAD_INDEX = 64
+ST_NO_BLOCK = 128
 SEQ_LENS_I64 = 1
 REQ_STATE_I64 = 2
 OVERLAP_PREV = 4
-DT_F32, DT_F16, DT_BF16 = 0, 1, 2
+DT_F32, DT_F16, DT_BF16, DT_E4M3 = 0, 1, 2, 3
+ROPE_INTERLEAVED = 1
 XFER_HAS_V, XFER_DEVICE_SOURCES = 1, 2
-ABI_VERSION = 8
+ABI_VERSION = 9
 
 # Every symbol include/hisparse.h declares.
 EXPORTS = ("hs_swap_in", "hs_swap_in_smem_bytes", "hs_store_kv", "hs_transfer_kv",
            "hs_gather_misses", "hs_fp8_store_kv", "hs_invalidate_tokens", "hs_probe_read", "hs_err_string", "hs_status_string", "hs_last_error",
            "hs_abi_version", "hs_wait_selftest", "hs_swap_in_timeout_selftest",
-           "hs_swap_in_layers", "hs_swap_in_layers_timeout_selftest")
+           "hs_swap_in_layers", "hs_swap_in_layers_timeout_selftest", "hs_assign_slots",
+           "hs_qk_norm_rope_store", "hs_paged_attention", "hs_paged_attention_workspace_bytes")
 
 
 class SwapInArgs(C.Structure):
@@ -59,6 +62,48 @@ class SwapInArgs(C.Structure):
         ("res_bt", C.c_void_p), ("res_bt_stride", C.c_int64), ("res_bt_blocks", C.c_int32),
         ("res_block_size", C.c_int32), ("res_null_block", C.c_int32),
         ("max_seq_len", C.c_int64),
+    ]
+
+
+class QkNormRopeArgs(C.Structure):
+    """Mirror of ``hs_qk_norm_rope_args``."""
+    _fields_ = [
+        ("n_tokens", C.c_int64),
+        ("num_heads", C.c_int32), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+        ("rot_dim", C.c_int32), ("in_dtype", C.c_int32), ("cache_dtype", C.c_int32),
+        ("flags", C.c_int32), ("page_size", C.c_int32),
+        ("eps", C.c_float), ("reserved", C.c_int32),
+        ("q", C.c_void_p), ("q_stride_token", C.c_int64), ("q_stride_head", C.c_int64),
+        ("k", C.c_void_p), ("k_stride_token", C.c_int64), ("k_stride_head", C.c_int64),
+        ("v", C.c_void_p), ("v_stride_token", C.c_int64), ("v_stride_head", C.c_int64),
+        ("q_weight", C.c_void_p), ("k_weight", C.c_void_p),
+        ("cos_sin", C.c_void_p), ("max_pos", C.c_int64), ("positions", C.c_void_p),
+        ("q_out", C.c_void_p), ("out_stride_token", C.c_int64), ("out_stride_head", C.c_int64),
+        ("k_cache", C.c_void_p), ("v_cache", C.c_void_p),
+        ("cache_stride_page", C.c_int64), ("cache_stride_offset", C.c_int64),
+        ("cache_stride_head", C.c_int64), ("num_slots", C.c_int64),
+        ("cache_loc", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+        ("status", C.c_void_p),
+    ]
+
+
+class PagedAttentionArgs(C.Structure):
+    """Mirror of ``hs_paged_attention_args``."""
+    _fields_ = [
+        ("batch", C.c_int32), ("num_heads", C.c_int32), ("num_kv_heads", C.c_int32),
+        ("head_dim", C.c_int32), ("in_dtype", C.c_int32), ("cache_dtype", C.c_int32),
+        ("flags", C.c_int32), ("page_size", C.c_int32), ("max_q_len", C.c_int32),
+        ("window", C.c_int32), ("scale", C.c_float), ("table_blocks", C.c_int32),
+        ("n_tokens", C.c_int64),
+        ("q", C.c_void_p), ("q_stride_token", C.c_int64), ("q_stride_head", C.c_int64),
+        ("out", C.c_void_p), ("out_stride_token", C.c_int64), ("out_stride_head", C.c_int64),
+        ("lse", C.c_void_p), ("k_cache", C.c_void_p), ("v_cache", C.c_void_p),
+        ("cache_stride_page", C.c_int64), ("cache_stride_offset", C.c_int64),
+        ("cache_stride_head", C.c_int64), ("num_pages", C.c_int64),
+        ("block_table", C.c_void_p), ("block_table_stride", C.c_int64), ("num_states", C.c_int64),
+        ("req_state", C.c_void_p), ("cu_q", C.c_void_p), ("seq_lens", C.c_void_p),
+        ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("status", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64),
     ]
 
 
@@ -112,6 +157,15 @@ def load() -> C.CDLL:
         lib.hs_invalidate_tokens.restype = C.c_int
         lib.hs_probe_read.argtypes = [vp, i64, vp, vp]
         lib.hs_probe_read.restype = C.c_int
+        lib.hs_assign_slots.argtypes = [vp, vp, vp, i32, i32, vp, i64, i64, i32, i32, vp, i64, vp,
+                                        vp, vp, vp, vp, vp, vp, i64, vp, vp]
+        lib.hs_assign_slots.restype = C.c_int
+        lib.hs_qk_norm_rope_store.argtypes = [C.POINTER(QkNormRopeArgs), vp]
+        lib.hs_qk_norm_rope_store.restype = C.c_int
+        lib.hs_paged_attention.argtypes = [C.POINTER(PagedAttentionArgs), vp]
+        lib.hs_paged_attention.restype = C.c_int
+        lib.hs_paged_attention_workspace_bytes.argtypes = [C.POINTER(PagedAttentionArgs)]
+        lib.hs_paged_attention_workspace_bytes.restype = i64
         lib.hs_err_string.argtypes = [i32]
         lib.hs_err_string.restype = C.c_char_p
         lib.hs_status_string.argtypes = [i32]

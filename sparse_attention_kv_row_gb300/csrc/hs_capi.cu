@@ -108,6 +108,7 @@ extern "C" const char* hs_status_string(int32_t bit) {
     case HS_ST_TIMEOUT: return "HS_ST_TIMEOUT";
     case HS_ST_BAD_STATE: return "HS_ST_BAD_STATE";
     case HS_ST_BAD_INDEX: return "HS_ST_BAD_INDEX";
+    case HS_ST_NO_BLOCK: return "HS_ST_NO_BLOCK";
     default: return "";
   }
 }

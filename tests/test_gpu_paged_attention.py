@@ -1,0 +1,300 @@
+"""paged_attention against a plain 64-bit statement: decode steps, short and long
+chunks, mixed batches, every type and cache form, page sizes that end inside a
+tile, odd head counts, windows, padding and empty rows, bad blocks, strided and
+unaligned inputs; unowned cache bytes hold NaN throughout."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from paged_cases import PagedInputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    return torch.device("cuda:0")
+
+
+def _hs():
+    import sparse_attention_kv_row_gb300 as hs
+
+    return hs
+
+
+DECODE = [(5, 1), (0, 1), (63, 1), (64, 1), (None, 0), (700, 1), (31, 1), (1500, 1)]
+DRAFTS = [(40, 4), (0, 3), (None, 0), (257, 1), (600, 5), (3, 0), (127, 2)]
+CHUNKS = [(0, 130), (None, 0), (300, 257), (500, 1), (77, 64), (3, 0), (0, 1), (1000, 33)]
+
+
+@pytest.mark.parametrize("lens", [DECODE, DRAFTS, CHUNKS], ids=["decode", "drafts", "chunks"])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("f16", "same"), ("bf16", "fp8"),
+                                         ("f16", "fp8")])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_types(dev, lens, dtype, cache, dim):
+    x = PagedInputs(lens, heads=8, kv_heads=2, dim=dim, dtype=dtype, cache=cache, page=16, seed=dim)
+    _, _, status = x.check(_hs(), dev, True)
+    assert not bool(status.any())
+
+
+@pytest.mark.parametrize("dtype,cache,dim", [("f32", "same", 64), ("f32", "fp8", 128),
+                                             ("bf16", "same", 40), ("f16", "fp8", 96),
+                                             ("bf16", "same", 256), ("f16", "same", 1),
+                                             ("bf16", "fp8", 320)])
+def test_general_form(dev, dtype, cache, dim):
+    x = PagedInputs([(0, 3), (70, 1), (None, 0), (33, 40), (100, 0)], heads=6, kv_heads=2, dim=dim,
+                    dtype=dtype, cache=cache, page=8, seed=dim, i64=False)
+    x.check(_hs(), dev, False)
+
+
+@pytest.mark.parametrize("page,flat", [(1, False), (3, False), (8, True), (48, False), (64, True),
+                                       (128, False), (256, False)])
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+def test_page_sizes(dev, page, flat, lens, cache):
+    x = PagedInputs(lens, heads=4, kv_heads=1, dim=128, dtype="bf16", cache=cache, page=page,
+                    flat=flat, seed=page)
+    x.check(_hs(), dev, True)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (3, 1), (5, 5), (12, 4), (16, 1), (7, 1), (48, 3)])
+@pytest.mark.parametrize("lens", [DECODE, DRAFTS, CHUNKS], ids=["decode", "drafts", "chunks"])
+def test_head_groups(dev, heads, kv_heads, lens):
+    x = PagedInputs(lens, heads=heads, kv_heads=kv_heads, dim=64, dtype="f16", page=16, seed=heads)
+    x.check(_hs(), dev, True)
+
+
+@pytest.mark.parametrize("window", [1, 2, 33, 100, 128, 500, 100000])
+@pytest.mark.parametrize("lens", [DECODE, DRAFTS, CHUNKS], ids=["decode", "drafts", "chunks"])
+def test_window(dev, window, lens):
+    """Blocks behind the window are given back: their entries are -1 and their bytes NaN."""
+    x = PagedInputs(lens, heads=4, kv_heads=2, dim=128, dtype="bf16", page=16, window=window, seed=window)
+    _, _, status = x.check(_hs(), dev, True)
+    assert not bool(status.any())
+
+
+def test_window_fp8(dev):
+    x = PagedInputs(CHUNKS + DECODE, heads=4, kv_heads=2, dim=64, dtype="bf16", cache="fp8", page=16,
+                    window=77, seed=5)
+    x.check(_hs(), dev, True)
+
+
+@pytest.mark.parametrize("dim,dtype,tensor_cores", [(128, "bf16", True), (80, "f16", False)])
+@pytest.mark.parametrize("long", [False, True])
+def test_rows_without_keys_and_bad_rows(dev, dim, dtype, tensor_cores, long):
+    """A chunk longer than its sequence, an empty sequence, a state row past the table, a
+    sequence past the table's blocks, too many queries; rows behind the last sequence."""
+    lens = [(20, 4), (9, 3), (30, 2), (10, 40 if long else 1), (50, 1)]
+    x = PagedInputs(lens, heads=4, kv_heads=2, dim=dim, dtype=dtype, page=16, seed=3, gap=3)
+    x.seq[0] = 2        # two of the four queries see nothing
+    x.seq[1] = 0        # none of three sees a key
+    x.req[2] = x.table.shape[0]
+    x.seq[4] = x.table.shape[1] * 16 + 1
+    out, lse, status = x.check(_hs(), dev, tensor_cores)
+    assert status.tolist() == [0, 0, 32, 0, 32]
+    if long:
+        _, _, status = x.check(_hs(), dev, tensor_cores, max_q=39)
+        assert status.tolist() == [0, 0, 32, 32, 32]
+
+
+def test_bad_cu(dev):
+    x = PagedInputs([(20, 4), (9, 3), (30, 2)], heads=4, kv_heads=2, dim=128, dtype="bf16", seed=3)
+    x.cu[3] = 50       # past the tokens
+    x.cu[1] = 8        # row 1 runs backwards, row 0 has more queries than announced
+    _, _, status = x.check(_hs(), dev, True, max_q=4)
+    assert status.tolist() == [32, 32, 32]
+
+
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+@pytest.mark.parametrize("dim,tensor_cores", [(128, True), (64, True), (48, False)])
+@pytest.mark.parametrize("n", [1, 50])
+def test_bad_blocks_are_zero_keys(dev, cache, dim, tensor_cores, n):
+    x = PagedInputs([(300, n), (200, n), (150, 1)], heads=4, kv_heads=2, dim=dim, dtype="bf16",
+                    cache=cache, page=16, seed=9)
+    x.table[x.req[0], 3] = x.kc.shape[0]
+    x.table[x.req[0], 7] = -1
+    x.table[x.req[2], 0] = 2 ** 31 - 1
+    _, _, status = x.check(_hs(), dev, tensor_cores)
+    assert status.tolist() == [64, 0, 64]
+
+
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
+def test_large_and_equal_scores(dev, lens):
+    """Scores of several hundred (weights that are nearly one-hot), and all scores equal."""
+    for sharp in (60.0, 0.0):
+        x = PagedInputs(lens, heads=4, kv_heads=1, dim=128, dtype="bf16", seed=4, sharp=sharp)
+        x.check(_hs(), dev, True)
+
+
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
+def test_fp8_keeps_small_and_huge_queries(dev, lens):
+    """bf16 queries beyond fp16's range on both sides, against an FP8 cache."""
+    for power in (18, -30):
+        x = PagedInputs(lens, heads=4, kv_heads=1, dim=128, dtype="bf16", cache="fp8", seed=4,
+                        scales=(2.0 ** -5, 0.11))
+        x.q *= 2.0 ** power
+        x.ks *= 2.0 ** -power
+        x.check(_hs(), dev, True)
+
+
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+def test_views_and_layouts(dev, lens, cache):
+    """q a slice of a packed projection, out strided, K and V interleaved in one cache."""
+    hs = _hs()
+    x = PagedInputs(lens, heads=4, kv_heads=2, dim=128, dtype="bf16", cache=cache, page=16, seed=8)
+    ref = x.plain()
+    tol, _ = x.tolerance(ref, True)
+    packed = torch.randn(x.T, 9, 128).to(torch.bfloat16)
+    packed[:, 2:6] = x.q
+    q = packed.to(dev)[:, 2:6]
+    both = torch.stack([x.kc.view(torch.uint8) if x.fp8 else x.kc,
+                        x.vc.view(torch.uint8) if x.fp8 else x.vc], 2).to(dev)
+    out = torch.full((x.T, 4, 2, 128), -7.0, dtype=torch.bfloat16, device=dev)
+    t = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    sc = lambda v: torch.tensor([v], device=dev) if x.fp8 else None  # noqa: E731
+    hs.paged_attention(q, both[:, :, 0], both[:, :, 1], t(x.table), t(x.req), t(x.cu), t(x.seq),
+                       out[:, :, 0], max_q_len=x.max_q + 13, page_size=16, k_scale=sc(x.ks),
+                       v_scale=sc(x.vs))
+    seen = ref[5]
+    assert bool(((out[:, :, 0].cpu().double() - ref[0]).abs() <= tol)[seen].all())
+    assert bool((out[:, :, 1] == -7).all())
+
+
+def test_unaligned_caches_and_queries(dev):
+    """Addresses that allow no 16-byte loads."""
+    hs = _hs()
+    x = PagedInputs([(40, 1), (100, 30)], heads=4, kv_heads=2, dim=64, dtype="f16", page=16, seed=8)
+    ref = x.plain()
+    tol, _ = x.tolerance(ref, True)
+
+    def shifted(a, by):
+        buf = torch.zeros(a.numel() + by, dtype=a.dtype, device=dev)
+        v = buf[by:].view(a.shape)
+        v.copy_(a)
+        return v
+
+    t = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    for bq, bk in ((1, 0), (0, 1), (3, 5)):
+        out = torch.zeros(x.q.shape, dtype=torch.float16, device=dev)
+        hs.paged_attention(shifted(x.q, bq), shifted(x.kc, bk), shifted(x.vc, bk), t(x.table),
+                           t(x.req), t(x.cu), t(x.seq), out, max_q_len=x.max_q, page_size=16)
+        assert bool(((out.cpu().double() - ref[0]).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
+def test_repeat_is_bitwise_and_streams(dev, lens):
+    """The same call gives the same bits; it runs on a given stream with its own workspace."""
+    hs = _hs()
+    x = PagedInputs(lens, heads=8, kv_heads=2, dim=128, dtype="bf16", seed=2)
+    a = x.call(hs, dev)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    b = x.call(hs, dev, stream=s)
+    c = x.call(hs, dev, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for u, v, w in zip(a, b, c):
+        assert torch.equal(u, v) and torch.equal(u, w)
+
+
+def test_batch_order_and_company(dev):
+    """A request's result is that of the request alone, up to the order of fp32 sums."""
+    hs = _hs()
+    x = PagedInputs(DECODE + CHUNKS, heads=8, kv_heads=2, dim=64, dtype="f16", seed=2)
+    x.check(hs, dev, True)
+
+
+def test_one_long_context(dev):
+    """One request, a long context: the keys are split over the whole GPU."""
+    for lens in ([(20000, 1)], [(9000, 40)]):
+        x = PagedInputs(lens, heads=4, kv_heads=1, dim=64, dtype="bf16", page=64, seed=6, sharp=1.0)
+        x.check(_hs(), dev, True)
+
+
+def test_many_short_requests(dev):
+    lens = [(i % 7, 1 + i % 3) for i in range(700)]
+    x = PagedInputs(lens, heads=2, kv_heads=1, dim=64, dtype="bf16", page=16, seed=6)
+    x.check(_hs(), dev, True)
+    lens = [(i % 7, 20 + i % 30) for i in range(150)]
+    x = PagedInputs(lens, heads=2, kv_heads=1, dim=64, dtype="bf16", page=16, seed=6)
+    x.check(_hs(), dev, True)
+
+
+def test_offsets_past_32_bits(dev):
+    """A cache of more than 2^32 bytes whose last pages are read."""
+    hs = _hs()
+    pages, ps, hk, d = 70000, 16, 8, 128  # 2.3 G elements, 4.6 GB each
+    lens = [(45, 1), (100, 30)]
+    x = PagedInputs(lens, heads=16, kv_heads=hk, dim=d, dtype="bf16", page=ps, seed=1)
+    ref = x.plain()
+    tol, _ = x.tolerance(ref, True)
+    n = x.kc.shape[0]
+    kc = torch.empty(pages, ps, hk, d, dtype=torch.bfloat16, device=dev)
+    vc = torch.empty_like(kc)
+    kc[pages - n:] = x.kc.to(dev)
+    vc[pages - n:] = x.vc.to(dev)
+    table = np.where(x.table >= 0, x.table + (pages - n), x.table).astype(np.int32)
+    t = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    for sel in ([0], [1]):  # the single token and the chunk
+        out = torch.zeros(x.q.shape, dtype=torch.bfloat16, device=dev)
+        a, e = int(x.cu[sel[0]]), int(x.cu[sel[0] + 1])
+        hs.paged_attention(x.q.to(dev)[a:e], kc, vc, t(table), t(x.req[sel]),
+                           torch.tensor([0, e - a], dtype=torch.int32, device=dev), t(x.seq[sel]),
+                           out[a:e], max_q_len=e - a, page_size=ps)
+        assert bool(((out.cpu().double() - ref[0]).abs() <= tol)[a:e].all())
+
+
+def test_captured_and_replayed(dev):
+    """Two captured calls with a workspace each; lengths and queries change between replays."""
+    hs = _hs()
+    for lens in (DECODE, CHUNKS):
+        x = PagedInputs(lens, heads=8, kv_heads=2, dim=128, dtype="bf16", seed=2)
+        t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+        q, kc, vc, table, req, cu, seq = (x.q.to(dev), x.kc.to(dev), x.vc.to(dev), t(x.table),
+                                          t(x.req), t(x.cu), t(x.seq))
+        outs = [torch.zeros_like(q) for _ in range(2)]
+        kw = dict(max_q_len=x.max_q, page_size=16)
+        n = hs.paged_attention_workspace_bytes(q, kc, vc, table, req, cu, seq, outs[0], **kw)
+        spaces = [torch.empty(n, dtype=torch.uint8, device=dev) for _ in outs]
+        call = lambda i: hs.paged_attention(q, kc, vc, table, req, cu, seq, outs[i],  # noqa: E731
+                                            workspace=spaces[i] if n else None, **kw)
+        call(0)
+        torch.cuda.synchronize()
+        graphs = []
+        for i in range(2):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[i]):
+                call(i)
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for step in range(3):
+            x.seq = np.maximum(x.seq - step, 0)
+            x.q = (x.q * (1 + step)).to(torch.bfloat16)
+            seq.copy_(t(x.seq))
+            q.copy_(x.q)
+            torch.cuda.synchronize()
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+            torch.cuda.synchronize()
+            ref = x.plain()
+            tol, _ = x.tolerance(ref, True)
+            assert torch.equal(outs[0], outs[1])
+            assert bool(((outs[0].cpu().double() - ref[0]).abs() <= tol)[ref[5]].all())
+
+
+def test_empty_calls(dev):
+    hs = _hs()
+    x = PagedInputs([(20, 0), (None, 0)], heads=4, kv_heads=2, dim=128, dtype="bf16", seed=3)
+    _, _, status = x.call(hs, dev)
+    assert status.tolist() == [0, 0]
+    q = torch.zeros(0, 4, 128, dtype=torch.bfloat16, device=dev)
+    kc = torch.zeros(0, 16, 2, 128, dtype=torch.bfloat16, device=dev)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    hs.paged_attention(q, kc, kc, torch.zeros(0, 0, dtype=torch.int32, device=dev), i32(), i32(0),
+                       i32(), q.clone(), max_q_len=0)
+    torch.cuda.synchronize()
