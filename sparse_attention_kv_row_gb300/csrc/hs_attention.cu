@@ -13,7 +13,7 @@
 
 #include <cstdint>
 
-#include "hs_attention.cuh"
+#include "hs_attention_split.cuh"
 
 namespace hs {
 namespace {
@@ -100,26 +100,8 @@ __global__ void __launch_bounds__(kGenThreads) attn_general_kernel(const AttnPar
   }
 }
 
-// One block per batch row: the row's own status, and whether a block that its
-// queries can see lies outside the pool.
-__device__ __forceinline__ void write_status(const AttnParams& p, int b) {
-  const AttnRow r = attn_row(p, b);
-  int bad = 0;
-  if (r.state >= 0 && r.hi > r.lo) {
-    const int32_t* bt = p.table + r.state * p.table_stride;
-    const int c1 = static_cast<int>(div_any(static_cast<uint32_t>(r.hi - 1), p.div_page));
-    for (int c = static_cast<int>(div_any(static_cast<uint32_t>(r.lo), p.div_page)) + threadIdx.x;
-         c <= c1; c += blockDim.x) {
-      const int32_t e = __ldg(bt + c);
-      bad |= e < 0 || e >= p.num_pages;
-    }
-  }
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) p.status[b] = r.status | (bad ? HS_ST_BAD_INDEX : 0);
-}
-
 __global__ void __launch_bounds__(kGenThreads) attn_status_kernel(const AttnParams p) {
-  write_status(p, blockIdx.x);
+  attn_write_status(p, blockIdx.x);
 }
 
 using GenFn = void (*)(const AttnParams);
@@ -163,6 +145,29 @@ hs_err check_args(const hs_paged_attention_args* a) {
       a->cache_stride_page < 1)
     return fail(HS_ERR_ARG, "%s: head strides must cover head_dim, cache strides be >= 1", who);
   return HS_OK;
+}
+
+// Which kernels a call takes, by sizes and types only (the workspace depends on it).
+enum class AttnForm { kGeneral, kSplit };
+AttnForm attn_form(const hs_paged_attention_args* a) {
+  const int64_t rows = static_cast<int64_t>(a->max_q_len) * (a->num_heads / a->num_kv_heads);
+  if (a->in_dtype == HS_DT_F32 || (a->head_dim != 64 && a->head_dim != 128) || rows == 0 ||
+      rows > kSplitRows || a->n_tokens == 0 ||
+      rows * a->num_kv_heads > INT32_MAX / 2 / a->batch)  // blocks of the join
+    return AttnForm::kGeneral;
+  return AttnForm::kSplit;
+}
+
+// Whether every address that the tensor-core kernels form allows 16-byte accesses.
+bool attn_aligned(const AttnParams& p) {
+  const uintptr_t all =
+      reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out) |
+      reinterpret_cast<uintptr_t>(p.cache[0]) | reinterpret_cast<uintptr_t>(p.cache[1]) |
+      static_cast<uintptr_t>(p.q_token) | static_cast<uintptr_t>(p.q_head) |
+      static_cast<uintptr_t>(p.out_token) | static_cast<uintptr_t>(p.out_head) |
+      static_cast<uintptr_t>(p.c_page) | static_cast<uintptr_t>(p.c_off) |
+      static_cast<uintptr_t>(p.c_head);
+  return all % 16 == 0;
 }
 
 AttnParams make_params(const hs_paged_attention_args* a) {
@@ -214,7 +219,10 @@ extern "C" int64_t hs_paged_attention_workspace_bytes(const hs_paged_attention_a
   clear_error();
   const hs_err err = check_args(a);
   if (err != HS_OK) return -static_cast<int64_t>(err);
-  return 0;
+  if (a->batch == 0 || attn_form(a) == AttnForm::kGeneral) return 0;
+  DeviceInfo dev;
+  if (current_device(&dev) != HS_OK) return -static_cast<int64_t>(HS_ERR_CUDA);
+  return split_workspace(a->in_dtype, a->cache_dtype == HS_DT_E4M3, a->head_dim, dev);
 }
 
 extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream_t stream) {
@@ -247,6 +255,8 @@ extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream
   const AttnParams p = make_params(a);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = a->cache_dtype == HS_DT_E4M3;
+  if (attn_form(a) == AttnForm::kSplit && attn_aligned(p))
+    return split_launch(p, a->in_dtype, fp8, a->workspace, dev, st);
   if (a->n_tokens > 0 && a->max_q_len > 0) {
     const GenFn fn = a->in_dtype == HS_DT_F32
                          ? general_fn<HS_DT_F32>(fp8, p.dim)
