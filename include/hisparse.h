@@ -573,7 +573,8 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  *  req_state   int32/int64 [batch] (flags & HS_REQ_STATE_I64), negative = padding
  *  cu_q        int32 [batch + 1], increasing; seq_lens int32/int64 [batch]
  *              (flags & HS_SEQ_LENS_I64)
- *  k_scale, v_scale  device fp32 [1] or NULL (HS_DT_E4M3 only)
+ *  scale       positive; k_scale, v_scale  device fp32 [1] or NULL (HS_DT_E4M3
+ *              only), positive too
  *  max_q_len   a bound on every request's n (host value; it sizes the launch)
  *  status      int32 [batch] or NULL, overwritten
  *  workspace   device memory, 256-byte aligned, of at least

@@ -131,8 +131,8 @@ hs_err check_args(const hs_paged_attention_args* a) {
                             ">= 0, block_table_stride >= table_blocks", who);
   if (a->num_heads % a->num_kv_heads != 0)
     return fail(HS_ERR_ARG, "%s: num_heads must be a multiple of num_kv_heads", who);
-  if (!(a->scale > -INFINITY && a->scale < INFINITY))
-    return fail(HS_ERR_ARG, "%s: scale must be finite", who);
+  if (!(a->scale > 0.f && a->scale < INFINITY))
+    return fail(HS_ERR_ARG, "%s: scale must be positive and finite", who);
   if (a->head_dim > kGenMaxDim || a->batch > kAttnMaxBatch || a->n_tokens > INT32_MAX ||
       static_cast<int64_t>(a->max_q_len) * a->num_heads > INT32_MAX)
     return fail(HS_ERR_UNSUPPORTED, "%s: head_dim <= %d, batch <= %d, n_tokens and max_q_len * "
@@ -148,14 +148,13 @@ hs_err check_args(const hs_paged_attention_args* a) {
 }
 
 // Which kernels a call takes, by sizes and types only (the workspace depends on it).
-enum class AttnForm { kGeneral, kSplit };
+enum class AttnForm { kGeneral, kSplit, kTiles };
 AttnForm attn_form(const hs_paged_attention_args* a) {
   const int64_t rows = static_cast<int64_t>(a->max_q_len) * (a->num_heads / a->num_kv_heads);
   if (a->in_dtype == HS_DT_F32 || (a->head_dim != 64 && a->head_dim != 128) || rows == 0 ||
-      rows > kSplitRows || a->n_tokens == 0 ||
-      rows * a->num_kv_heads > INT32_MAX / 2 / a->batch)  // blocks of the join
+      a->n_tokens == 0 || rows * a->num_kv_heads > INT32_MAX / 2 / a->batch)  // blocks of the join
     return AttnForm::kGeneral;
-  return AttnForm::kSplit;
+  return rows <= kSplitRows ? AttnForm::kSplit : AttnForm::kTiles;
 }
 
 // Whether every address that the tensor-core kernels form allows 16-byte accesses.
@@ -219,9 +218,11 @@ extern "C" int64_t hs_paged_attention_workspace_bytes(const hs_paged_attention_a
   clear_error();
   const hs_err err = check_args(a);
   if (err != HS_OK) return -static_cast<int64_t>(err);
-  if (a->batch == 0 || attn_form(a) == AttnForm::kGeneral) return 0;
+  const AttnForm form = a->batch == 0 ? AttnForm::kGeneral : attn_form(a);
+  if (form == AttnForm::kGeneral) return 0;
   DeviceInfo dev;
   if (current_device(&dev) != HS_OK) return -static_cast<int64_t>(HS_ERR_CUDA);
+  if (form == AttnForm::kTiles) return tiles_workspace(a->head_dim, dev);
   return split_workspace(a->in_dtype, a->cache_dtype == HS_DT_E4M3, a->head_dim, dev);
 }
 
@@ -255,8 +256,9 @@ extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream
   const AttnParams p = make_params(a);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = a->cache_dtype == HS_DT_E4M3;
-  if (attn_form(a) == AttnForm::kSplit && attn_aligned(p))
-    return split_launch(p, a->in_dtype, fp8, a->workspace, dev, st);
+  const AttnForm form = attn_aligned(p) ? attn_form(a) : AttnForm::kGeneral;
+  if (form == AttnForm::kSplit) return split_launch(p, a->in_dtype, fp8, a->workspace, dev, st);
+  if (form == AttnForm::kTiles) return tiles_launch(p, a->in_dtype, fp8, a->workspace, dev, st);
   if (a->n_tokens > 0 && a->max_q_len > 0) {
     const GenFn fn = a->in_dtype == HS_DT_F32
                          ? general_fn<HS_DT_F32>(fp8, p.dim)

@@ -150,7 +150,9 @@ __global__ void __launch_bounds__(SplitShape<kIn, kFp8, D>::kWarps * kWarp, 1)
   extern __shared__ __align__(128) unsigned char smem[];
   uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + S::kRing);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t total = attn_prefix(p, prefix, kTile);
+  const uint32_t total = attn_prefix(p, prefix, [&](const AttnRow& r) {
+    return static_cast<uint32_t>(attn_tiles(r, kTile)) * p.kv_heads;
+  });
   grid_dep_launch_dependents();
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= p.batch; b += blockDim.x) ws.prefix[b] = prefix[b];

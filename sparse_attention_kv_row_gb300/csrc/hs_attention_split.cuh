@@ -33,9 +33,10 @@ __device__ __forceinline__ int attn_tiles(const AttnRow& r, int size) {
   return n > 1 ? n : 1;
 }
 
-// Fills prefix[0 .. batch] (shared memory) with the running tile counts of
-// every kv head of every row and returns the total.  All threads of the block call it.
-__device__ __forceinline__ uint32_t attn_prefix(const AttnParams& p, uint32_t* prefix, int size) {
+// Fills prefix[0 .. batch] (shared memory) with the running sum of cost(row)
+// over the rows that have work, and returns the total.  All threads of the block call it.
+template <typename Cost>
+__device__ __forceinline__ uint32_t attn_prefix(const AttnParams& p, uint32_t* prefix, Cost cost) {
   __shared__ uint32_t warp_sum[kWarp];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   uint32_t run = 0;
@@ -44,7 +45,7 @@ __device__ __forceinline__ uint32_t attn_prefix(const AttnParams& p, uint32_t* p
     uint32_t n = 0;
     if (b < p.batch) {
       const AttnRow r = attn_row(p, b);
-      if (r.state >= 0) n = static_cast<uint32_t>(attn_tiles(r, size)) * p.kv_heads;
+      if (r.state >= 0) n = cost(r);
     }
     uint32_t x = n;
 #pragma unroll
@@ -81,10 +82,17 @@ __device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t two) {
   return r;
 }
 
-// Turns row half h of a 16-row fragment of bf16 queries into fp16, times a
-// power of two that brings the row's largest magnitude to [2^8, 2^9): exact but
-// for elements below 2^-22 of it.  Returns the factor to undo it.  The four
-// lanes of a row group call it together.
+// The power of two that brings a row of bf16 queries to fp16, where `top` is
+// the bits of its largest magnitude: to [2^8, 2^9), which keeps everything above
+// 2^-22 of it exact (2^62 at most: what is still small then scores nothing).  An
+// infinity or NaN passes through any factor.
+__device__ __forceinline__ float f16_factor(uint32_t top) {
+  const int e = static_cast<int>(top >> 7);  // biased exponent
+  return __uint_as_float(static_cast<uint32_t>(262 - min(max(e, 73), 254)) << 23);
+}
+
+// Turns row half h of a 16-row fragment of bf16 queries into fp16 by that
+// factor and returns what undoes it.  The four lanes of a row group call it together.
 template <int kSteps>
 __device__ __forceinline__ float rows_to_f16(uint32_t (&q)[kSteps][4], int h) {
   uint32_t top = 0;  // largest magnitude: bf16 bits order like whole numbers
@@ -98,11 +106,7 @@ __device__ __forceinline__ float rows_to_f16(uint32_t (&q)[kSteps][4], int h) {
   }
   top = max(top, __shfl_xor_sync(kFullMask, top, 1));
   top = max(top, __shfl_xor_sync(kFullMask, top, 2));
-  const int e = static_cast<int>(top >> 7);  // biased exponent; 255: infinite or NaN
-  // Exponents from the smallest normal number up; an infinity or NaN in the row
-  // passes through any factor.
-  const int shift = 127 + 8 - min(max(e, 9), 254);
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + max(min(shift, 127), -126)) << 23);
+  const float up = f16_factor(top);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
@@ -119,7 +123,7 @@ __device__ __forceinline__ float rows_to_f16(uint32_t (&q)[kSteps][4], int h) {
 
 // One block: batch row b's own status, and whether a block that its queries can
 // see lies outside the pool.
-__device__ __forceinline__ void attn_write_status(const AttnParams& p, int b) {
+__device__ __forceinline__ void attn_write_status(const AttnParams& p, int b, int also = 0) {
   const AttnRow r = attn_row(p, b);
   int bad = 0;
   if (r.state >= 0 && r.hi > r.lo) {
@@ -132,12 +136,16 @@ __device__ __forceinline__ void attn_write_status(const AttnParams& p, int b) {
     }
   }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) p.status[b] = r.status | (bad ? HS_ST_BAD_INDEX : 0);
+  if (threadIdx.x == 0) p.status[b] = r.status | (bad ? HS_ST_BAD_INDEX : 0) | also;
 }
 
 // hs_attention_split.cu: few queries per request.
 int64_t split_workspace(int in_dtype, bool fp8, int dim, const DeviceInfo& dev);
 hs_err split_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace,
+                    const DeviceInfo& dev, cudaStream_t stream);
+// hs_attention_tiles.cu: chunks of many queries.
+int64_t tiles_workspace(int dim, const DeviceInfo& dev);
+hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace,
                     const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace hs

@@ -1,0 +1,904 @@
+// hs_attention_tiles.cu -- paged attention for chunks of many queries per
+// request (prompts, chunked prefill, mixed batches), for sm_103a.
+//
+// A unit is 256 query rows (new tokens x query heads of one kv head) of one
+// request against the keys they see, in tiles of 128 keys:
+//   S = Q K^T (128 x 128 x D),  P = 2^(S c - m),  O += P V (128 x D x 128),
+// twice, once for each half of the rows.  4 D operations per (row, key) make
+// the tensor cores the bound; the softmax of one half runs while the tensor
+// cores work on the other.  S, P and O stay in tensor memory: S0 S1 (128 columns
+// each, P over its S) and O0 O1 fill it.  Roles: two warpgroups of softmax (a
+// thread per row), one that loads, one warp that issues the MMAs.
+//
+// The running maximum m is only raised, and O rescaled, when a row's new
+// maximum is more than 2^8 above the old one: a larger weight is as good in the
+// products' type, and sums stay in fp32.
+//
+// The flattened list of tiles of all units, each with one more for its fixed
+// cost, is cut into equal runs, one per SM.  A unit that a run covers alone is
+// written at once; the others leave their parts in the workspace, and a second
+// kernel joins them.
+//
+// K and V tiles come by tensor-map loads, a box per page, where pages are a
+// power-of-two part or a multiple of 128 keys and the cache is 16-bit.  An FP8
+// cache is widened to fp16 on the way through registers, exactly; so are other
+// page sizes, and a V tile that holds positions no query sees, whose rows must
+// be zeros because 0 times what they hold may not be 0.
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "hs_attention_split.cuh"
+#include "hs_tcgen05.cuh"
+
+namespace hs {
+namespace {
+
+constexpr int kKeys = 128;         // keys per tile
+constexpr int kHalf = 128;         // rows per MMA
+constexpr int kUnitRows = 2 * kHalf;
+constexpr int kThreads = 512;
+constexpr int kLoaders = 128;
+constexpr uint32_t kSoftmaxRegs = 176, kLoaderRegs = 112, kMmaRegs = 48;
+static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 512, "65536 registers per SM");
+constexpr float kRaise = 8.f;      // log2 of how far weights may exceed 1
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+struct TilesSpace {
+  int4* joins;       // [workers]: the split unit that a worker's boundary is the first to cut
+  int32_t* failed;   // [workers]: a bounded wait gave up
+  float* slots;      // two per worker: o [256][D], then log2-sum-exp [256]
+  uint32_t workers;
+};
+__host__ __device__ constexpr int tiles_slot_floats(int dim) { return kUnitRows * (dim + 1); }
+
+template <int kIn, bool kFp8, int D>
+struct TilesShape {
+  static constexpr int kPanels = D / 64;                 // 128-byte-wide panels of a tile
+  static constexpr int kPanel = kKeys * 128;             // bytes
+  static constexpr int kStage = kPanels * kPanel;        // one K or V tile, 16-bit
+  static constexpr int kQ = 2 * kStage;                  // both halves
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kRing = kQ + kStages * kStage;
+  static constexpr int kRowBytes = kFp8 ? D : 2 * D;     // a cache row
+  static constexpr int kRowChunks = kRowBytes / 16;
+  // A piece is what the loaders hold in registers at once: up to 8 chunks each.
+  static constexpr int kPieceChunks = kKeys * kRowChunks / kLoaders > 8 ? 8 : kKeys * kRowChunks / kLoaders;
+  static constexpr int kPieces = kKeys * kRowChunks / kLoaders / kPieceChunks;
+};
+
+// A unit of one batch row: its rows and tiles.
+struct Unit {
+  int first, rows;    // first row, rows of it (<= 256)
+  int tile, tiles;    // first tile, number (at least 1)
+};
+__device__ __forceinline__ Unit unit_of(const AttnParams& p, const AttnRow& r, int rt, FastDiv by_group) {
+  Unit u;
+  u.first = rt * kUnitRows;
+  u.rows = min(kUnitRows, r.n * p.group - u.first);
+  const int i0 = div_any(u.first, by_group), i1 = div_any(u.first + u.rows - 1, by_group);
+  const int hi = max(0, r.len - r.n + i1 + 1), lo = seen_lo(p, r.len - r.n + i0);
+  u.tile = lo / kKeys;
+  u.tiles = max(1, (hi + kKeys - 1) / kKeys - u.tile);
+  return u;
+}
+__device__ __forceinline__ int units_of(const AttnParams& p, const AttnRow& r) {
+  return (r.n * p.group + kUnitRows - 1) / kUnitRows;
+}
+__device__ __forceinline__ uint32_t row_cost(const AttnParams& p, const AttnRow& r, FastDiv by_group) {
+  uint32_t n = 0;
+  const int units = units_of(p, r);
+  for (int rt = 0; rt < units; ++rt) n += unit_of(p, r, rt, by_group).tiles + 1;
+  return n * p.kv_heads;
+}
+
+// Walks the units of a worker's run; all roles walk the same way.
+struct Walk {
+  uint32_t c1;        // end of the run
+  uint32_t u0;        // cost index of the current unit
+  int b, rt, g;
+  AttnRow row;
+  Unit unit;
+  int k0, k1;         // this run's tiles of the unit (relative)
+
+  __device__ __forceinline__ void clip(uint32_t c0) {
+    const int64_t a = static_cast<int64_t>(c0) - u0 - 1, e = static_cast<int64_t>(c1) - u0 - 1;
+    k0 = a > 0 ? static_cast<int>(a) : 0;
+    k1 = e < unit.tiles ? static_cast<int>(e) : unit.tiles;
+  }
+  __device__ __forceinline__ bool seek(uint32_t c0, uint32_t end, const uint32_t* prefix,
+                                       const AttnParams& p, FastDiv by_group) {
+    c1 = end;
+    if (c0 >= c1) return false;
+    int a = 0, n = p.batch;  // the largest b with prefix[b] <= c0
+    while (n - a > 1) {
+      const int mid = (a + n) >> 1;
+      if (prefix[mid] <= c0)
+        a = mid;
+      else
+        n = mid;
+    }
+    b = a;
+    row = attn_row(p, b);
+    u0 = prefix[b];
+    rt = 0;
+    for (;;) {
+      unit = unit_of(p, row, rt, by_group);
+      const uint32_t all = static_cast<uint32_t>(unit.tiles + 1) * p.kv_heads;
+      if (c0 - u0 < all) break;
+      u0 += all;
+      ++rt;
+    }
+    g = (c0 - u0) / (unit.tiles + 1);
+    u0 += static_cast<uint32_t>(g) * (unit.tiles + 1);
+    clip(c0);
+    return k1 > k0 || next(prefix, p, by_group);
+  }
+  // The next unit with tiles in the run.
+  __device__ __forceinline__ bool next(const uint32_t* prefix, const AttnParams& p, FastDiv by_group) {
+    u0 += unit.tiles + 1;
+    if (u0 + 1 >= c1) return false;
+    if (++g == p.kv_heads) {
+      g = 0;
+      if (++rt == units_of(p, row)) {
+        rt = 0;
+        do ++b;
+        while (prefix[b + 1] == prefix[b]);
+        row = attn_row(p, b);
+      }
+      unit = unit_of(p, row, rt, by_group);
+    }
+    clip(u0);
+    return true;
+  }
+};
+
+struct Shared {
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+  uint64_t kv_full[6], kv_empty[6];
+  uint32_t tmem;
+  volatile int dead;
+  float q_factor[2][kUnitRows];
+  int64_t offs[2][kKeys];
+};
+
+// Waits for phase `parity`, unless the block has given up; gives up itself
+// after kWaitNs.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((n & 15) == 15) {
+      if (*dead) return false;
+      const uint64_t now = global_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitNs) {
+        *dead = 1;
+        return false;
+      }
+    }
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2t(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16-byte chunk c (of 64 elements' eight) of row r of a panel.
+__device__ __forceinline__ uint32_t in_panel(int r, int c) {
+  return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same, and whether `ok` holds for every loader: they give up together.
+__device__ __forceinline__ bool loaders_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+
+// ------------------------------------------------------------------ the loading warpgroup
+template <int kIn, bool kFp8, int D>
+struct Loader {
+  using S = TilesShape<kIn, kFp8, D>;
+  const AttnParams& p;
+  Shared& sh;
+  uint32_t q_at, ring;
+  int tid;
+
+  // Chunks of piece k of the K or V tile whose row offsets are offs[buf].
+  __device__ __forceinline__ void fetch(uint4 (&r)[S::kPieceChunks], int buf, int piece, bool v,
+                                        int64_t head) {
+#pragma unroll
+    for (int i = 0; i < S::kPieceChunks; ++i) {
+      const int c = (piece * S::kPieceChunks + i) * kLoaders + tid;
+      const int64_t off = sh.offs[buf][c / S::kRowChunks];
+      r[i] = make_uint4(0, 0, 0, 0);
+      if (off >= 0)
+        r[i] = ld_stream_v4((v ? p.cache[1] : p.cache[0]) + off + head + (c % S::kRowChunks) * 16);
+    }
+  }
+  __device__ __forceinline__ void store(const uint4 (&r)[S::kPieceChunks], int stage, int piece) {
+    const uint32_t at = ring + stage * S::kStage;
+#pragma unroll
+    for (int i = 0; i < S::kPieceChunks; ++i) {
+      const int c = (piece * S::kPieceChunks + i) * kLoaders + tid;
+      const int row = c / S::kRowChunks, ch = c % S::kRowChunks;
+      if constexpr (kFp8) {
+        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[2 * j] = e4m3_to_f16(w[j] & 0xFFFF);
+          h[2 * j + 1] = e4m3_to_f16(w[j] >> 16);
+        }
+        const uint32_t panel = at + (ch / 4) * S::kPanel;
+        st_shared_v4(panel + in_panel(row, (ch % 4) * 2), make_uint4(h[0], h[1], h[2], h[3]));
+        st_shared_v4(panel + in_panel(row, (ch % 4) * 2 + 1), make_uint4(h[4], h[5], h[6], h[7]));
+      } else {
+        st_shared_v4(at + (ch / 8) * S::kPanel + in_panel(row, ch % 8), r[i]);
+      }
+    }
+  }
+  // Row offsets of one tile, a loader per key; -1 for keys that no query of the
+  // request sees and for blocks outside the pool.
+  __device__ __forceinline__ void look_up(const AttnRow& row, int tile, int buf) {
+    const int j = tile * kKeys + tid;
+    sh.offs[buf][tid] = j >= row.lo && j < row.hi
+                            ? key_offset(p, p.table + row.state * p.table_stride, j)
+                            : -1;
+    loaders_sync();
+  }
+  __device__ __forceinline__ void load_q(const Walk& w, FastDiv by_group, int buf) {
+    const int halves = w.unit.rows > kHalf ? 2 : 1;
+    if constexpr (kFp8 && kIn == HS_DT_BF16) {
+      // A thread per row: a power of two brings its largest magnitude to
+      // [2^8, 2^9) and the row to fp16 (see rows_to_f16).
+      for (int m = tid; m < halves * kHalf; m += kLoaders) {
+        const uint32_t at = q_at + (m / kHalf) * S::kStage;
+        const int r = m % kHalf;
+        const bool live = m < w.unit.rows;
+        const int i = div_any(w.unit.first + m, by_group), hg = w.unit.first + m - i * p.group;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + static_cast<int64_t>(w.row.q0 + i) * p.q_token +
+            static_cast<int64_t>(w.g * p.group + hg) * p.q_head);
+        uint32_t top = 0;
+        if (live) {
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = __ldg(src + c);
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
+          }
+        }
+        const float up = f16_factor(top);
+        sh.q_factor[buf][m] = 1.0f / up;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) x = __ldg(src + c);
+          uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = pack2t<false>(__uint_as_float(v[j] << 16) * up,
+                                 __uint_as_float(v[j] & 0xFFFF0000u) * up);
+          st_shared_v4(at + (c / 8) * S::kPanel + in_panel(r, c % 8), make_uint4(v[0], v[1], v[2], v[3]));
+        }
+      }
+    } else {
+      constexpr int kC = D / 8, kBatch = 8;
+      for (int c0 = 0; c0 < halves * kHalf * kC; c0 += kBatch * kLoaders) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int c = c0 + i * kLoaders + tid, m = c / kC;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (m < w.unit.rows) {
+            const int tok = div_any(w.unit.first + m, by_group), hg = w.unit.first + m - tok * p.group;
+            x[i] = __ldg(reinterpret_cast<const uint4*>(
+                             p.q + static_cast<int64_t>(w.row.q0 + tok) * p.q_token +
+                             static_cast<int64_t>(w.g * p.group + hg) * p.q_head) + c % kC);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int c = c0 + i * kLoaders + tid, m = c / kC, ch = c % kC;
+          st_shared_v4(q_at + (m / kHalf) * S::kStage + (ch / 8) * S::kPanel + in_panel(m % kHalf, ch % 8),
+                       x[i]);
+        }
+      }
+    }
+  }
+};
+
+template <int kIn, bool kFp8, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tiles_kernel(const AttnParams p, const TilesSpace ws, const FastDiv by_group,
+                      const __grid_constant__ CUtensorMap k_map,
+                      const __grid_constant__ CUtensorMap v_map, const int box_keys) {
+  using S = TilesShape<kIn, kFp8, D>;
+  constexpr bool kBf16 = kIn == HS_DT_BF16 && !kFp8;  // type of the products
+  // fp16 weights reach 2^(6 + 8) and keep what is 2^-30 of the reference.
+  constexpr float kBias = kBf16 ? 0.f : 6.f;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + S::kRing);
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t q_at = smem_addr(smem), ring = q_at + S::kQ;
+
+  if (tid == 0) {
+    mbar_init(&sh.q_full, kLoaders);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], kHalf);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sh.kv_full[i], kLoaders);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    fence_mbar_init();
+    sh.dead = 0;
+  }
+  if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  const uint32_t total = attn_prefix(p, prefix, [&](const AttnRow& r) { return row_cost(p, r, by_group); });
+  grid_dep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t workers = min(ws.workers, total);
+  const uint32_t me = blockIdx.x;
+  const uint32_t c0 = me < workers ? split_begin(me, total, workers) : 0;
+  const uint32_t c1 = me < workers ? split_begin(me + 1, total, workers) : 0;
+  volatile int* dead = &sh.dead;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    regs_grow<kSoftmaxRegs>();
+    const int half = warp >> 2, r = tid & (kHalf - 1);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + half * kKeys, o_at = tmem + lanes + 256 + half * D;
+    const float ks = p.scale[0] ? __ldg(p.scale[0]) : 1.0f, vs = p.scale[1] ? __ldg(p.scale[1]) : 1.0f;
+    uint32_t s_ph = 0, o_ph = 0, u_n = 0;
+    Walk w;
+    bool more = w.seek(c0, c1, prefix, p, by_group);
+    for (; more; more = w.next(prefix, p, by_group), ++u_n) {
+      const int m = half * kHalf + r;  // row of the unit
+      if (half == 1 && w.unit.rows <= kHalf) continue;
+      const bool live = m < w.unit.rows;
+      const int i = div_any(w.unit.first + m, by_group);
+      const int pos = w.row.len - w.row.n + i;
+      // Rows past the unit's end are computed like the others and not written.
+      const int vis_hi = live ? pos + 1 : INT_MAX, vis_lo = live ? seen_lo(p, pos) : 0;
+      // Keys that every row of this warp's half sees need no mask.
+      const int i_first = div_any(w.unit.first + half * kHalf, by_group);
+      const int i_last = div_any(w.unit.first + min(w.unit.rows, (half + 1) * kHalf) - 1, by_group);
+      const int all_hi = w.row.len - w.row.n + i_first + 1;
+      const int all_lo = seen_lo(p, w.row.len - w.row.n + i_last);
+      float sc = p.softmax_scale * kLog2e * ks;
+      float top = -INFINITY, ref = -kBias, l = 0.f;  // ref: what scores are taken relative to
+      bool ok = true;
+      for (int k = w.k0; k < w.k1; ++k) {
+        ok = __all_sync(kFullMask, wait_for(&sh.s_full[half], s_ph, dead));
+        if (!ok) break;
+        s_ph ^= 1;
+        tc_fence_after();
+        if constexpr (kFp8 && kIn == HS_DT_BF16)
+          if (k == w.k0) sc *= sh.q_factor[u_n & 1][m];  // there before the product was issued
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s[q], s_at + q * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_pin(s[q]);
+        const int j0 = (w.unit.tile + k) * kKeys;
+        if (j0 + kKeys > all_hi || j0 < all_lo) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int j = j0 + q * 32 + c;
+              if (j >= vis_hi || j < vis_lo) s[q][c] = 0xFF800000u;  // -inf
+            }
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int c = 1; c < 32; ++c) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][c]));
+        }
+        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool raise = mine > top + kRaise;
+        if (__any_sync(kFullMask, raise)) {
+          const float back = raise ? fast_exp2(top - mine) : 1.f;
+          if (raise) {
+            top = mine;
+            ref = mine - kBias;
+            l *= back;
+          }
+          if (k > w.k0) {
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(o, o_at + q * 32);
+              tmem_wait_ld();
+              tmem_pin(o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * back);
+              tmem_st32(o_at + q * 32, o);
+            }
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w32[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint32_t* x = s[2 * h + (c >> 4)] + (c & 15) * 2;
+            const float a = fast_exp2(fmaf(__uint_as_float(x[0]), sc, -ref));
+            const float b = fast_exp2(fmaf(__uint_as_float(x[1]), sc, -ref));
+            sum[c & 3] += a + b;
+            w32[c] = pack2t<kBf16>(a, b);  // half a step off each
+          }
+          tmem_st32(s_at + h * 32, w32);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.p_full[half]);
+      }
+      if (!ok) break;
+      if (!__all_sync(kFullMask, wait_for(&sh.o_full[half], o_ph, dead))) break;
+      o_ph ^= 1;
+      tc_fence_after();
+      const bool whole = w.k0 == 0 && w.k1 == w.unit.tiles;
+      const bool none = top == -INFINITY;
+      const float inv = none ? 0.f : 1.0f / l;
+      const float lse = none ? -INFINITY : ref + log2f(l);
+      const int head = w.g * p.group + (w.unit.first + m - i * p.group);
+      const int64_t tok = w.row.q0 + i;
+      unsigned char* dst = p.out + tok * p.out_token + head * p.out_head;
+      float* part = ws.slots + static_cast<int64_t>(2 * me + (w.k0 == 0 ? 1 : 0)) * tiles_slot_floats(D);
+      const float f = whole ? inv * vs : inv;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(o, o_at + q * 32);
+        tmem_wait_ld();
+        tmem_pin(o);
+        if (live && whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[c * 8 + e * 2]) * f,
+                                               __uint_as_float(o[c * 8 + e * 2 + 1]) * f);
+            *reinterpret_cast<uint4*>(dst + q * 64 + c * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        } else if (live) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(part + m * D + q * 32 + c * 4) =
+                make_float4(__uint_as_float(o[c * 4]) * f, __uint_as_float(o[c * 4 + 1]) * f,
+                            __uint_as_float(o[c * 4 + 2]) * f, __uint_as_float(o[c * 4 + 3]) * f);
+        }
+      }
+      if (live && !whole) part[kUnitRows * D + m] = lse;
+      if (live && whole && p.lse) p.lse[tok * p.heads + head] = lse * kLn2;
+      tc_fence_before();  // O is read before the next unit's first product, which waits for P
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- loads
+    regs_shrink<kLoaderRegs>();
+    Loader<kIn, kFp8, D> ld{p, sh, q_at, ring, tid - 256};
+    const int lt = tid - 256;
+    uint32_t at = 0, u_n = 0;  // K and V tiles so far; units so far
+    auto claim = [&]() {
+      return loaders_all(wait_for(&sh.kv_empty[at % S::kStages], ((at / S::kStages) & 1) ^ 1, dead));
+    };
+    auto publish = [&]() {
+      fence_proxy_async_smem();  // the MMA reads through the async proxy
+      mbar_arrive(&sh.kv_full[at % S::kStages]);
+      ++at;
+    };
+    bool ok = true;
+    Walk w;
+    bool more = w.seek(c0, c1, prefix, p, by_group);
+    for (; more && ok; more = w.next(prefix, p, by_group), ++u_n) {
+      ok = loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead));
+      if (!ok) break;
+      ld.load_q(w, by_group, u_n & 1);
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.q_full);
+      const int64_t head = w.g * p.c_head;
+      if (!kFp8 && box_keys > 0) {
+        for (int k = w.k0; k < w.k1 && ok; ++k) {
+          const int j0 = (w.unit.tile + k) * kKeys;
+          const bool edge = j0 < w.row.lo || j0 + kKeys > w.row.hi;
+#pragma unroll 1
+          for (int v = 0; v < 2 && ok; ++v) {
+            ok = claim();
+            if (!ok) break;
+            if (v == 1 && edge) {
+              ld.look_up(w.row, w.unit.tile + k, 0);
+#pragma unroll 1
+              for (int x = 0; x < S::kPieces; ++x) {
+                uint4 r[S::kPieceChunks];
+                ld.fetch(r, 0, x, true, head);
+                ld.store(r, at % S::kStages, x);
+              }
+              loaders_sync();  // offs is written again
+              publish();
+              continue;
+            }
+            uint64_t* bar = &sh.kv_full[at % S::kStages];
+            const uint32_t dst = ring + (at % S::kStages) * S::kStage;
+            if (lt == 0)
+              mbar_arrive_expect_tx(bar, S::kStage);
+            else
+              mbar_arrive(bar);
+            if (lt < kKeys / box_keys) {
+              const int j = j0 + lt * box_keys;
+              // A box that no query sees, or outside the pool, is past the last
+              // page: it reads zeros.
+              int page = static_cast<int>(p.num_pages), in_page = 0;
+              if (j + box_keys > w.row.lo && j < w.row.hi) {
+                const uint32_t c = div_any(static_cast<uint32_t>(j), p.div_page);
+                const int32_t e = __ldg(p.table + w.row.state * p.table_stride + c);
+                if (e >= 0 && e < p.num_pages) {
+                  page = e;
+                  in_page = j - static_cast<int>(c * p.page_size);
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < S::kPanels; ++x)
+                tensor_load_4d(dst + x * S::kPanel + lt * box_keys * 128, v ? &v_map : &k_map, x * 64,
+                               w.g, in_page, page, bar);
+            }
+            ++at;
+          }
+        }
+      } else {
+        // Pieces through registers, two in flight: K and V of each tile in turn.
+        constexpr int kPer = 2 * S::kPieces;
+        const int pieces = (w.k1 - w.k0) * kPer;
+        uint4 ra[S::kPieceChunks], rb[S::kPieceChunks];
+        auto fetch = [&](uint4 (&r)[S::kPieceChunks], int x) {
+          const int k = w.k0 + x / kPer, in = x % kPer;
+          if (in == 0) ld.look_up(w.row, w.unit.tile + k, k & 1);
+          ld.fetch(r, k & 1, in % S::kPieces, in >= S::kPieces, head);
+        };
+        auto put = [&](const uint4 (&r)[S::kPieceChunks], int x) {
+          const int in = x % S::kPieces;
+          if (in == 0) ok = claim();
+          if (!ok) return;
+          ld.store(r, at % S::kStages, in);
+          if (in == S::kPieces - 1) publish();
+        };
+        fetch(ra, 0);
+#pragma unroll 1
+        for (int x = 0; x < pieces; x += 2) {
+          fetch(rb, x + 1);  // an even number of pieces
+          put(ra, x);
+          if (!ok) break;
+          if (x + 2 < pieces) fetch(ra, x + 2);
+          put(rb, x + 1);
+          if (!ok) break;
+        }
+      }
+    }
+    if (!ok) {
+      // The tensor-map loads still on their way write shared memory: see them in.
+      volatile int no = 0;
+      for (uint32_t n = at > S::kStages ? at - S::kStages : 0; n < at; ++n)
+        wait_for(&sh.kv_full[n % S::kStages], (n / S::kStages) & 1, &no);
+    }
+  } else {
+    // ---------------------------------------------------------------- MMA
+    regs_shrink<kMmaRegs>();
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t kQk = mma_shape(kBf16, kHalf, kKeys, false);
+      constexpr uint32_t kPv = mma_shape(kBf16, kHalf, D, true);
+      uint32_t at = 0, u_n = 0, p_ph[2] = {0, 0};
+      auto qk = [&](int half, uint32_t stage) {
+        const uint32_t a = q_at + half * S::kStage, b = ring + stage * S::kStage;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t o = (x / 4) * S::kPanel + (x % 4) * 32;
+          mma_smem(tmem + half * kKeys, mma_desc(a + o, 16, 1024), mma_desc(b + o, 16, 1024), kQk, x > 0);
+        }
+      };
+      auto pv = [&](int half, uint32_t stage, bool add) {
+        const uint32_t b = ring + stage * S::kStage;
+#pragma unroll
+        for (int x = 0; x < kKeys / 16; ++x)
+          mma_tmem(tmem + 256 + half * D, tmem + half * kKeys + x * 8,
+                   mma_desc(b + x * 2048, S::kPanel, 1024), kPv, add || x > 0);
+      };
+      auto arrived = [&](uint32_t n) {
+        const bool ok = wait_for(&sh.kv_full[n % S::kStages], (n / S::kStages) & 1, dead);
+        tc_fence_after();
+        return ok;
+      };
+      bool ok = true;
+      Walk w;
+      bool more = w.seek(c0, c1, prefix, p, by_group);
+      for (; more && ok; more = w.next(prefix, p, by_group), ++u_n) {
+        const int halves = w.unit.rows > kHalf ? 2 : 1;
+        const int n = w.k1 - w.k0;
+        // K of tile k is stage at + 2 k, V the one after it.
+        ok = wait_for(&sh.q_full, u_n & 1, dead) && arrived(at);
+        if (!ok) break;
+        for (int h = 0; h < halves; ++h) {
+          qk(h, at % S::kStages);
+          mma_commit(&sh.s_full[h]);
+        }
+        mma_commit(&sh.kv_empty[at % S::kStages]);
+        if (n == 1) mma_commit(&sh.q_empty);
+        for (int k = 0; k < n && ok; ++k) {
+          const uint32_t v = at + 2 * k + 1, next_k = at + 2 * k + 2;
+          for (int h = 0; h < halves && ok; ++h) {
+            if (h == 0) ok = arrived(v);
+            ok = ok && wait_for(&sh.p_full[h], p_ph[h], dead);
+            if (!ok) break;
+            p_ph[h] ^= 1;
+            tc_fence_after();
+            pv(h, v % S::kStages, k > 0);
+            if (h == halves - 1) mma_commit(&sh.kv_empty[v % S::kStages]);
+            if (k + 1 == n) {
+              mma_commit(&sh.o_full[h]);
+              continue;
+            }
+            if (h == 0) ok = arrived(next_k);
+            if (!ok) break;
+            qk(h, next_k % S::kStages);  // after the product that reads P, in issue order
+            mma_commit(&sh.s_full[h]);
+            if (h == halves - 1) {
+              mma_commit(&sh.kv_empty[next_k % S::kStages]);
+              if (k + 2 == n) mma_commit(&sh.q_empty);
+            }
+          }
+        }
+        at += 2 * n;
+      }
+      if (!ok) {
+        // Give what was issued a while to end before tensor memory is freed.
+        volatile int no = 0;
+        mma_commit(&sh.drain);
+        wait_for(&sh.drain, 0, &no);
+      }
+    }
+    __syncwarp();
+    if (warp == 13 && lane == 0) {
+      // Where this run's start cuts a unit, and is the first to do so, the unit's
+      // parts are joined in this worker's name.
+      int4 j = make_int4(-1, 0, 0, 0);
+      Walk w;
+      if (w.seek(c0, c1, prefix, p, by_group) && w.k0 > 0 &&
+          split_worker(w.u0 + 1, total, workers) + 1 == me)
+        j = make_int4(w.b, w.g, w.rt, static_cast<int>(split_worker(w.u0 + w.unit.tiles, total, workers)));
+      ws.joins[me] = j;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_free(tmem, 512);
+  if (tid == 0) ws.failed[me] = *dead;
+}
+
+
+constexpr int kTilesJoinThreads = 256, kJoinRows = 32;
+
+// Joins the parts of the unit that worker w's boundary is the first to cut, 32
+// rows a block: out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).  Blocks past
+// the workers write the status words.
+template <int kIn, int D>
+__global__ void __launch_bounds__(kTilesJoinThreads)
+    attn_tiles_join_kernel(const AttnParams p, const TilesSpace ws) {
+  constexpr int kLanes = D / 4, kAtOnce = kTilesJoinThreads / kLanes;
+  constexpr int kBlocks = kUnitRows / kJoinRows;
+  grid_dep_wait();  // in every block: this grid must not be done before the first kernel is
+  const int units = static_cast<int>(ws.workers) * kBlocks;
+  if (static_cast<int>(blockIdx.x) >= units) {
+    int late = 0;
+    for (uint32_t w = threadIdx.x; w < ws.workers; w += blockDim.x) late |= ws.failed[w];
+    late = __syncthreads_or(late);
+    attn_write_status(p, blockIdx.x - units, late ? HS_ST_TIMEOUT : 0);
+    return;
+  }
+  const int w = blockIdx.x / kBlocks;
+  const int4 j = ws.joins[w];
+  if (j.x < 0) return;
+  const AttnRow row = attn_row(p, j.x);
+  const int w0 = w - 1, w1 = j.w;
+  const int rows = min(kUnitRows, row.n * p.group - j.z * kUnitRows);
+  const float vs = p.scale[1] ? __ldg(p.scale[1]) : 1.0f;
+  const int lane = threadIdx.x % kLanes;
+  const int first = (blockIdx.x % kBlocks) * kJoinRows;
+  for (int m = first + threadIdx.x / kLanes; m < min(rows, first + kJoinRows); m += kAtOnce) {
+    auto part = [&](int x) {
+      return ws.slots + static_cast<int64_t>(2 * x + (x == w0 ? 1 : 0)) * tiles_slot_floats(D);
+    };
+    float top = -INFINITY, l = 0.f;
+    for (int x = w0; x <= w1; ++x) top = fmaxf(top, part(x)[kUnitRows * D + m]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = w0; x <= w1; ++x) {
+      const float* s = part(x);
+      const float add = fast_exp2(s[kUnitRows * D + m] - ref);
+      const float4 o = *reinterpret_cast<const float4*>(s + m * D + lane * 4);
+      l += add;
+      acc.x += add * o.x;
+      acc.y += add * o.y;
+      acc.z += add * o.z;
+      acc.w += add * o.w;
+    }
+    const float f = top == -INFINITY ? 0.f : vs / l;
+    const int r = j.z * kUnitRows + m, i = r / p.group, head = j.y * p.group + (r - i * p.group);
+    const int64_t tok = row.q0 + i;
+    constexpr bool kB = kIn == HS_DT_BF16;
+    *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + lane * 8) =
+        make_uint2(pack2t<kB>(acc.x * f, acc.y * f), pack2t<kB>(acc.z * f, acc.w * f));
+    if (lane == 0 && p.lse)
+      p.lse[tok * p.heads + head] = top == -INFINITY ? -INFINITY : kLn2 * (top + log2f(l));
+  }
+}
+
+struct TilesKernels {
+  void (*main)(const AttnParams, const TilesSpace, const FastDiv, const CUtensorMap,
+               const CUtensorMap, int);
+  void (*join)(const AttnParams, const TilesSpace);
+  int smem;
+};
+template <int kIn, bool kFp8, int D>
+TilesKernels tiles_kernels() {
+  return TilesKernels{attn_tiles_kernel<kIn, kFp8, D>, attn_tiles_join_kernel<kIn, D>,
+                      TilesShape<kIn, kFp8, D>::kRing + 1024};
+}
+TilesKernels tiles_pick(int in_dtype, bool fp8, int dim) {
+  if (in_dtype == HS_DT_BF16) {
+    if (dim == 128)
+      return fp8 ? tiles_kernels<HS_DT_BF16, true, 128>() : tiles_kernels<HS_DT_BF16, false, 128>();
+    return fp8 ? tiles_kernels<HS_DT_BF16, true, 64>() : tiles_kernels<HS_DT_BF16, false, 64>();
+  }
+  if (dim == 128)
+    return fp8 ? tiles_kernels<HS_DT_F16, true, 128>() : tiles_kernels<HS_DT_F16, false, 128>();
+  return fp8 ? tiles_kernels<HS_DT_F16, true, 64>() : tiles_kernels<HS_DT_F16, false, 64>();
+}
+
+std::mutex g_mu;
+bool g_ready[64] = {false};
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+// Once per device: shared memory opt-in, and a check that the kernel was
+// launched with the registers that its warpgroups redistribute (a split of
+// more than the launch's total would wait for ever).
+hs_err tiles_setup(const DeviceInfo& dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (g_ready[dev.device]) return HS_OK;
+  for (int dt : {HS_DT_F16, HS_DT_BF16})
+    for (bool fp8 : {false, true})
+      for (int dim : {64, 128}) {
+        const TilesKernels k = tiles_pick(dt, fp8, dim);
+        const void* f = reinterpret_cast<const void*>(k.main);
+        cudaFuncAttributes at;
+        cudaError_t e = cudaFuncGetAttributes(&at, f);
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem + kPrefixBytes);
+        if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention: %s", cudaGetErrorString(e));
+        if (at.numRegs * 4 < static_cast<int>(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs))
+          return fail(HS_ERR_CUDA, "hs_paged_attention: built with %d registers a thread", at.numRegs);
+      }
+  if (g_encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got);
+    if (e != cudaSuccess || got != cudaDriverEntryPointSuccess || fn == nullptr)
+      return fail(HS_ERR_CUDA, "hs_paged_attention: cuTensorMapEncodeTiled is not available");
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  g_ready[dev.device] = true;
+  return HS_OK;
+}
+
+// A cache as [pages][page][heads][dim], read in boxes of `keys` rows of 64 dims
+// of one head, swizzled as the MMA wants it.
+bool encode_cache(CUtensorMap* map, const AttnParams& p, int which, bool bf16, int keys) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.kv_heads),
+                              p.page_size, static_cast<cuuint64_t>(p.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.c_head), static_cast<cuuint64_t>(p.c_off),
+                                 static_cast<cuuint64_t>(p.c_page)};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(keys), 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<unsigned char*>(p.cache[which]), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int64_t kTilesHead = 64 * 1024;  // joins and failure words, up to 2048 workers
+
+}  // namespace
+
+int64_t tiles_workspace(int dim, const DeviceInfo& dev) {
+  return kTilesHead + 2ll * dev.sm_count * tiles_slot_floats(dim) * 4;
+}
+
+hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace,
+                    const DeviceInfo& dev, cudaStream_t stream) {
+  if (dev.sm_count > 2048) return fail(HS_ERR_UNSUPPORTED, "hs_paged_attention: %d SMs", dev.sm_count);
+  const hs_err err = tiles_setup(dev);
+  if (err != HS_OK) return err;
+  const TilesKernels k = tiles_pick(in_dtype, fp8, p.dim);
+  TilesSpace ws;
+  unsigned char* at = static_cast<unsigned char*>(workspace);
+  ws.joins = reinterpret_cast<int4*>(at);
+  ws.failed = reinterpret_cast<int32_t*>(at + 2048 * sizeof(int4));
+  ws.slots = reinterpret_cast<float*>(at + kTilesHead);
+  ws.workers = static_cast<uint32_t>(dev.sm_count);
+  CUtensorMap maps[2] = {};
+  int box = 0;
+  if (!fp8) {
+    if (p.page_size % kKeys == 0)
+      box = kKeys;
+    else if (p.page_size % 8 == 0 && kKeys % p.page_size == 0)
+      box = static_cast<int>(p.page_size);
+    if (p.num_pages < 1 || p.num_pages >= INT32_MAX) box = 0;
+    // Strides that a tensor map cannot hold go through registers.
+    for (int i = 0; box > 0 && i < 2; ++i)
+      if (!encode_cache(&maps[i], p, i, in_dtype == HS_DT_BF16, box)) box = 0;
+  }
+  const uint32_t group = static_cast<uint32_t>(p.group);
+  k.main<<<dev.sm_count, kThreads, k.smem + (p.batch + 1) * 4, stream>>>(
+      p, ws, FastDiv{fastdiv_magic(group), group}, maps[0], maps[1], box);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention launch: %s", cudaGetErrorString(e));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count * (kUnitRows / kJoinRows) + (p.status ? p.batch : 0)));
+  cfg.blockDim = dim3(kTilesJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k.join, p, ws);
+  if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention join: %s", cudaGetErrorString(e));
+  return HS_OK;
+}
+
+}  // namespace hs
