@@ -440,26 +440,61 @@ def probe_read(src, sink, stream=None) -> None:
                 "hs_probe_read")
 
 
-def _on_device(device, **tensors):
-    """Every given tensor is on the same CUDA device; returns its device guard."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {device}")
-    return torch.cuda.device(device)
+# The serving operators run once per layer of every decode step, where the call
+# itself costs as much as the kernel: their checks read each attribute once and
+# build messages only on failure, the argument blocks are packed in one go, and
+# the device guard is entered only when it changes something.
+def _device_of(first, *others) -> int:
+    """Index of the CUDA device that holds every given tensor."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+    return dev
 
 
-def _lens_flags(lens, req_state, batch, name):
-    """(seq, req) width flags of int32 or int64 [batch] lengths and state rows."""
-    for t, what in ((lens, name), (req_state, "req_state")):
-        if t.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
-        _need(t, t.dtype, what, 1)
-        if t.numel() != batch:
-            raise ValueError(f"{what} needs one entry per batch row ({batch}), got {t.numel()}")
-    return (_capi.SEQ_LENS_I64 if lens.dtype == torch.int64 else 0) | (
-        _capi.REQ_STATE_I64 if req_state.dtype == torch.int64 else 0)
+def _raw_stream(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _launch(dev, where, fn, *args) -> None:
+    if torch._C._cuda_getDevice() == dev:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args)
+    if code:
+        _capi.check(code, where)
+
+
+def _vector(t, dtype, n, name):
+    """A contiguous 1-D tensor of n entries; returns its address."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} entries, got "
+                         f"{list(t.shape)}")
+    return t.data_ptr()
+
+
+def _matrix(t, dtype, name):
+    """A 2-D tensor with contiguous rows; returns its address, row stride, rows and columns."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {list(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return t.data_ptr(), t.stride(0), rows, cols
+
+
+def _lens(t, n, name):
+    """Address of an int32 or int64 [n] vector, and whether it is int64."""
+    wide = t.dtype is torch.int64
+    return _vector(t, torch.int64 if wide else torch.int32, n, name), wide
 
 
 def assign_slots(ctx_lens, new_lens, req_state, block_table, free_blocks, free_top, *, block_size,
@@ -474,81 +509,78 @@ def assign_slots(ctx_lens, new_lens, req_state, block_table, free_blocks, free_t
     ``ctx_lens``); ``cache_loc`` and ``positions`` int64; the rest int32.  ``free_top_out``
     (default ``free_top`` itself) gets the new height, and ``seq_lens`` may be ``ctx_lens``:
     a captured call then carries both from one replay to the next."""
-    batch = new_lens.numel()
-    _need(new_lens, torch.int32, "new_lens", 1)
-    flags = _lens_flags(ctx_lens, req_state, batch, "ctx_lens")
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(free_blocks, torch.int32, "free_blocks", 1)
-    if free_top_out is None:
-        free_top_out = free_top
-    for t, name, n in ((free_top, "free_top", 1), (free_top_out, "free_top_out", 1),
-                       (cu_new, "cu_new", batch + 1)):
-        _need(t, torch.int32, name, 1)
-        if t.numel() != n:
-            raise ValueError(f"{name} needs {n} entries, got {t.numel()}")
-    _need(seq_lens, ctx_lens.dtype, "seq_lens", 1)
-    _need(cache_loc, torch.int64, "cache_loc", 1)
-    if seq_lens.numel() != batch:
-        raise ValueError("seq_lens needs one entry per batch row")
-    for t, dtype, name, n in ((positions, torch.int64, "positions", cache_loc.numel()),
-                              (token_row, torch.int32, "token_row", cache_loc.numel()),
-                              (status, torch.int32, "status", batch)):
-        if t is not None:
-            _need(t, dtype, name, 1)
-            if t.numel() != n:
-                raise ValueError(f"{name} needs {n} entries, got {t.numel()}")
-    with _on_device(ctx_lens.device, new_lens=new_lens, req_state=req_state,
-                    block_table=block_table, free_blocks=free_blocks, free_top=free_top,
-                    free_top_out=free_top_out, cu_new=cu_new, seq_lens=seq_lens,
-                    cache_loc=cache_loc, positions=positions, token_row=token_row, status=status):
-        _capi.check(_lib().hs_assign_slots(
-            _ptr(ctx_lens), _ptr(new_lens), _ptr(req_state), batch, flags, _ptr(block_table),
-            block_table.stride(0), block_table.shape[0], block_table.shape[1], int(block_size),
-            _ptr(free_blocks), free_blocks.numel(), _ptr(free_top), _ptr(free_top_out),
-            _ptr(cu_new), _ptr(seq_lens), _ptr(cache_loc), _ptr(positions), _ptr(token_row),
-            cache_loc.numel(), _ptr(status), C.c_void_p(_stream(stream))), "hs_assign_slots")
+    i32, i64 = torch.int32, torch.int64
+    batch, n, free = new_lens.numel(), cache_loc.numel(), free_blocks.numel()
+    new_p = _vector(new_lens, i32, batch, "new_lens")
+    ctx_p, wide_len = _lens(ctx_lens, batch, "ctx_lens")
+    req_p, wide_req = _lens(req_state, batch, "req_state")
+    table_p, table_stride, states, blocks = _matrix(block_table, i32, "block_table")
+    free_p = _vector(free_blocks, i32, free, "free_blocks")
+    top_p = _vector(free_top, i32, 1, "free_top")
+    out_p = top_p if free_top_out is None else _vector(free_top_out, i32, 1, "free_top_out")
+    cu_p = _vector(cu_new, i32, batch + 1, "cu_new")
+    seq_p = _vector(seq_lens, ctx_lens.dtype, batch, "seq_lens")
+    loc_p = _vector(cache_loc, i64, n, "cache_loc")
+    pos_p = 0 if positions is None else _vector(positions, i64, n, "positions")
+    row_p = 0 if token_row is None else _vector(token_row, i32, n, "token_row")
+    st_p = 0 if status is None else _vector(status, i32, batch, "status")
+    dev = _device_of(ctx_lens, new_lens, req_state, block_table, free_blocks, free_top,
+                     free_top_out, cu_new, seq_lens, cache_loc, positions, token_row, status)
+    _launch(dev, "hs_assign_slots", _lib().hs_assign_slots, ctx_p, new_p, req_p, batch,
+            (_capi.SEQ_LENS_I64 if wide_len else 0) | (_capi.REQ_STATE_I64 if wide_req else 0),
+            table_p, table_stride, states, blocks, block_size, free_p, free, top_p, out_p, cu_p,
+            seq_p, loc_p, pos_p, row_p, n, st_p, _raw_stream(stream, dev))
 
 
 def _paged_cache(k_cache, v_cache, dtype, page_size):
     """(cache dtype code, kv heads, dim, page / offset / head strides in bytes, pages) of a
     paged cache [pages, page_size, heads, dim] or [slots, heads, dim] of ``dtype`` or FP8."""
-    if k_cache.dtype != v_cache.dtype or (k_cache.dtype != dtype
-                                          and k_cache.dtype not in _FP8_CACHE):
+    kind = k_cache.dtype
+    if v_cache.dtype is not kind or (kind is not dtype and kind not in _FP8_CACHE):
         raise TypeError(f"caches must both be {dtype}, float8_e4m3fn or uint8 (E4M3 codes)")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache need the same shape and layout")
     strides, shape = k_cache.stride(), k_cache.shape
-    if k_cache.dim() == 4:
-        if shape[1] != page_size:
-            raise ValueError(f"page_size mismatch: cache has {shape[1]}, expected {page_size}")
-        pages, (page, off, head) = shape[0], strides[:3]
-    elif k_cache.dim() == 3:
-        pages, page, (off, head) = shape[0] // page_size, strides[0] * page_size, strides[:2]
+    if shape != v_cache.shape or strides != v_cache.stride():
+        raise ValueError("k_cache and v_cache need the same shape and layout")
+    if len(shape) == 4:
+        pages, rows, heads, dim = shape
+        page, off, head, last = strides
+        if rows != page_size:
+            raise ValueError(f"page_size mismatch: cache has {rows}, expected {page_size}")
+    elif len(shape) == 3:
+        if page_size < 1:
+            raise ValueError("page_size must be >= 1")
+        slots, heads, dim = shape
+        off, head, last = strides
+        pages, page = slots // page_size, off * page_size
     else:
         raise ValueError("caches must be 3-D or 4-D")
-    if shape[-1] > 1 and strides[-1] != 1:
+    if dim > 1 and last != 1:
         raise ValueError("caches need contiguous dims")
-    size = k_cache.element_size()
-    code = _capi.DT_E4M3 if k_cache.dtype in _FP8_CACHE and dtype != k_cache.dtype else _FP8_IN[dtype]
-    return code, shape[-2], shape[-1], page * size, off * size, head * size, pages
+    if kind is dtype:
+        size = 4 if dtype is torch.float32 else 2
+        return _FP8_IN[dtype], heads, dim, page * size, off * size, head * size, pages
+    return _capi.DT_E4M3, heads, dim, page, off, head, pages
 
 
-def _heads(t, dtype, name, shape):
-    """Token and head strides of [tokens, heads, dim] with contiguous dims."""
-    if t.dtype != dtype:
+def _heads(t, dtype, name, tokens, heads, dim):
+    """Address, token and head strides of [tokens, heads, dim] with contiguous dims."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or (shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be {list(shape)} with a contiguous last dim, got "
+    if t.shape != (tokens, heads, dim) or (dim > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be {[tokens, heads, dim]} with a contiguous last dim, got "
                          f"{list(t.shape)}")
-    return t.stride(0), t.stride(1)
+    strides = t.stride()
+    return t.data_ptr(), strides[0], strides[1]
 
 
-def _cache_scales(code, k_scale, v_scale):
-    for sc, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if sc is not None:
-            _need(sc, torch.float32, name)
-            if code != _capi.DT_E4M3 or sc.numel() != 1:
-                raise ValueError(f"{name}: one element, with an FP8 cache only")
+def _cache_scale(t, code, name):
+    if t is None:
+        return 0
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if code != _capi.DT_E4M3 or t.numel() != 1:
+        raise ValueError(f"{name}: one element, with an FP8 cache only")
+    return t.data_ptr()
 
 
 def qk_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k_cache, v_cache,
@@ -560,96 +592,101 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k
     ``q_out`` (may be q) and k and v to slot cache_loc[t] of a paged cache (see
     include/hisparse.h; layouts and FP8 scales as in ``fp8_store_kv``).  float32, float16 or
     bfloat16; the cache has the same type or is FP8.  ``cos_sin`` None = no rotation."""
-    if q.dtype not in _FP8_IN:
+    dt = q.dtype
+    if dt not in _FP8_IN:
         raise TypeError("q must be float32, float16 or bfloat16")
     if q.dim() != 3:
         raise ValueError(f"q must be [tokens, heads, dim], got {list(q.shape)}")
-    code, kv_heads, dim, c_page, c_off, c_head, pages = _paged_cache(k_cache, v_cache, q.dtype,
+    code, kv_heads, dim, c_page, c_off, c_head, pages = _paged_cache(k_cache, v_cache, dt,
                                                                      page_size)
-    T, heads = q.shape[0], q.shape[1]
-    qs = _heads(q, q.dtype, "q", (T, heads, dim))
-    ks = _heads(k, q.dtype, "k", (T, kv_heads, dim))
-    vs = _heads(v, q.dtype, "v", (T, kv_heads, dim))
-    os = _heads(q_out, q.dtype, "q_out", (T, heads, dim))
-    if q_out.data_ptr() == q.data_ptr() and os != qs:
+    T, heads, _ = q.shape
+    q_a = _heads(q, dt, "q", T, heads, dim)
+    k_a = _heads(k, dt, "k", T, kv_heads, dim)
+    v_a = _heads(v, dt, "v", T, kv_heads, dim)
+    o_a = _heads(q_out, dt, "q_out", T, heads, dim)
+    if o_a[0] == q_a[0] and o_a != q_a:
         raise ValueError("q_out may be q itself, not another view of its memory")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, q.dtype, name, 1)
-            if w.numel() != dim:
-                raise ValueError(f"{name} needs {dim} entries")
-    rot = max_pos = 0
-    if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin", 2)
-        _need(positions, torch.int64, "positions", 1)
-        if not cos_sin.is_contiguous() or positions.numel() != T:
-            raise ValueError("cos_sin must be contiguous and positions have one entry per token")
-        max_pos, rot = cos_sin.shape
-    else:
+    qw_p = 0 if q_weight is None else _vector(q_weight, dt, dim, "q_weight")
+    kw_p = 0 if k_weight is None else _vector(k_weight, dt, dim, "k_weight")
+    rot = max_pos = cs_p = pos_p = 0
+    if cos_sin is None:
         positions = None
-    _need(cache_loc, torch.int64, "cache_loc", 1)
-    if cache_loc.numel() != T:
-        raise ValueError("cache_loc needs one entry per token")
-    _cache_scales(code, k_scale, v_scale)
-    if status is not None:
-        _need(status, torch.int32, "status", 1)
-    with _on_device(q.device, k=k, v=v, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
-                    positions=positions, q_out=q_out, k_cache=k_cache, v_cache=v_cache,
-                    cache_loc=cache_loc, k_scale=k_scale, v_scale=v_scale, status=status):
-        args = _capi.QkNormRopeArgs(
-            T, heads, kv_heads, dim, rot, _FP8_IN[q.dtype], code,
-            _capi.ROPE_INTERLEAVED if interleaved else 0, page_size, eps, 0, _ptr(q), *qs, _ptr(k),
-            *ks, _ptr(v), *vs, _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), max_pos,
-            _ptr(positions), _ptr(q_out), *os, _ptr(k_cache), _ptr(v_cache), c_page, c_off, c_head,
-            pages * page_size, _ptr(cache_loc), _ptr(k_scale), _ptr(v_scale), _ptr(status))
-        _capi.check(_lib().hs_qk_norm_rope_store(C.byref(args), C.c_void_p(_stream(stream))),
-                    "hs_qk_norm_rope_store")
+    else:
+        cs_p, cs_stride, max_pos, rot = _matrix(cos_sin, torch.float32, "cos_sin")
+        if cs_stride != rot and max_pos > 1:
+            raise ValueError("cos_sin must be contiguous")
+        pos_p = _vector(positions, torch.int64, T, "positions")
+    loc_p = _vector(cache_loc, torch.int64, T, "cache_loc")
+    ks_p, vs_p = _cache_scale(k_scale, code, "k_scale"), _cache_scale(v_scale, code, "v_scale")
+    st_p = 0 if status is None else _vector(status, torch.int32, 1, "status")
+    dev = _device_of(q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k_cache, v_cache,
+                     cache_loc, k_scale, v_scale, status)
+    block = _capi.QK_NORM_ROPE.pack(
+        T, heads, kv_heads, dim, rot, _FP8_IN[dt], code,
+        _capi.ROPE_INTERLEAVED if interleaved else 0, page_size, eps, 0, *q_a, *k_a, *v_a, qw_p,
+        kw_p, cs_p, max_pos, pos_p, *o_a, k_cache.data_ptr(), v_cache.data_ptr(), c_page, c_off,
+        c_head, pages * page_size, loc_p, ks_p, vs_p, st_p)
+    _launch(dev, "hs_qk_norm_rope_store", _lib().hs_qk_norm_rope_store, block,
+            _raw_stream(stream, dev))
 
 
-def _paged_attention_args(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, *,
-                          max_q_len, scale, window, k_scale, v_scale, page_size, lse, status):
-    if q.dtype not in _FP8_IN:
+def _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, max_q_len,
+                     scale, window, k_scale, v_scale, page_size, lse, status):
+    """The device and the fields of hs_paged_attention_args before its workspace."""
+    i32 = torch.int32
+    dt = q.dtype
+    if dt not in _FP8_IN:
         raise TypeError("q must be float32, float16 or bfloat16")
     if q.dim() != 3:
         raise ValueError(f"q must be [tokens, heads, dim], got {list(q.shape)}")
-    code, kv_heads, dim, c_page, c_off, c_head, pages = _paged_cache(k_cache, v_cache, q.dtype,
+    code, kv_heads, dim, c_page, c_off, c_head, pages = _paged_cache(k_cache, v_cache, dt,
                                                                      page_size)
-    T, heads = q.shape[0], q.shape[1]
-    qs = _heads(q, q.dtype, "q", (T, heads, dim))
-    os = _heads(out, q.dtype, "out", (T, heads, dim))
-    _need(cu_q, torch.int32, "cu_q", 1)
+    T, heads, _ = q.shape
+    q_a = _heads(q, dt, "q", T, heads, dim)
+    o_a = _heads(out, dt, "out", T, heads, dim)
     batch = cu_q.numel() - 1
     if batch < 0:
         raise ValueError("cu_q needs batch + 1 entries")
-    flags = _lens_flags(seq_lens, req_state, batch, "seq_lens")
-    _need(block_table, torch.int32, "block_table", 2)
+    cu_p = _vector(cu_q, i32, batch + 1, "cu_q")
+    seq_p, wide_len = _lens(seq_lens, batch, "seq_lens")
+    req_p, wide_req = _lens(req_state, batch, "req_state")
+    table_p, table_stride, states, blocks = _matrix(block_table, i32, "block_table")
+    lse_p = 0
     if lse is not None:
-        _need(lse, torch.float32, "lse", 2)
-        if tuple(lse.shape) != (T, heads) or not lse.is_contiguous():
+        lse_p, lse_stride, lse_rows, lse_cols = _matrix(lse, torch.float32, "lse")
+        if (lse_rows, lse_cols) != (T, heads) or (lse_stride != heads and T > 1):
             raise ValueError(f"lse must be a contiguous [{T}, {heads}]")
-    if status is not None:
-        _need(status, torch.int32, "status", 1)
-        if status.numel() != batch:
-            raise ValueError("status needs one entry per batch row")
-    _cache_scales(code, k_scale, v_scale)
-    return _capi.PagedAttentionArgs(
-        batch, heads, kv_heads, dim, _FP8_IN[q.dtype], code, flags, page_size, max_q_len, window,
-        dim ** -0.5 if scale is None else scale, block_table.shape[1], T, _ptr(q), *qs, _ptr(out),
-        *os, _ptr(lse), _ptr(k_cache), _ptr(v_cache), c_page, c_off, c_head, pages,
-        _ptr(block_table), block_table.stride(0), block_table.shape[0], _ptr(req_state),
-        _ptr(cu_q), _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale), _ptr(status), None, 0)
+    st_p = 0 if status is None else _vector(status, i32, batch, "status")
+    ks_p, vs_p = _cache_scale(k_scale, code, "k_scale"), _cache_scale(v_scale, code, "v_scale")
+    dev = _device_of(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, lse,
+                     k_scale, v_scale, status)
+    return dev, (
+        batch, heads, kv_heads, dim, _FP8_IN[dt], code,
+        (_capi.SEQ_LENS_I64 if wide_len else 0) | (_capi.REQ_STATE_I64 if wide_req else 0),
+        page_size, max_q_len, window, dim ** -0.5 if scale is None else scale, blocks, T, *q_a,
+        *o_a, lse_p, k_cache.data_ptr(), v_cache.data_ptr(), c_page, c_off, c_head, pages, table_p,
+        table_stride, states, req_p, cu_p, seq_p, ks_p, vs_p, st_p)
+
+
+def _attention_workspace(dev, fields) -> int:
+    block = _capi.PAGED_ATTENTION.pack(*fields, 0, 0)
+    fn = _lib().hs_paged_attention_workspace_bytes
+    if torch._C._cuda_getDevice() == dev:
+        n = fn(block)
+    else:
+        with torch.cuda.device(dev):
+            n = fn(block)
+    if n < 0:
+        _capi.check(-n, "hs_paged_attention_workspace_bytes")
+    return n
 
 
 def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
                                     out, *, max_q_len, window=0, page_size=16) -> int:
     """Bytes of workspace that ``paged_attention`` needs for tensors of these shapes and types."""
-    args = _paged_attention_args(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out,
-                                 max_q_len=max_q_len, scale=None, window=window, k_scale=None,
-                                 v_scale=None, page_size=page_size, lse=None, status=None)
-    with _on_device(q.device):
-        n = int(_lib().hs_paged_attention_workspace_bytes(C.byref(args)))
-    _capi.check(max(0, -n), "hs_paged_attention_workspace_bytes")
-    return n
+    return _attention_workspace(*_attention_block(
+        q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, max_q_len, None, window,
+        None, None, page_size, None, None))
 
 
 def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, *, max_q_len,
@@ -662,23 +699,22 @@ def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
     last ``window`` keys only; ``lse`` [T, heads] gets the softmax's log-sum-exp.  ``workspace``
     (uint8, 256-byte aligned, ``paged_attention_workspace_bytes`` of it) may be passed to keep
     one for a captured graph; otherwise one is allocated for the call."""
-    args = _paged_attention_args(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out,
-                                 max_q_len=max_q_len, scale=scale, window=window, k_scale=k_scale,
-                                 v_scale=v_scale, page_size=page_size, lse=lse, status=status)
-    lib = _lib()
-    with _on_device(q.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                    req_state=req_state, cu_q=cu_q, seq_lens=seq_lens, out=out, lse=lse,
-                    k_scale=k_scale, v_scale=v_scale, status=status, workspace=workspace):
-        stream = _stream(stream)
-        if workspace is None:
-            n = int(lib.hs_paged_attention_workspace_bytes(C.byref(args)))
-            if n > 0:
-                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-                if stream != torch.cuda.current_stream().cuda_stream:
-                    # the allocator must not hand it out again before that stream is done
-                    workspace.record_stream(torch.cuda.ExternalStream(stream))
-        if workspace is not None:
-            _need(workspace, torch.uint8, "workspace", 1)
-            args.workspace, args.workspace_bytes = _ptr(workspace), workspace.numel()
-        _capi.check(lib.hs_paged_attention(C.byref(args), C.c_void_p(stream)),
-                    "hs_paged_attention")
+    dev, fields = _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
+                                   out, max_q_len, scale, window, k_scale, v_scale, page_size,
+                                   lse, status)
+    raw = _raw_stream(stream, dev)
+    space_p = n = 0
+    if workspace is not None:
+        n = workspace.numel()
+        space_p = _vector(workspace, torch.uint8, n, "workspace")
+        _device_of(q, workspace)
+    else:
+        n = _attention_workspace(dev, fields)
+        if n > 0:
+            workspace = q.new_empty(n, dtype=torch.uint8)
+            space_p = workspace.data_ptr()
+            if stream is not None and raw != torch._C._cuda_getCurrentRawStream(dev):
+                # the allocator must not hand it out again before that stream is done
+                workspace.record_stream(torch.cuda.ExternalStream(raw, device=dev))
+    _launch(dev, "hs_paged_attention", _lib().hs_paged_attention,
+            _capi.PAGED_ATTENTION.pack(*fields, space_p, n), raw)

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -107,6 +108,18 @@ class PagedAttentionArgs(C.Structure):
     ]
 
 
+def _packer(block) -> struct.Struct:
+    """The layout of an argument block, for filling one in a single call."""
+    code = {C.c_int32: "i", C.c_int64: "q", C.c_float: "f", C.c_void_p: "P"}
+    p = struct.Struct("@" + "".join(code[t] for _, t in block._fields_))
+    assert p.size == C.sizeof(block)
+    return p
+
+
+QK_NORM_ROPE = _packer(QkNormRopeArgs)
+PAGED_ATTENTION = _packer(PagedAttentionArgs)
+
+
 class HisparseError(RuntimeError):
     def __init__(self, code: int, where: str, msg: str):
         super().__init__(f"{where}: {msg} (hs_err {code})")
@@ -119,6 +132,8 @@ _lib: C.CDLL | None = None
 
 def load() -> C.CDLL:
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -160,11 +175,12 @@ def load() -> C.CDLL:
         lib.hs_assign_slots.argtypes = [vp, vp, vp, i32, i32, vp, i64, i64, i32, i32, vp, i64, vp,
                                         vp, vp, vp, vp, vp, vp, i64, vp, vp]
         lib.hs_assign_slots.restype = C.c_int
-        lib.hs_qk_norm_rope_store.argtypes = [C.POINTER(QkNormRopeArgs), vp]
+        # argument blocks come as packed bytes or by reference
+        lib.hs_qk_norm_rope_store.argtypes = [vp, vp]
         lib.hs_qk_norm_rope_store.restype = C.c_int
-        lib.hs_paged_attention.argtypes = [C.POINTER(PagedAttentionArgs), vp]
+        lib.hs_paged_attention.argtypes = [vp, vp]
         lib.hs_paged_attention.restype = C.c_int
-        lib.hs_paged_attention_workspace_bytes.argtypes = [C.POINTER(PagedAttentionArgs)]
+        lib.hs_paged_attention_workspace_bytes.argtypes = [vp]
         lib.hs_paged_attention_workspace_bytes.restype = i64
         lib.hs_err_string.argtypes = [i32]
         lib.hs_err_string.restype = C.c_char_p

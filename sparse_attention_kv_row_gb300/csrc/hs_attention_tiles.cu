@@ -40,7 +40,7 @@ constexpr int kHalf = 128;         // rows per MMA
 constexpr int kUnitRows = 2 * kHalf;
 constexpr int kThreads = 512;
 constexpr int kLoaders = 128;
-constexpr uint32_t kSoftmaxRegs = 176, kLoaderRegs = 112, kMmaRegs = 48;
+constexpr uint32_t kSoftmaxRegs = 176, kLoaderRegs = 96, kMmaRegs = 64;
 static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 512, "65536 registers per SM");
 constexpr float kRaise = 8.f;      // log2 of how far weights may exceed 1
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -159,6 +159,7 @@ struct Shared {
   uint64_t kv_full[6], kv_empty[6];
   uint32_t tmem;
   volatile int dead;
+  int2 unit[2];  // for the MMA warp: rows and tiles of a unit, no tiles at the end
   float q_factor[2][kUnitRows];
   int64_t offs[2][kKeys];
 };
@@ -198,6 +199,44 @@ __device__ __forceinline__ uint32_t pack2t(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// Pairs of floats in 64-bit registers and the paired fp32 operations on them.
+__device__ __forceinline__ uint64_t two_words(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t two_floats(float lo, float hi) {
+  return two_words(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float low_float(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x));
+}
+__device__ __forceinline__ float high_float(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A place in the ring of K and V tiles.
+template <int kStages>
+struct RingAt {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 // 16-byte chunk c (of 64 elements' eight) of row r of a panel.
 __device__ __forceinline__ uint32_t in_panel(int r, int c) {
@@ -435,7 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 4; ++q) {
           mx[q] = __uint_as_float(s[q][0]);
 #pragma unroll
-          for (int c = 1; c < 32; ++c) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][c]));
+          for (int c = 1; c < 31; c += 2)
+            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[q][c])), __uint_as_float(s[q][c + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
         }
         const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         const bool raise = mine > top + kRaise;
@@ -447,33 +488,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= back;
           }
           if (k > w.k0) {
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(o, o_at + q * 32);
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(o, o_at + q * 16);
               tmem_wait_ld();
               tmem_pin(o);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * back);
-              tmem_st32(o_at + q * 32, o);
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * back);
+              tmem_st16(o_at + q * 16, o);
             }
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sc2 = two_floats(sc, sc), ref2 = two_floats(-ref, -ref);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w32[32];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w16[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint32_t* x = s[2 * h + (c >> 4)] + (c & 15) * 2;
-            const float a = fast_exp2(fmaf(__uint_as_float(x[0]), sc, -ref));
-            const float b = fast_exp2(fmaf(__uint_as_float(x[1]), sc, -ref));
-            sum[c & 3] += a + b;
-            w32[c] = pack2t<kBf16>(a, b);  // half a step off each
+          for (int c = 0; c < 16; ++c) {
+            const uint64_t x = fma2(two_words(s[q][2 * c], s[q][2 * c + 1]), sc2, ref2);
+            const float a = fast_exp2(low_float(x)), b = fast_exp2(high_float(x));
+            sum[c & 1] = add2(sum[c & 1], two_floats(a, b));
+            w16[c] = pack2t<kBf16>(a, b);  // half a step off each
           }
-          tmem_st32(s_at + h * 32, w32);
+          tmem_st16(s_at + q * 16, w16);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const uint64_t both = add2(sum[0], sum[1]);
+        l += low_float(both) + high_float(both);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&sh.p_full[half]);
@@ -491,26 +533,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* dst = p.out + tok * p.out_token + head * p.out_head;
       float* part = ws.slots + static_cast<int64_t>(2 * me + (w.k0 == 0 ? 1 : 0)) * tiles_slot_floats(D);
       const float f = whole ? inv * vs : inv;
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
-        tmem_ld32(o, o_at + q * 32);
+#pragma unroll 2
+      for (int q = 0; q < D / 16; ++q) {
+        uint32_t o[16];
+        tmem_ld16(o, o_at + q * 16);
         tmem_wait_ld();
         tmem_pin(o);
         if (live && whole) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               x[e] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[c * 8 + e * 2]) * f,
                                                __uint_as_float(o[c * 8 + e * 2 + 1]) * f);
-            *reinterpret_cast<uint4*>(dst + q * 64 + c * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(dst + q * 32 + c * 16) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         } else if (live) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<float4*>(part + m * D + q * 32 + c * 4) =
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float4*>(part + m * D + q * 16 + c * 4) =
                 make_float4(__uint_as_float(o[c * 4]) * f, __uint_as_float(o[c * 4 + 1]) * f,
                             __uint_as_float(o[c * 4 + 2]) * f, __uint_as_float(o[c * 4 + 3]) * f);
         }
@@ -524,22 +566,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_shrink<kLoaderRegs>();
     Loader<kIn, kFp8, D> ld{p, sh, q_at, ring, tid - 256};
     const int lt = tid - 256;
-    uint32_t at = 0, u_n = 0;  // K and V tiles so far; units so far
+    uint32_t u_n = 0, issued = 0;
+    RingAt<S::kStages> kv;
     auto claim = [&]() {
-      return loaders_all(wait_for(&sh.kv_empty[at % S::kStages], ((at / S::kStages) & 1) ^ 1, dead));
+      return loaders_all(wait_for(&sh.kv_empty[kv.stage], kv.phase ^ 1, dead));
     };
     auto publish = [&]() {
       fence_proxy_async_smem();  // the MMA reads through the async proxy
-      mbar_arrive(&sh.kv_full[at % S::kStages]);
-      ++at;
+      mbar_arrive(&sh.kv_full[kv.stage]);
+      kv.step();
+      ++issued;
     };
     bool ok = true;
     Walk w;
     bool more = w.seek(c0, c1, prefix, p, by_group);
+    if (lt == 0) {
+      // Where this run's start cuts a unit, and is the first to do so, the unit's
+      // parts are joined in this worker's name.
+      int4 j = make_int4(-1, 0, 0, 0);
+      if (more && w.k0 > 0 && split_worker(w.u0 + 1, total, workers) + 1 == me)
+        j = make_int4(w.b, w.g, w.rt, static_cast<int>(split_worker(w.u0 + w.unit.tiles, total, workers)));
+      ws.joins[me] = j;
+    }
     for (; more && ok; more = w.next(prefix, p, by_group), ++u_n) {
       ok = loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead));
       if (!ok) break;
       ld.load_q(w, by_group, u_n & 1);
+      if (lt == 0) sh.unit[u_n & 1] = make_int2(w.unit.rows, w.k1 - w.k0);
       fence_proxy_async_smem();
       mbar_arrive(&sh.q_full);
       const int64_t head = w.g * p.c_head;
@@ -557,14 +610,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int x = 0; x < S::kPieces; ++x) {
                 uint4 r[S::kPieceChunks];
                 ld.fetch(r, 0, x, true, head);
-                ld.store(r, at % S::kStages, x);
+                ld.store(r, kv.stage, x);
               }
               loaders_sync();  // offs is written again
               publish();
               continue;
             }
-            uint64_t* bar = &sh.kv_full[at % S::kStages];
-            const uint32_t dst = ring + (at % S::kStages) * S::kStage;
+            uint64_t* bar = &sh.kv_full[kv.stage];
+            const uint32_t dst = ring + kv.stage * S::kStage;
             if (lt == 0)
               mbar_arrive_expect_tx(bar, S::kStage);
             else
@@ -587,7 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tensor_load_4d(dst + x * S::kPanel + lt * box_keys * 128, v ? &v_map : &k_map, x * 64,
                                w.g, in_page, page, bar);
             }
-            ++at;
+            kv.step();
+            ++issued;
           }
         }
       } else {
@@ -604,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int in = x % S::kPieces;
           if (in == 0) ok = claim();
           if (!ok) return;
-          ld.store(r, at % S::kStages, in);
+          ld.store(r, kv.stage, in);
           if (in == S::kPieces - 1) publish();
         };
         fetch(ra, 0);
@@ -619,10 +673,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (ok) {
+      ok = loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead));
+      if (lt == 0) sh.unit[u_n & 1] = make_int2(0, 0);
+      mbar_arrive(&sh.q_full);
+    }
     if (!ok) {
       // The tensor-map loads still on their way write shared memory: see them in.
       volatile int no = 0;
-      for (uint32_t n = at > S::kStages ? at - S::kStages : 0; n < at; ++n)
+      for (uint32_t n = issued > S::kStages ? issued - S::kStages : 0; n < issued; ++n)
         wait_for(&sh.kv_full[n % S::kStages], (n / S::kStages) & 1, &no);
     }
   } else {
@@ -631,67 +690,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 12 && lane == 0) {
       constexpr uint32_t kQk = mma_shape(kBf16, kHalf, kKeys, false);
       constexpr uint32_t kPv = mma_shape(kBf16, kHalf, D, true);
-      uint32_t at = 0, u_n = 0, p_ph[2] = {0, 0};
+      constexpr uint32_t kHi = mma_desc_hi(1024);
       auto qk = [&](int half, uint32_t stage) {
-        const uint32_t a = q_at + half * S::kStage, b = ring + stage * S::kStage;
+        const uint32_t a = mma_desc_lo(q_at + half * S::kStage, 16);
+        const uint32_t b = mma_desc_lo(ring + stage * S::kStage, 16);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          const uint32_t o = (x / 4) * S::kPanel + (x % 4) * 32;
-          mma_smem(tmem + half * kKeys, mma_desc(a + o, 16, 1024), mma_desc(b + o, 16, 1024), kQk, x > 0);
+          const uint32_t o = ((x / 4) * S::kPanel + (x % 4) * 32) >> 4;
+          mma_smem<kHi>(tmem + half * kKeys, a + o, b + o, kQk, x > 0);
         }
+        mma_commit(&sh.s_full[half]);
       };
       auto pv = [&](int half, uint32_t stage, bool add) {
-        const uint32_t b = ring + stage * S::kStage;
+        const uint32_t b = mma_desc_lo(ring + stage * S::kStage, S::kPanel);
 #pragma unroll
         for (int x = 0; x < kKeys / 16; ++x)
-          mma_tmem(tmem + 256 + half * D, tmem + half * kKeys + x * 8,
-                   mma_desc(b + x * 2048, S::kPanel, 1024), kPv, add || x > 0);
+          mma_tmem<kHi>(tmem + 256 + half * D, tmem + half * kKeys + x * 8, b + x * 128, kPv, add || x > 0);
       };
-      auto arrived = [&](uint32_t n) {
-        const bool ok = wait_for(&sh.kv_full[n % S::kStages], (n / S::kStages) & 1, dead);
+      uint32_t u_n = 0, p0 = 0, p1 = 0;
+      RingAt<S::kStages> kv;
+      auto arrived = [&]() {
+        const bool got = wait_for(&sh.kv_full[kv.stage], kv.phase, dead);
         tc_fence_after();
-        return ok;
+        return got;
+      };
+      auto weights = [&](int half, uint32_t& phase) {
+        const bool got = wait_for(&sh.p_full[half], phase, dead);
+        phase ^= 1;
+        tc_fence_after();
+        return got;
       };
       bool ok = true;
-      Walk w;
-      bool more = w.seek(c0, c1, prefix, p, by_group);
-      for (; more && ok; more = w.next(prefix, p, by_group), ++u_n) {
-        const int halves = w.unit.rows > kHalf ? 2 : 1;
-        const int n = w.k1 - w.k0;
-        // K of tile k is stage at + 2 k, V the one after it.
-        ok = wait_for(&sh.q_full, u_n & 1, dead) && arrived(at);
-        if (!ok) break;
-        for (int h = 0; h < halves; ++h) {
-          qk(h, at % S::kStages);
-          mma_commit(&sh.s_full[h]);
-        }
-        mma_commit(&sh.kv_empty[at % S::kStages]);
-        if (n == 1) mma_commit(&sh.q_empty);
-        for (int k = 0; k < n && ok; ++k) {
-          const uint32_t v = at + 2 * k + 1, next_k = at + 2 * k + 2;
-          for (int h = 0; h < halves && ok; ++h) {
-            if (h == 0) ok = arrived(v);
-            ok = ok && wait_for(&sh.p_full[h], p_ph[h], dead);
-            if (!ok) break;
-            p_ph[h] ^= 1;
-            tc_fence_after();
-            pv(h, v % S::kStages, k > 0);
-            if (h == halves - 1) mma_commit(&sh.kv_empty[v % S::kStages]);
-            if (k + 1 == n) {
-              mma_commit(&sh.o_full[h]);
-              continue;
-            }
-            if (h == 0) ok = arrived(next_k);
-            if (!ok) break;
-            qk(h, next_k % S::kStages);  // after the product that reads P, in issue order
-            mma_commit(&sh.s_full[h]);
-            if (h == halves - 1) {
-              mma_commit(&sh.kv_empty[next_k % S::kStages]);
-              if (k + 2 == n) mma_commit(&sh.q_empty);
-            }
+      for (; ok; ++u_n) {
+        if (!(ok = wait_for(&sh.q_full, u_n & 1, dead))) break;
+        const bool two = sh.unit[u_n & 1].x > kHalf;
+        int left = sh.unit[u_n & 1].y;
+        if (left == 0 || !(ok = arrived())) break;
+        qk(0, kv.stage);
+        if (two) qk(1, kv.stage);
+        mma_commit(&sh.kv_empty[kv.stage]);
+        kv.step();
+        if (left == 1) mma_commit(&sh.q_empty);
+        for (bool add = false; left > 0; add = true) {
+          // The ring holds this tile's V and the next one's K.
+          --left;
+          if (!(ok = arrived() && weights(0, p0))) break;
+          const uint32_t v = kv.stage;
+          kv.step();
+          pv(0, v, add);
+          if (left == 0) {
+            mma_commit(&sh.o_full[0]);
+          } else {
+            if (!(ok = arrived())) break;
+            qk(0, kv.stage);  // over P, after the product that reads it: in issue order
           }
+          if (two) {
+            if (!(ok = weights(1, p1))) break;
+            pv(1, v, add);
+          }
+          mma_commit(&sh.kv_empty[v]);
+          if (left == 0) {
+            if (two) mma_commit(&sh.o_full[1]);
+            break;
+          }
+          if (two) qk(1, kv.stage);
+          mma_commit(&sh.kv_empty[kv.stage]);
+          if (left == 1) mma_commit(&sh.q_empty);
+          kv.step();
         }
-        at += 2 * n;
       }
       if (!ok) {
         // Give what was issued a while to end before tensor memory is freed.
@@ -701,16 +767,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    if (warp == 13 && lane == 0) {
-      // Where this run's start cuts a unit, and is the first to do so, the unit's
-      // parts are joined in this worker's name.
-      int4 j = make_int4(-1, 0, 0, 0);
-      Walk w;
-      if (w.seek(c0, c1, prefix, p, by_group) && w.k0 > 0 &&
-          split_worker(w.u0 + 1, total, workers) + 1 == me)
-        j = make_int4(w.b, w.g, w.rt, static_cast<int>(split_worker(w.u0 + w.unit.tiles, total, workers)));
-      ws.joins[me] = j;
-    }
   }
   tc_fence_before();
   __syncthreads();

@@ -31,20 +31,17 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-#define HS_R32(r)                                                                                 \
-  r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], r[10], r[11], r[12], r[13], r[14], \
-      r[15], r[16], r[17], r[18], r[19], r[20], r[21], r[22], r[23], r[24], r[25], r[26], r[27], \
-      r[28], r[29], r[30], r[31]
-#define HS_C32(c, r)                                                                            \
-  c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7]), c(r[8]), c(r[9]),     \
-      c(r[10]), c(r[11]), c(r[12]), c(r[13]), c(r[14]), c(r[15]), c(r[16]), c(r[17]), c(r[18]), \
-      c(r[19]), c(r[20]), c(r[21]), c(r[22]), c(r[23]), c(r[24]), c(r[25]), c(r[26]), c(r[27]), \
-      c(r[28]), c(r[29]), c(r[30]), c(r[31])
+#define HS_C16(c, r)                                                                        \
+  c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7]), c(r[8]), c(r[9]), \
+      c(r[10]), c(r[11]), c(r[12]), c(r[13]), c(r[14]), c(r[15])
+#define HS_C32(c, r)                                                                              \
+  HS_C16(c, r), c(r[16]), c(r[17]), c(r[18]), c(r[19]), c(r[20]), c(r[21]), c(r[22]), c(r[23]),  \
+      c(r[24]), c(r[25]), c(r[26]), c(r[27]), c(r[28]), c(r[29]), c(r[30]), c(r[31])
 #define HS_OUT(x) "=r"(x)
 #define HS_IN(x) "r"(x)
 #define HS_BOTH(x) "+r"(x)
 
-// 32 columns of this warp's 32 lanes, one lane a thread.  The values may be
+// 32 (16) columns of this warp's 32 lanes, one lane a thread.  The values may be
 // used after tmem_wait_ld() and tmem_pin() on them.
 __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
   asm volatile(
@@ -54,11 +51,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::
-          HS_C32(HS_IN, r),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : HS_C16(HS_OUT, r)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15};" ::HS_C16(HS_IN, r),
       "r"(addr)
       : "memory");
 }
@@ -72,6 +76,9 @@ __device__ __forceinline__ void tmem_wait_st() {
 __device__ __forceinline__ void tmem_pin(uint32_t (&r)[32]) {
   asm volatile("" : HS_C32(HS_BOTH, r)::"memory");
 }
+__device__ __forceinline__ void tmem_pin(uint32_t (&r)[16]) {
+  asm volatile("" : HS_C16(HS_BOTH, r)::"memory");
+}
 
 // ------------------------------------------------------------------ matrix multiply
 // Descriptor of an operand tile in shared memory, 128-byte swizzle (16-byte
@@ -79,9 +86,13 @@ __device__ __forceinline__ void tmem_pin(uint32_t (&r)[32]) {
 // K along the rows: groups of 8 rows are `group` bytes apart.  K across the
 // rows (rows hold 64 elements of M or N): `group` is the distance of 8 rows of
 // K, `block` that of the next 64 elements.
-__device__ __forceinline__ uint64_t mma_desc(uint32_t addr, uint32_t block, uint32_t group) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) |
-         (static_cast<uint64_t>(group >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// The low word holds the address (in 16 bytes) and `block`, the high word
+// `group`, the version and the swizzle.
+__device__ __forceinline__ uint32_t mma_desc_lo(uint32_t addr, uint32_t block) {
+  return ((addr & 0x3FFFF) >> 4) | (block >> 4 << 16);
+}
+__host__ __device__ constexpr uint32_t mma_desc_hi(uint32_t group) {
+  return group >> 4 | 1u << 14 | 2u << 29;
 }
 // Instruction descriptor: fp16 or bf16 operands, fp32 accumulator, M x N.
 __host__ __device__ constexpr uint32_t mma_shape(bool bf16, int m, int n, bool b_across) {
@@ -90,18 +101,23 @@ __host__ __device__ constexpr uint32_t mma_shape(bool bf16, int m, int n, bool b
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 // D (+)= A B^T with both operands in shared memory, or A in tensor memory.
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+// Operands come as the low words of their descriptors, with one high word.
+template <uint32_t kHi>
+__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(kHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+template <uint32_t kHi>
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(kHi)
       : "memory");
 }
 // One arrival on `bar` when every MMA that this thread issued so far is done.
