@@ -45,6 +45,16 @@ static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 512, "65536 registers
 constexpr float kRaise = 8.f;      // log2 of how far weights may exceed 1
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+// A unit's fixed cost in tiles: its queries' way in and its outputs' way out.
+constexpr int kUnitCost = 3;
+
+struct TilesParams : AttnParams {
+  FastDiv by_group;
+  int unit_query, unit_rem;  // 256 rows are unit_query queries and unit_rem rows
+  int box_keys;              // keys per tensor-map box of the cache, 0: through registers
+  int box_queries;           // queries per 128 rows for the tensor map of q, 0: registers
+};
+
 struct TilesSpace {
   int4* joins;       // [workers]: the split unit that a worker's boundary is the first to cut
   int32_t* failed;   // [workers]: a bounded wait gave up
@@ -68,28 +78,50 @@ struct TilesShape {
   static constexpr int kPieces = kKeys * kRowChunks / kLoaders / kPieceChunks;
 };
 
-// A unit of one batch row: its rows and tiles.
+// A unit of one batch row: its rows and tiles.  The first query of the next
+// unit is carried along as quotient and remainder by the group, so that a step
+// needs no division.
 struct Unit {
   int first, rows;    // first row, rows of it (<= 256)
+  int query, rem;     // first row = query * group + rem
   int tile, tiles;    // first tile, number (at least 1)
 };
-__device__ __forceinline__ Unit unit_of(const AttnParams& p, const AttnRow& r, int rt, FastDiv by_group) {
-  Unit u;
-  u.first = rt * kUnitRows;
+__device__ __forceinline__ void unit_tiles(Unit& u, const TilesParams& p, const AttnRow& r) {
   u.rows = min(kUnitRows, r.n * p.group - u.first);
-  const int i0 = div_any(u.first, by_group), i1 = div_any(u.first + u.rows - 1, by_group);
-  const int hi = max(0, r.len - r.n + i1 + 1), lo = seen_lo(p, r.len - r.n + i0);
+  // The last row is at most rem + rows - 1 rows past the first one's query.
+  const int before = r.len - r.n;
+  int last = r.n - 1;
+  if (u.rows == kUnitRows) {
+    last = u.query + p.unit_query;
+    if (u.rem + p.unit_rem > p.group) ++last;
+    if (u.rem + p.unit_rem == 0) --last;
+  }
+  const int hi = max(0, before + last + 1), lo = seen_lo(p, before + u.query);
   u.tile = lo / kKeys;
   u.tiles = max(1, (hi + kKeys - 1) / kKeys - u.tile);
+}
+__device__ __forceinline__ Unit first_unit(const TilesParams& p, const AttnRow& r) {
+  Unit u{0, 0, 0, 0, 0, 0};
+  unit_tiles(u, p, r);
   return u;
 }
-__device__ __forceinline__ int units_of(const AttnParams& p, const AttnRow& r) {
-  return (r.n * p.group + kUnitRows - 1) / kUnitRows;
+__device__ __forceinline__ bool next_unit(Unit& u, const TilesParams& p, const AttnRow& r) {
+  u.first += kUnitRows;
+  if (u.first >= r.n * p.group) return false;
+  u.query += p.unit_query;
+  u.rem += p.unit_rem;
+  if (u.rem >= p.group) {
+    u.rem -= p.group;
+    ++u.query;
+  }
+  unit_tiles(u, p, r);
+  return true;
 }
-__device__ __forceinline__ uint32_t row_cost(const AttnParams& p, const AttnRow& r, FastDiv by_group) {
+__device__ __forceinline__ uint32_t row_cost(const TilesParams& p, const AttnRow& r) {
   uint32_t n = 0;
-  const int units = units_of(p, r);
-  for (int rt = 0; rt < units; ++rt) n += unit_of(p, r, rt, by_group).tiles + 1;
+  Unit u = first_unit(p, r);
+  do n += u.tiles + kUnitCost;
+  while (next_unit(u, p, r));
   return n * p.kv_heads;
 }
 
@@ -103,12 +135,12 @@ struct Walk {
   int k0, k1;         // this run's tiles of the unit (relative)
 
   __device__ __forceinline__ void clip(uint32_t c0) {
-    const int64_t a = static_cast<int64_t>(c0) - u0 - 1, e = static_cast<int64_t>(c1) - u0 - 1;
+    const int64_t a = static_cast<int64_t>(c0) - u0 - kUnitCost, e = static_cast<int64_t>(c1) - u0 - kUnitCost;
     k0 = a > 0 ? static_cast<int>(a) : 0;
     k1 = e < unit.tiles ? static_cast<int>(e) : unit.tiles;
   }
   __device__ __forceinline__ bool seek(uint32_t c0, uint32_t end, const uint32_t* prefix,
-                                       const AttnParams& p, FastDiv by_group) {
+                                       const TilesParams& p) {
     c1 = end;
     if (c0 >= c1) return false;
     int a = 0, n = p.batch;  // the largest b with prefix[b] <= c0
@@ -123,31 +155,33 @@ struct Walk {
     row = attn_row(p, b);
     u0 = prefix[b];
     rt = 0;
+    unit = first_unit(p, row);
     for (;;) {
-      unit = unit_of(p, row, rt, by_group);
-      const uint32_t all = static_cast<uint32_t>(unit.tiles + 1) * p.kv_heads;
+      const uint32_t all = static_cast<uint32_t>(unit.tiles + kUnitCost) * p.kv_heads;
       if (c0 - u0 < all) break;
       u0 += all;
       ++rt;
+      next_unit(unit, p, row);
     }
-    g = (c0 - u0) / (unit.tiles + 1);
-    u0 += static_cast<uint32_t>(g) * (unit.tiles + 1);
+    g = (c0 - u0) / (unit.tiles + kUnitCost);
+    u0 += static_cast<uint32_t>(g) * (unit.tiles + kUnitCost);
     clip(c0);
-    return k1 > k0 || next(prefix, p, by_group);
+    return k1 > k0 || next(prefix, p);
   }
   // The next unit with tiles in the run.
-  __device__ __forceinline__ bool next(const uint32_t* prefix, const AttnParams& p, FastDiv by_group) {
-    u0 += unit.tiles + 1;
-    if (u0 + 1 >= c1) return false;
+  __device__ __forceinline__ bool next(const uint32_t* prefix, const TilesParams& p) {
+    u0 += unit.tiles + kUnitCost;
+    if (u0 + kUnitCost >= c1) return false;
     if (++g == p.kv_heads) {
       g = 0;
-      if (++rt == units_of(p, row)) {
+      ++rt;
+      if (!next_unit(unit, p, row)) {
         rt = 0;
         do ++b;
         while (prefix[b + 1] == prefix[b]);
         row = attn_row(p, b);
+        unit = first_unit(p, row);
       }
-      unit = unit_of(p, row, rt, by_group);
     }
     clip(u0);
     return true;
@@ -264,7 +298,7 @@ __device__ __forceinline__ bool loaders_all(bool ok) {
 template <int kIn, bool kFp8, int D>
 struct Loader {
   using S = TilesShape<kIn, kFp8, D>;
-  const AttnParams& p;
+  const TilesParams& p;
   Shared& sh;
   uint32_t q_at, ring;
   int tid;
@@ -312,7 +346,7 @@ struct Loader {
                             : -1;
     loaders_sync();
   }
-  __device__ __forceinline__ void load_q(const Walk& w, FastDiv by_group, int buf) {
+  __device__ __forceinline__ void load_q(const Walk& w, int buf) {
     const int halves = w.unit.rows > kHalf ? 2 : 1;
     if constexpr (kFp8 && kIn == HS_DT_BF16) {
       // A thread per row: a power of two brings its largest magnitude to
@@ -321,7 +355,7 @@ struct Loader {
         const uint32_t at = q_at + (m / kHalf) * S::kStage;
         const int r = m % kHalf;
         const bool live = m < w.unit.rows;
-        const int i = div_any(w.unit.first + m, by_group), hg = w.unit.first + m - i * p.group;
+        const int i = div_any(w.unit.first + m, p.by_group), hg = w.unit.first + m - i * p.group;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + static_cast<int64_t>(w.row.q0 + i) * p.q_token +
             static_cast<int64_t>(w.g * p.group + hg) * p.q_head);
@@ -358,7 +392,7 @@ struct Loader {
           const int c = c0 + i * kLoaders + tid, m = c / kC;
           x[i] = make_uint4(0, 0, 0, 0);
           if (m < w.unit.rows) {
-            const int tok = div_any(w.unit.first + m, by_group), hg = w.unit.first + m - tok * p.group;
+            const int tok = div_any(w.unit.first + m, p.by_group), hg = w.unit.first + m - tok * p.group;
             x[i] = __ldg(reinterpret_cast<const uint4*>(
                              p.q + static_cast<int64_t>(w.row.q0 + tok) * p.q_token +
                              static_cast<int64_t>(w.g * p.group + hg) * p.q_head) + c % kC);
@@ -377,9 +411,10 @@ struct Loader {
 
 template <int kIn, bool kFp8, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tiles_kernel(const AttnParams p, const TilesSpace ws, const FastDiv by_group,
+    attn_tiles_kernel(const TilesParams p, const TilesSpace ws,
                       const __grid_constant__ CUtensorMap k_map,
-                      const __grid_constant__ CUtensorMap v_map, const int box_keys) {
+                      const __grid_constant__ CUtensorMap v_map,
+                      const __grid_constant__ CUtensorMap q_map) {
   using S = TilesShape<kIn, kFp8, D>;
   constexpr bool kBf16 = kIn == HS_DT_BF16 && !kFp8;  // type of the products
   // fp16 weights reach 2^(6 + 8) and keep what is 2^-30 of the reference.
@@ -408,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.dead = 0;
   }
   if (warp == 12) tmem_alloc(&sh.tmem, 512);
-  const uint32_t total = attn_prefix(p, prefix, [&](const AttnRow& r) { return row_cost(p, r, by_group); });
+  const uint32_t total = attn_prefix(p, prefix, [&](const AttnRow& r) { return row_cost(p, r); });
   grid_dep_launch_dependents();
   tc_fence_before();
   __syncthreads();
@@ -429,18 +464,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float ks = p.scale[0] ? __ldg(p.scale[0]) : 1.0f, vs = p.scale[1] ? __ldg(p.scale[1]) : 1.0f;
     uint32_t s_ph = 0, o_ph = 0, u_n = 0;
     Walk w;
-    bool more = w.seek(c0, c1, prefix, p, by_group);
-    for (; more; more = w.next(prefix, p, by_group), ++u_n) {
+    bool more = w.seek(c0, c1, prefix, p);
+    for (; more; more = w.next(prefix, p), ++u_n) {
       const int m = half * kHalf + r;  // row of the unit
       if (half == 1 && w.unit.rows <= kHalf) continue;
       const bool live = m < w.unit.rows;
-      const int i = div_any(w.unit.first + m, by_group);
+      const int i = div_any(w.unit.first + m, p.by_group);
       const int pos = w.row.len - w.row.n + i;
       // Rows past the unit's end are computed like the others and not written.
       const int vis_hi = live ? pos + 1 : INT_MAX, vis_lo = live ? seen_lo(p, pos) : 0;
       // Keys that every row of this warp's half sees need no mask.
-      const int i_first = div_any(w.unit.first + half * kHalf, by_group);
-      const int i_last = div_any(w.unit.first + min(w.unit.rows, (half + 1) * kHalf) - 1, by_group);
+      const int i_first = div_any(w.unit.first + half * kHalf, p.by_group);
+      const int i_last = div_any(w.unit.first + min(w.unit.rows, (half + 1) * kHalf) - 1, p.by_group);
       const int all_hi = w.row.len - w.row.n + i_first + 1;
       const int all_lo = seen_lo(p, w.row.len - w.row.n + i_last);
       float sc = p.softmax_scale * kLog2e * ks;
@@ -533,28 +568,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* dst = p.out + tok * p.out_token + head * p.out_head;
       float* part = ws.slots + static_cast<int64_t>(2 * me + (w.k0 == 0 ? 1 : 0)) * tiles_slot_floats(D);
       const float f = whole ? inv * vs : inv;
-#pragma unroll 2
-      for (int q = 0; q < D / 16; ++q) {
-        uint32_t o[16];
-        tmem_ld16(o, o_at + q * 16);
+#pragma unroll 1
+      for (int q = 0; q < D / 64; ++q) {
+        uint32_t o[2][32];
+        tmem_ld32(o[0], o_at + q * 64);
+        tmem_ld32(o[1], o_at + q * 64 + 32);
         tmem_wait_ld();
-        tmem_pin(o);
+        tmem_pin(o[0]);
+        tmem_pin(o[1]);
         if (live && whole) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 8; ++c) {
             uint32_t x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              x[e] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[c * 8 + e * 2]) * f,
-                                               __uint_as_float(o[c * 8 + e * 2 + 1]) * f);
-            *reinterpret_cast<uint4*>(dst + q * 32 + c * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+              x[e] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[c / 4][(c % 4) * 8 + e * 2]) * f,
+                                               __uint_as_float(o[c / 4][(c % 4) * 8 + e * 2 + 1]) * f);
+            *reinterpret_cast<uint4*>(dst + q * 128 + c * 16) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         } else if (live) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<float4*>(part + m * D + q * 16 + c * 4) =
-                make_float4(__uint_as_float(o[c * 4]) * f, __uint_as_float(o[c * 4 + 1]) * f,
-                            __uint_as_float(o[c * 4 + 2]) * f, __uint_as_float(o[c * 4 + 3]) * f);
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t* x = o[c / 8] + (c % 8) * 4;
+            *reinterpret_cast<float4*>(part + m * D + q * 64 + c * 4) =
+                make_float4(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f,
+                            __uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f);
+          }
         }
       }
       if (live && !whole) part[kUnitRows * D + m] = lse;
@@ -579,73 +618,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     Walk w;
-    bool more = w.seek(c0, c1, prefix, p, by_group);
+    bool more = w.seek(c0, c1, prefix, p);
     if (lt == 0) {
       // Where this run's start cuts a unit, and is the first to do so, the unit's
       // parts are joined in this worker's name.
       int4 j = make_int4(-1, 0, 0, 0);
-      if (more && w.k0 > 0 && split_worker(w.u0 + 1, total, workers) + 1 == me)
-        j = make_int4(w.b, w.g, w.rt, static_cast<int>(split_worker(w.u0 + w.unit.tiles, total, workers)));
+      if (more && w.k0 > 0 && split_worker(w.u0 + kUnitCost, total, workers) + 1 == me)
+        j = make_int4(w.b, w.g, w.rt, static_cast<int>(split_worker(w.u0 + kUnitCost + w.unit.tiles - 1, total, workers)));
       ws.joins[me] = j;
     }
-    for (; more && ok; more = w.next(prefix, p, by_group), ++u_n) {
+    // A K (v = 0) or V tile by tensor-map boxes, a page or part of one each.
+    auto boxes = [&](int tile, int v) {
+      uint64_t* bar = &sh.kv_full[kv.stage];
+      if (lt == 0)
+        mbar_arrive_expect_tx(bar, S::kStage);
+      else
+        mbar_arrive(bar);
+      if (lt < kKeys / p.box_keys) {
+        const uint32_t dst = ring + kv.stage * S::kStage + lt * p.box_keys * 128;
+        const int j = tile * kKeys + lt * p.box_keys;
+        // A box that no query sees, or outside the pool, is past the last page:
+        // it reads zeros.
+        int page = static_cast<int>(p.num_pages), in_page = 0;
+        if (j + p.box_keys > w.row.lo && j < w.row.hi) {
+          const uint32_t c = div_any(static_cast<uint32_t>(j), p.div_page);
+          const int32_t e = __ldg(p.table + w.row.state * p.table_stride + c);
+          if (e >= 0 && e < p.num_pages) {
+            page = e;
+            in_page = j - static_cast<int>(c * p.page_size);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < S::kPanels; ++x)
+          tensor_load_4d(dst + x * S::kPanel, v ? &v_map : &k_map, x * 64, w.g, in_page, page, bar);
+      }
+      kv.step();
+      ++issued;
+    };
+    auto queries = [&]() {
       ok = loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead));
-      if (!ok) break;
-      ld.load_q(w, by_group, u_n & 1);
+      if (!ok) return;
       if (lt == 0) sh.unit[u_n & 1] = make_int2(w.unit.rows, w.k1 - w.k0);
+      if (!(kFp8 && kIn == HS_DT_BF16) && p.box_queries > 0) {
+        // 128 rows are box_queries tokens of the kv head's query heads.  Rows
+        // past the request's last query bring the next one's, and are not written.
+        const int halves = w.unit.rows > kHalf ? 2 : 1;
+        if (lt == 0) {
+          mbar_arrive_expect_tx(&sh.q_full, halves * S::kStage);
+          for (int h = 0; h < halves; ++h)
+#pragma unroll
+            for (int x = 0; x < S::kPanels; ++x)
+              tensor_load_3d(q_at + h * S::kStage + x * S::kPanel, &q_map, x * 64, w.g * p.group,
+                             w.row.q0 + w.unit.query + h * p.box_queries, &sh.q_full);
+        } else {
+          mbar_arrive(&sh.q_full);
+        }
+        return;
+      }
+      ld.load_q(w, u_n & 1);
       fence_proxy_async_smem();
       mbar_arrive(&sh.q_full);
+    };
+    for (; more && ok; more = w.next(prefix, p), ++u_n) {
       const int64_t head = w.g * p.c_head;
-      if (!kFp8 && box_keys > 0) {
-        for (int k = w.k0; k < w.k1 && ok; ++k) {
-          const int j0 = (w.unit.tile + k) * kKeys;
-          const bool edge = j0 < w.row.lo || j0 + kKeys > w.row.hi;
-#pragma unroll 1
-          for (int v = 0; v < 2 && ok; ++v) {
-            ok = claim();
+      if (!kFp8 && p.box_keys > 0) {
+        // The first K tile does not wait for the queries' buffer.
+        for (int k = w.k0; k < w.k1; ++k) {
+          const int tile = w.unit.tile + k;
+          if (!(ok = claim())) break;
+          boxes(tile, 0);
+          if (k == w.k0) {
+            queries();
             if (!ok) break;
-            if (v == 1 && edge) {
-              ld.look_up(w.row, w.unit.tile + k, 0);
+          }
+          if (!(ok = claim())) break;
+          if (tile * kKeys < w.row.lo || (tile + 1) * kKeys > w.row.hi) {
+            // Positions that no query sees: their V rows must be zeros.
+            ld.look_up(w.row, tile, 0);
 #pragma unroll 1
-              for (int x = 0; x < S::kPieces; ++x) {
-                uint4 r[S::kPieceChunks];
-                ld.fetch(r, 0, x, true, head);
-                ld.store(r, kv.stage, x);
-              }
-              loaders_sync();  // offs is written again
-              publish();
-              continue;
+            for (int x = 0; x < S::kPieces; ++x) {
+              uint4 r[S::kPieceChunks];
+              ld.fetch(r, 0, x, true, head);
+              ld.store(r, kv.stage, x);
             }
-            uint64_t* bar = &sh.kv_full[kv.stage];
-            const uint32_t dst = ring + kv.stage * S::kStage;
-            if (lt == 0)
-              mbar_arrive_expect_tx(bar, S::kStage);
-            else
-              mbar_arrive(bar);
-            if (lt < kKeys / box_keys) {
-              const int j = j0 + lt * box_keys;
-              // A box that no query sees, or outside the pool, is past the last
-              // page: it reads zeros.
-              int page = static_cast<int>(p.num_pages), in_page = 0;
-              if (j + box_keys > w.row.lo && j < w.row.hi) {
-                const uint32_t c = div_any(static_cast<uint32_t>(j), p.div_page);
-                const int32_t e = __ldg(p.table + w.row.state * p.table_stride + c);
-                if (e >= 0 && e < p.num_pages) {
-                  page = e;
-                  in_page = j - static_cast<int>(c * p.page_size);
-                }
-              }
-#pragma unroll
-              for (int x = 0; x < S::kPanels; ++x)
-                tensor_load_4d(dst + x * S::kPanel + lt * box_keys * 128, v ? &v_map : &k_map, x * 64,
-                               w.g, in_page, page, bar);
-            }
-            kv.step();
-            ++issued;
+            loaders_sync();  // offs is written again
+            publish();
+          } else {
+            boxes(tile, 1);
           }
         }
       } else {
         // Pieces through registers, two in flight: K and V of each tile in turn.
+        queries();
+        if (!ok) break;
         constexpr int kPer = 2 * S::kPieces;
         const int pieces = (w.k1 - w.k0) * kPer;
         uint4 ra[S::kPieceChunks], rb[S::kPieceChunks];
@@ -683,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int no = 0;
       for (uint32_t n = issued > S::kStages ? issued - S::kStages : 0; n < issued; ++n)
         wait_for(&sh.kv_full[n % S::kStages], (n / S::kStages) & 1, &no);
+      wait_for(&sh.q_full, u_n & 1, &no);
     }
   } else {
     // ---------------------------------------------------------------- MMA
@@ -783,7 +849,7 @@ constexpr int kTilesJoinThreads = 256, kJoinRows = 32;
 // the workers write the status words.
 template <int kIn, int D>
 __global__ void __launch_bounds__(kTilesJoinThreads)
-    attn_tiles_join_kernel(const AttnParams p, const TilesSpace ws) {
+    attn_tiles_join_kernel(const TilesParams p, const TilesSpace ws) {
   constexpr int kLanes = D / 4, kAtOnce = kTilesJoinThreads / kLanes;
   constexpr int kBlocks = kUnitRows / kJoinRows;
   grid_dep_wait();  // in every block: this grid must not be done before the first kernel is
@@ -834,9 +900,9 @@ __global__ void __launch_bounds__(kTilesJoinThreads)
 }
 
 struct TilesKernels {
-  void (*main)(const AttnParams, const TilesSpace, const FastDiv, const CUtensorMap,
-               const CUtensorMap, int);
-  void (*join)(const AttnParams, const TilesSpace);
+  void (*main)(const TilesParams, const TilesSpace, const CUtensorMap, const CUtensorMap,
+               const CUtensorMap);
+  void (*join)(const TilesParams, const TilesSpace);
   int smem;
 };
 template <int kIn, bool kFp8, int D>
@@ -906,6 +972,20 @@ bool encode_cache(CUtensorMap* map, const AttnParams& p, int which, bool bf16, i
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q as [tokens][heads][dim], read in boxes of the query heads of one kv head of
+// as many tokens as make 128 rows.
+bool encode_queries(CUtensorMap* map, const AttnParams& p, bool bf16) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.heads),
+                              static_cast<cuuint64_t>(p.n_tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.q_head), static_cast<cuuint64_t>(p.q_token)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(kHalf / p.group)};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<unsigned char*>(p.q), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int64_t kTilesHead = 64 * 1024;  // joins and failure words, up to 2048 workers
 
 }  // namespace
@@ -926,21 +1006,28 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   ws.failed = reinterpret_cast<int32_t*>(at + 2048 * sizeof(int4));
   ws.slots = reinterpret_cast<float*>(at + kTilesHead);
   ws.workers = static_cast<uint32_t>(dev.sm_count);
-  CUtensorMap maps[2] = {};
-  int box = 0;
+  TilesParams tp;
+  static_cast<AttnParams&>(tp) = p;
+  const uint32_t group = static_cast<uint32_t>(p.group);
+  tp.by_group = FastDiv{fastdiv_magic(group), group};
+  tp.unit_query = kUnitRows / p.group;
+  tp.unit_rem = kUnitRows % p.group;
+  tp.box_keys = tp.box_queries = 0;
+  CUtensorMap maps[3] = {};
   if (!fp8) {
     if (p.page_size % kKeys == 0)
-      box = kKeys;
+      tp.box_keys = kKeys;
     else if (p.page_size % 8 == 0 && kKeys % p.page_size == 0)
-      box = static_cast<int>(p.page_size);
-    if (p.num_pages < 1 || p.num_pages >= INT32_MAX) box = 0;
+      tp.box_keys = static_cast<int>(p.page_size);
+    if (p.num_pages < 1 || p.num_pages >= INT32_MAX) tp.box_keys = 0;
     // Strides that a tensor map cannot hold go through registers.
-    for (int i = 0; box > 0 && i < 2; ++i)
-      if (!encode_cache(&maps[i], p, i, in_dtype == HS_DT_BF16, box)) box = 0;
+    for (int i = 0; tp.box_keys > 0 && i < 2; ++i)
+      if (!encode_cache(&maps[i], p, i, in_dtype == HS_DT_BF16, tp.box_keys)) tp.box_keys = 0;
   }
-  const uint32_t group = static_cast<uint32_t>(p.group);
-  k.main<<<dev.sm_count, kThreads, k.smem + (p.batch + 1) * 4, stream>>>(
-      p, ws, FastDiv{fastdiv_magic(group), group}, maps[0], maps[1], box);
+  if (kHalf % p.group == 0 && !(fp8 && in_dtype == HS_DT_BF16) &&
+      encode_queries(&maps[2], p, in_dtype == HS_DT_BF16))
+    tp.box_queries = kHalf / p.group;
+  k.main<<<dev.sm_count, kThreads, k.smem + (p.batch + 1) * 4, stream>>>(tp, ws, maps[0], maps[1], maps[2]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention launch: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
@@ -952,7 +1039,7 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k.join, p, ws);
+  e = cudaLaunchKernelEx(&cfg, k.join, tp, ws);
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention join: %s", cudaGetErrorString(e));
   return HS_OK;
 }

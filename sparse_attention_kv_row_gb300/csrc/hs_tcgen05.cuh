@@ -139,6 +139,15 @@ __device__ __forceinline__ void tensor_load_4d(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
+__device__ __forceinline__ void tensor_load_3d(uint32_t dst, const CUtensorMap* map, int x0, int x1,
+                                               int x2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x0), "r"(x1), "r"(x2)
+      : "memory");
+}
+
 template <uint32_t kRegs>
 __device__ __forceinline__ void regs_grow() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
