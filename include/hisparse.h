@@ -597,7 +597,7 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  * with HS_DT_E4M3 bf16 queries are multiplied by a power of two per row and
  * taken as fp16.  Results do not depend on what else is in the batch, except
  * through the order of fp32 sums.
- * Limits: head_dim <= 512, num_heads a multiple of num_kv_heads, batch <= 4096,
+ * Limits: head_dim <= 512, num_heads a multiple of num_kv_heads, batch <= 2048,
  * L <= INT32_MAX (else HS_ERR_UNSUPPORTED, or HS_ST_BAD_STATE for L).
  */
 typedef struct hs_paged_attention_args {

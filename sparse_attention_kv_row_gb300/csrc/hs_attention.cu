@@ -154,7 +154,9 @@ AttnForm attn_form(const hs_paged_attention_args* a) {
   if (a->in_dtype == HS_DT_F32 || (a->head_dim != 64 && a->head_dim != 128) || rows == 0 ||
       a->n_tokens == 0 || rows * a->num_kv_heads > INT32_MAX / 2 / a->batch)  // blocks of the join
     return AttnForm::kGeneral;
-  return rows <= kSplitRows ? AttnForm::kSplit : AttnForm::kTiles;
+  if (rows <= kSplitRows) return AttnForm::kSplit;
+  // A half of 128 rows holds whole queries.
+  return a->num_heads / a->num_kv_heads <= 128 ? AttnForm::kTiles : AttnForm::kGeneral;
 }
 
 // Whether every address that the tensor-core kernels form allows 16-byte accesses.

@@ -13,7 +13,7 @@
 
 namespace hs {
 
-constexpr int kAttnMaxBatch = 4096;
+constexpr int kAttnMaxBatch = 2048;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -1,14 +1,15 @@
 // hs_attention_tiles.cu -- paged attention for chunks of many queries per
 // request (prompts, chunked prefill, mixed batches), for sm_103a.
 //
-// A unit is 256 query rows (new tokens x query heads of one kv head) of one
-// request against the keys they see, in tiles of 128 keys:
+// A unit is up to 256 query rows (new tokens x query heads of one kv head, whole
+// tokens in each half of 128) of one request against the keys they see, in tiles of 128 keys:
 //   S = Q K^T (128 x 128 x D),  P = 2^(S c - m),  O += P V (128 x D x 128),
 // twice, once for each half of the rows.  4 D operations per (row, key) make
 // the tensor cores the bound; the softmax of one half runs while the tensor
 // cores work on the other.  S, P and O stay in tensor memory: S0 S1 (128 columns
 // each, P over its S) and O0 O1 fill it.  Roles: two warpgroups of softmax (a
-// thread per row), one that loads, one warp that issues the MMAs.
+// thread per row), one that loads or widens, one warp that issues the MMAs and
+// one that issues the loads.
 //
 // The running maximum m is only raised, and O rescaled, when a row's new
 // maximum is more than 2^8 above the old one: a larger weight is as good in the
@@ -20,10 +21,11 @@
 // kernel joins them.
 //
 // K and V tiles come by tensor-map loads, a box per page, where pages are a
-// power-of-two part or a multiple of 128 keys and the cache is 16-bit.  An FP8
-// cache is widened to fp16 on the way through registers, exactly; so are other
-// page sizes, and a V tile that holds positions no query sees, whose rows must
-// be zeros because 0 times what they hold may not be 0.
+// power-of-two part or a multiple of 128 keys: one warp issues them, straight
+// into the ring for a 16-bit cache, or as bytes that a warpgroup widens to fp16
+// (exactly) for an FP8 one.  Other page sizes go through registers.  A V tile
+// with positions that no query sees gets zero rows there: 0 times what they hold
+// may not be 0.
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -50,9 +52,9 @@ constexpr int kUnitCost = 3;
 
 struct TilesParams : AttnParams {
   FastDiv by_group;
-  int unit_query, unit_rem;  // 256 rows are unit_query queries and unit_rem rows
-  int box_keys;              // keys per tensor-map box of the cache, 0: through registers
-  int box_queries;           // queries per 128 rows for the tensor map of q, 0: registers
+  int half_queries;  // whole queries in 128 rows
+  int box_keys;      // keys per tensor-map box of the cache, 0: through registers
+  bool q_box;        // the queries come by tensor map too
 };
 
 struct TilesSpace {
@@ -69,8 +71,11 @@ struct TilesShape {
   static constexpr int kPanel = kKeys * 128;             // bytes
   static constexpr int kStage = kPanels * kPanel;        // one K or V tile, 16-bit
   static constexpr int kQ = 2 * kStage;                  // both halves
-  static constexpr int kStages = D == 128 ? 4 : 6;
-  static constexpr int kRing = kQ + kStages * kStage;
+  static constexpr int kStages = D == 128 ? (kFp8 ? 3 : 4) : (kFp8 ? 5 : 6);
+  static constexpr int kRawTiles = kFp8 ? (D == 128 ? 2 : 4) : 0;  // FP8 tiles to be widened
+  static constexpr int kRaw = kKeys * D;
+  static constexpr int kRing = kQ + kStages * kStage + kRawTiles * kRaw;
+  static constexpr int kOut = 8 * 32 * 64;               // outputs on their way: 64 bytes of each row
   static constexpr int kRowBytes = kFp8 ? D : 2 * D;     // a cache row
   static constexpr int kRowChunks = kRowBytes / 16;
   // A piece is what the loaders hold in registers at once: up to 8 chunks each.
@@ -78,43 +83,28 @@ struct TilesShape {
   static constexpr int kPieces = kKeys * kRowChunks / kLoaders / kPieceChunks;
 };
 
-// A unit of one batch row: its rows and tiles.  The first query of the next
-// unit is carried along as quotient and remainder by the group, so that a step
-// needs no division.
+// A unit of one batch row: its queries and tiles.
 struct Unit {
-  int first, rows;    // first row, rows of it (<= 256)
-  int query, rem;     // first row = query * group + rem
-  int tile, tiles;    // first tile, number (at least 1)
+  int query, queries;  // first query, number (at most two halves')
+  int tile, tiles;     // first tile, number (at least 1)
 };
-__device__ __forceinline__ void unit_tiles(Unit& u, const TilesParams& p, const AttnRow& r) {
-  u.rows = min(kUnitRows, r.n * p.group - u.first);
-  // The last row is at most rem + rows - 1 rows past the first one's query.
-  const int before = r.len - r.n;
-  int last = r.n - 1;
-  if (u.rows == kUnitRows) {
-    last = u.query + p.unit_query;
-    if (u.rem + p.unit_rem > p.group) ++last;
-    if (u.rem + p.unit_rem == 0) --last;
-  }
-  const int hi = max(0, before + last + 1), lo = seen_lo(p, before + u.query);
+__device__ __forceinline__ void unit_at(Unit& u, int query, const TilesParams& p, const AttnRow& r) {
+  u.query = query;
+  u.queries = min(2 * p.half_queries, r.n - query);
+  const int pos = r.len - r.n + query;  // of the first query
+  const int hi = max(0, pos + u.queries), lo = seen_lo(p, pos);
   u.tile = lo / kKeys;
   u.tiles = max(1, (hi + kKeys - 1) / kKeys - u.tile);
 }
 __device__ __forceinline__ Unit first_unit(const TilesParams& p, const AttnRow& r) {
-  Unit u{0, 0, 0, 0, 0, 0};
-  unit_tiles(u, p, r);
+  Unit u;
+  unit_at(u, 0, p, r);
   return u;
 }
 __device__ __forceinline__ bool next_unit(Unit& u, const TilesParams& p, const AttnRow& r) {
-  u.first += kUnitRows;
-  if (u.first >= r.n * p.group) return false;
-  u.query += p.unit_query;
-  u.rem += p.unit_rem;
-  if (u.rem >= p.group) {
-    u.rem -= p.group;
-    ++u.query;
-  }
-  unit_tiles(u, p, r);
+  const int query = u.query + 2 * p.half_queries;
+  if (query >= r.n) return false;
+  unit_at(u, query, p, r);
   return true;
 }
 __device__ __forceinline__ uint32_t row_cost(const TilesParams& p, const AttnRow& r) {
@@ -129,7 +119,7 @@ __device__ __forceinline__ uint32_t row_cost(const TilesParams& p, const AttnRow
 struct Walk {
   uint32_t c1;        // end of the run
   uint32_t u0;        // cost index of the current unit
-  int b, rt, g;
+  int b, g;
   AttnRow row;
   Unit unit;
   int k0, k1;         // this run's tiles of the unit (relative)
@@ -154,13 +144,11 @@ struct Walk {
     b = a;
     row = attn_row(p, b);
     u0 = prefix[b];
-    rt = 0;
     unit = first_unit(p, row);
     for (;;) {
       const uint32_t all = static_cast<uint32_t>(unit.tiles + kUnitCost) * p.kv_heads;
       if (c0 - u0 < all) break;
       u0 += all;
-      ++rt;
       next_unit(unit, p, row);
     }
     g = (c0 - u0) / (unit.tiles + kUnitCost);
@@ -174,9 +162,7 @@ struct Walk {
     if (u0 + kUnitCost >= c1) return false;
     if (++g == p.kv_heads) {
       g = 0;
-      ++rt;
       if (!next_unit(unit, p, row)) {
-        rt = 0;
         do ++b;
         while (prefix[b + 1] == prefix[b]);
         row = attn_row(p, b);
@@ -189,11 +175,11 @@ struct Walk {
 };
 
 struct Shared {
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
-  uint64_t kv_full[6], kv_empty[6];
+  uint64_t q_full, q_empty, s_full[2], p_half[2], p_full[2], o_full[2], drain, edge;
+  uint64_t kv_full[6], kv_empty[6], raw_full[4], raw_empty[4];
   uint32_t tmem;
   volatile int dead;
-  int2 unit[2];  // for the MMA warp: rows and tiles of a unit, no tiles at the end
+  int2 unit[2];  // for the MMA warp: queries and tiles of a unit, no tiles at the end
   float q_factor[2][kUnitRows];
   int64_t offs[2][kKeys];
 };
@@ -260,6 +246,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // A place in the ring of K and V tiles.
 template <int kStages>
 struct RingAt {
@@ -280,6 +272,14 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
                : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // The same, and whether `ok` holds for every loader: they give up together.
@@ -322,16 +322,7 @@ struct Loader {
       const int c = (piece * S::kPieceChunks + i) * kLoaders + tid;
       const int row = c / S::kRowChunks, ch = c % S::kRowChunks;
       if constexpr (kFp8) {
-        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[2 * j] = e4m3_to_f16(w[j] & 0xFFFF);
-          h[2 * j + 1] = e4m3_to_f16(w[j] >> 16);
-        }
-        const uint32_t panel = at + (ch / 4) * S::kPanel;
-        st_shared_v4(panel + in_panel(row, (ch % 4) * 2), make_uint4(h[0], h[1], h[2], h[3]));
-        st_shared_v4(panel + in_panel(row, (ch % 4) * 2 + 1), make_uint4(h[4], h[5], h[6], h[7]));
+        widen(at, row, ch, r[i]);
       } else {
         st_shared_v4(at + (ch / 8) * S::kPanel + in_panel(row, ch % 8), r[i]);
       }
@@ -346,66 +337,64 @@ struct Loader {
                             : -1;
     loaders_sync();
   }
+  // The unit's queries, zeros past its last; bf16 ones times a power of two a
+  // row, as fp16, where the cache is FP8.
   __device__ __forceinline__ void load_q(const Walk& w, int buf) {
-    const int halves = w.unit.rows > kHalf ? 2 : 1;
-    if constexpr (kFp8 && kIn == HS_DT_BF16) {
-      // A thread per row: a power of two brings its largest magnitude to
-      // [2^8, 2^9) and the row to fp16 (see rows_to_f16).
-      for (int m = tid; m < halves * kHalf; m += kLoaders) {
-        const uint32_t at = q_at + (m / kHalf) * S::kStage;
-        const int r = m % kHalf;
-        const bool live = m < w.unit.rows;
-        const int i = div_any(w.unit.first + m, p.by_group), hg = w.unit.first + m - i * p.group;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + static_cast<int64_t>(w.row.q0 + i) * p.q_token +
-            static_cast<int64_t>(w.g * p.group + hg) * p.q_head);
-        uint32_t top = 0;
-        if (live) {
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = __ldg(src + c);
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+    const int halves = w.unit.queries > p.half_queries ? 2 : 1;
+    constexpr int kC = D / 8, kBatch = 8;
+#pragma unroll 1
+    for (int c0 = 0; c0 < halves * kHalf * kC; c0 += kBatch * kLoaders) {
+      uint4 x[kBatch];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
-          }
-        }
-        const float up = f16_factor(top);
-        sh.q_factor[buf][m] = 1.0f / up;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (live) x = __ldg(src + c);
-          uint32_t v[4] = {x.x, x.y, x.z, x.w};
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = c0 + i * kLoaders + tid, m = c / kC;
+        const int in = div_any(m % kHalf, p.by_group), tok = (m / kHalf) * p.half_queries + in;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (in < p.half_queries && tok < w.unit.queries)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(
+                           p.q + static_cast<int64_t>(w.row.q0 + w.unit.query + tok) * p.q_token +
+                           static_cast<int64_t>(w.g * p.group + m % kHalf - in * p.group) * p.q_head) + c % kC);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = c0 + i * kLoaders + tid, m = c / kC, ch = c % kC;
+        if constexpr (kFp8 && kIn == HS_DT_BF16) {
+          // A row is kC neighbouring lanes'.
+          uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, top = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
+#pragma unroll
+          for (int j = kC / 2; j > 0; j >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, j));
+          const float up = f16_factor(top);
+          if (ch == 0) sh.q_factor[buf][m] = 1.0f / up;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             v[j] = pack2t<false>(__uint_as_float(v[j] << 16) * up,
                                  __uint_as_float(v[j] & 0xFFFF0000u) * up);
-          st_shared_v4(at + (c / 8) * S::kPanel + in_panel(r, c % 8), make_uint4(v[0], v[1], v[2], v[3]));
+          x[i] = make_uint4(v[0], v[1], v[2], v[3]);
         }
-      }
-    } else {
-      constexpr int kC = D / 8, kBatch = 8;
-      for (int c0 = 0; c0 < halves * kHalf * kC; c0 += kBatch * kLoaders) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int c = c0 + i * kLoaders + tid, m = c / kC;
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (m < w.unit.rows) {
-            const int tok = div_any(w.unit.first + m, p.by_group), hg = w.unit.first + m - tok * p.group;
-            x[i] = __ldg(reinterpret_cast<const uint4*>(
-                             p.q + static_cast<int64_t>(w.row.q0 + tok) * p.q_token +
-                             static_cast<int64_t>(w.g * p.group + hg) * p.q_head) + c % kC);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int c = c0 + i * kLoaders + tid, m = c / kC, ch = c % kC;
-          st_shared_v4(q_at + (m / kHalf) * S::kStage + (ch / 8) * S::kPanel + in_panel(m % kHalf, ch % 8),
-                       x[i]);
-        }
+        st_shared_v4(q_at + (m / kHalf) * S::kStage + (ch / 8) * S::kPanel + in_panel(m % kHalf, ch % 8),
+                     x[i]);
       }
     }
+  }
+  // 16 FP8 values of row `row`, chunk `ch` of it, to fp16 in a ring stage.
+  __device__ __forceinline__ void widen(uint32_t at, int row, int ch, uint4 raw) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[2 * j] = e4m3_to_f16(w[j] & 0xFFFF);
+      h[2 * j + 1] = e4m3_to_f16(w[j] >> 16);
+    }
+    const uint32_t panel = at + (ch / 4) * S::kPanel;
+    // The lanes of the second panel write their chunks in the other order: the
+    // eight of a row then hit different banks.
+    const bool other = ch & 4;
+    const int c = (ch % 4) * 2;
+    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+    st_shared_v4(panel + in_panel(row, c + (other ? 1 : 0)), other ? hi : lo);
+    st_shared_v4(panel + in_panel(row, c + (other ? 0 : 1)), other ? lo : hi);
   }
 };
 
@@ -421,23 +410,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr float kBias = kBf16 ? 0.f : 6.f;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + S::kRing);
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + S::kRing + S::kOut);
   __shared__ Shared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
   const uint32_t q_at = smem_addr(smem), ring = q_at + S::kQ;
 
+  const bool boxes = p.box_keys > 0;
   if (tid == 0) {
-    mbar_init(&sh.q_full, kLoaders);
+    mbar_init(&sh.q_full, p.q_box ? 1 : kLoaders);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.drain, 1);
+    mbar_init(&sh.edge, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], kHalf);
       mbar_init(&sh.p_full[i], kHalf);
       mbar_init(&sh.o_full[i], 1);
     }
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&sh.kv_full[i], kLoaders);
+      mbar_init(&sh.kv_full[i], boxes && !kFp8 ? 1 : kLoaders);
       mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < S::kRawTiles; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], kLoaders);
     }
     fence_mbar_init();
     sh.dead = 0;
@@ -448,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(kFullMask, sh.tmem, 0);
   const uint32_t workers = min(ws.workers, total);
   const uint32_t me = blockIdx.x;
   const uint32_t c0 = me < workers ? split_begin(me, total, workers) : 0;
@@ -462,22 +458,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + half * kKeys, o_at = tmem + lanes + 256 + half * D;
     const float ks = p.scale[0] ? __ldg(p.scale[0]) : 1.0f, vs = p.scale[1] ? __ldg(p.scale[1]) : 1.0f;
+    const uint32_t out_at = q_at + S::kRing + warp * 2048;
     uint32_t s_ph = 0, o_ph = 0, u_n = 0;
     Walk w;
     bool more = w.seek(c0, c1, prefix, p);
     for (; more; more = w.next(prefix, p), ++u_n) {
-      const int m = half * kHalf + r;  // row of the unit
-      if (half == 1 && w.unit.rows <= kHalf) continue;
-      const bool live = m < w.unit.rows;
-      const int i = div_any(w.unit.first + m, p.by_group);
-      const int pos = w.row.len - w.row.n + i;
-      // Rows past the unit's end are computed like the others and not written.
-      const int vis_hi = live ? pos + 1 : INT_MAX, vis_lo = live ? seen_lo(p, pos) : 0;
-      // Keys that every row of this warp's half sees need no mask.
-      const int i_first = div_any(w.unit.first + half * kHalf, p.by_group);
-      const int i_last = div_any(w.unit.first + min(w.unit.rows, (half + 1) * kHalf) - 1, p.by_group);
-      const int all_hi = w.row.len - w.row.n + i_first + 1;
-      const int all_lo = seen_lo(p, w.row.len - w.row.n + i_last);
+      if (half == 1 && w.unit.queries <= p.half_queries) continue;
+      const int in = div_any(r, p.by_group);                 // query of the half
+      const int i = w.unit.query + half * p.half_queries + in;  // of the request
+      const int before = w.row.len - w.row.n;
+      // Rows past the last query are computed like the others and not written.
+      const bool live = in < p.half_queries && i < w.row.n;
+      const int vis_hi = live ? before + i + 1 : INT_MAX, vis_lo = live ? seen_lo(p, before + i) : 0;
+      // Keys that every row of this half sees need no mask.
+      const int i0 = w.unit.query + half * p.half_queries;
+      const int all_hi = before + i0 + 1;
+      const int all_lo = seen_lo(p, before + min(i0 + p.half_queries, w.row.n) - 1);
       float sc = p.softmax_scale * kLog2e * ks;
       float top = -INFINITY, ref = -kBias, l = 0.f;  // ref: what scores are taken relative to
       bool ok = true;
@@ -487,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_ph ^= 1;
         tc_fence_after();
         if constexpr (kFp8 && kIn == HS_DT_BF16)
-          if (k == w.k0) sc *= sh.q_factor[u_n & 1][m];  // there before the product was issued
+          if (k == w.k0) sc *= sh.q_factor[u_n & 1][half * kHalf + r];  // there before the product was issued
         uint32_t s[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(s[q], s_at + q * 32);
@@ -510,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[q] = __uint_as_float(s[q][0]);
 #pragma unroll
           for (int c = 1; c < 31; c += 2)
-            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[q][c])), __uint_as_float(s[q][c + 1]));
+            mx[q] = max3(mx[q], __uint_as_float(s[q][c]), __uint_as_float(s[q][c + 1]));
           mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
         }
         const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
@@ -548,6 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             w16[c] = pack2t<kBf16>(a, b);  // half a step off each
           }
           tmem_st16(s_at + q * 16, w16);
+          if (q == 1) {
+            // The first 64 keys' weights go ahead: their product starts while the
+            // others are computed.
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sh.p_half[half]);
+          }
         }
         const uint64_t both = add2(sum[0], sum[1]);
         l += low_float(both) + high_float(both);
@@ -563,157 +566,125 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool none = top == -INFINITY;
       const float inv = none ? 0.f : 1.0f / l;
       const float lse = none ? -INFINITY : ref + log2f(l);
-      const int head = w.g * p.group + (w.unit.first + m - i * p.group);
-      const int64_t tok = w.row.q0 + i;
-      unsigned char* dst = p.out + tok * p.out_token + head * p.out_head;
-      float* part = ws.slots + static_cast<int64_t>(2 * me + (w.k0 == 0 ? 1 : 0)) * tiles_slot_floats(D);
       const float f = whole ? inv * vs : inv;
-#pragma unroll 1
-      for (int q = 0; q < D / 64; ++q) {
-        uint32_t o[2][32];
-        tmem_ld32(o[0], o_at + q * 64);
-        tmem_ld32(o[1], o_at + q * 64 + 32);
-        tmem_wait_ld();
-        tmem_pin(o[0]);
-        tmem_pin(o[1]);
-        if (live && whole) {
+      float* part = ws.slots + static_cast<int64_t>(2 * me + (w.k0 == 0 ? 1 : 0)) * tiles_slot_floats(D);
+      // 64 bytes of each of the warp's rows at a time through shared memory, so
+      // that four lanes write one row's: 16 bytes a lane of 32 rows would fill
+      // half a sector each.
+      unsigned char* to[4];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[c / 4][(c % 4) * 8 + e * 2]) * f,
-                                               __uint_as_float(o[c / 4][(c % 4) * 8 + e * 2 + 1]) * f);
-            *reinterpret_cast<uint4*>(dst + q * 128 + c * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        } else if (live) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t* x = o[c / 8] + (c % 8) * 4;
-            *reinterpret_cast<float4*>(part + m * D + q * 64 + c * 4) =
-                make_float4(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f,
-                            __uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f);
-          }
-        }
+      for (int x = 0; x < 4; ++x) {
+        const int rr = r - lane + x * 8 + (lane >> 2), q = div_any(rr, p.by_group);
+        const int t = w.unit.query + half * p.half_queries + q;
+        to[x] = nullptr;
+        if (q < p.half_queries && t < w.row.n)
+          to[x] = (whole ? p.out + static_cast<int64_t>(w.row.q0 + t) * p.out_token +
+                               static_cast<int64_t>(w.g * p.group + rr - q * p.group) * p.out_head
+                         : reinterpret_cast<unsigned char*>(part + (half * kHalf + rr) * D)) + (lane & 3) * 16;
       }
-      if (live && !whole) part[kUnitRows * D + m] = lse;
-      if (live && whole && p.lse) p.lse[tok * p.heads + head] = lse * kLn2;
+      const uint32_t mine_at = out_at + lane * 64, swap = (lane >> 1) & 3;
+      const int cols = whole ? 32 : 16;
+#pragma unroll 1
+      for (int d = 0; d < D; d += cols) {
+        uint32_t o[32];
+        if (whole)
+          tmem_ld32(o, o_at + d);
+        else
+          tmem_ld16(*reinterpret_cast<uint32_t(*)[16]>(o), o_at + d);
+        tmem_wait_ld();
+        tmem_pin(o);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = whole ? pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[c * 8 + e * 2]) * f,
+                                                     __uint_as_float(o[c * 8 + e * 2 + 1]) * f)
+                         : __float_as_uint(__uint_as_float(o[c * 4 + e]) * f);
+          st_shared_v4(mine_at + ((c ^ swap) << 4), make_uint4(x[0], x[1], x[2], x[3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int rr = x * 8 + (lane >> 2);
+          const uint4 v = ld_shared_v4(out_at + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+          if (to[x] != nullptr) *reinterpret_cast<uint4*>(to[x] + d * (whole ? 2 : 4)) = v;
+        }
+        __syncwarp();
+      }
+      if (live && !whole) part[kUnitRows * D + half * kHalf + r] = lse;
+      if (live && whole && p.lse)
+        p.lse[static_cast<int64_t>(w.row.q0 + i) * p.heads + w.g * p.group + r - in * p.group] = lse * kLn2;
       tc_fence_before();  // O is read before the next unit's first product, which waits for P
     }
   } else if (warp < 12) {
-    // ---------------------------------------------------------------- loads
+    // ---------------------------------------------------------------- through registers
     regs_shrink<kLoaderRegs>();
-    Loader<kIn, kFp8, D> ld{p, sh, q_at, ring, tid - 256};
     const int lt = tid - 256;
-    uint32_t u_n = 0, issued = 0;
+    Loader<kIn, kFp8, D> ld{p, sh, q_at, ring, lt};
+    uint32_t u_n = 0;
     RingAt<S::kStages> kv;
-    auto claim = [&]() {
-      return loaders_all(wait_for(&sh.kv_empty[kv.stage], kv.phase ^ 1, dead));
-    };
+    bool ok = true;
+    Walk w;
     auto publish = [&]() {
       fence_proxy_async_smem();  // the MMA reads through the async proxy
       mbar_arrive(&sh.kv_full[kv.stage]);
       kv.step();
-      ++issued;
     };
-    bool ok = true;
-    Walk w;
-    bool more = w.seek(c0, c1, prefix, p);
-    if (lt == 0) {
-      // Where this run's start cuts a unit, and is the first to do so, the unit's
-      // parts are joined in this worker's name.
-      int4 j = make_int4(-1, 0, 0, 0);
-      if (more && w.k0 > 0 && split_worker(w.u0 + kUnitCost, total, workers) + 1 == me)
-        j = make_int4(w.b, w.g, w.rt, static_cast<int>(split_worker(w.u0 + kUnitCost + w.unit.tiles - 1, total, workers)));
-      ws.joins[me] = j;
-    }
-    // A K (v = 0) or V tile by tensor-map boxes, a page or part of one each.
-    auto boxes = [&](int tile, int v) {
-      uint64_t* bar = &sh.kv_full[kv.stage];
-      if (lt == 0)
-        mbar_arrive_expect_tx(bar, S::kStage);
-      else
-        mbar_arrive(bar);
-      if (lt < kKeys / p.box_keys) {
-        const uint32_t dst = ring + kv.stage * S::kStage + lt * p.box_keys * 128;
-        const int j = tile * kKeys + lt * p.box_keys;
-        // A box that no query sees, or outside the pool, is past the last page:
-        // it reads zeros.
-        int page = static_cast<int>(p.num_pages), in_page = 0;
-        if (j + p.box_keys > w.row.lo && j < w.row.hi) {
-          const uint32_t c = div_any(static_cast<uint32_t>(j), p.div_page);
-          const int32_t e = __ldg(p.table + w.row.state * p.table_stride + c);
-          if (e >= 0 && e < p.num_pages) {
-            page = e;
-            in_page = j - static_cast<int>(c * p.page_size);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < S::kPanels; ++x)
-          tensor_load_4d(dst + x * S::kPanel, v ? &v_map : &k_map, x * 64, w.g, in_page, page, bar);
-      }
-      kv.step();
-      ++issued;
-    };
-    auto queries = [&]() {
-      ok = loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead));
-      if (!ok) return;
-      if (lt == 0) sh.unit[u_n & 1] = make_int2(w.unit.rows, w.k1 - w.k0);
-      if (!(kFp8 && kIn == HS_DT_BF16) && p.box_queries > 0) {
-        // 128 rows are box_queries tokens of the kv head's query heads.  Rows
-        // past the request's last query bring the next one's, and are not written.
-        const int halves = w.unit.rows > kHalf ? 2 : 1;
-        if (lt == 0) {
-          mbar_arrive_expect_tx(&sh.q_full, halves * S::kStage);
-          for (int h = 0; h < halves; ++h)
-#pragma unroll
-            for (int x = 0; x < S::kPanels; ++x)
-              tensor_load_3d(q_at + h * S::kStage + x * S::kPanel, &q_map, x * 64, w.g * p.group,
-                             w.row.q0 + w.unit.query + h * p.box_queries, &sh.q_full);
-        } else {
-          mbar_arrive(&sh.q_full);
-        }
-        return;
-      }
-      ld.load_q(w, u_n & 1);
+    auto publish_q = [&](bool end) {
+      if (lt == 0) sh.unit[u_n & 1] = end ? make_int2(0, 0) : make_int2(w.unit.queries, w.k1 - w.k0);
       fence_proxy_async_smem();
       mbar_arrive(&sh.q_full);
     };
-    for (; more && ok; more = w.next(prefix, p), ++u_n) {
-      const int64_t head = w.g * p.c_head;
-      if (!kFp8 && p.box_keys > 0) {
-        // The first K tile does not wait for the queries' buffer.
-        for (int k = w.k0; k < w.k1; ++k) {
-          const int tile = w.unit.tile + k;
-          if (!(ok = claim())) break;
-          boxes(tile, 0);
-          if (k == w.k0) {
-            queries();
-            if (!ok) break;
-          }
-          if (!(ok = claim())) break;
-          if (tile * kKeys < w.row.lo || (tile + 1) * kKeys > w.row.hi) {
-            // Positions that no query sees: their V rows must be zeros.
-            ld.look_up(w.row, tile, 0);
-#pragma unroll 1
-            for (int x = 0; x < S::kPieces; ++x) {
-              uint4 r[S::kPieceChunks];
-              ld.fetch(r, 0, x, true, head);
-              ld.store(r, kv.stage, x);
-            }
-            loaders_sync();  // offs is written again
-            publish();
-          } else {
-            boxes(tile, 1);
-          }
+    if (kFp8 && boxes) {
+      // Widens the tiles that the loading warp brings.  Each thread waits for
+      // itself: no barrier, so that a block that gives up leaves nobody behind.
+      RingAt<S::kRawTiles ? S::kRawTiles : 1> raw;
+      const uint32_t raw_at = ring + S::kStages * S::kStage;
+      auto widen = [&](const Walk& w, int k, bool v) {
+        if (!wait_for(&sh.raw_full[raw.stage], raw.phase, dead)) return false;
+        if (!wait_for(&sh.kv_empty[kv.stage], kv.phase ^ 1, dead)) return false;
+        const uint32_t from = raw_at + raw.stage * S::kRaw, to = ring + kv.stage * S::kStage;
+        const int j0 = (w.unit.tile + k) * kKeys;
+        const bool edge = v && (j0 < w.row.lo || j0 + kKeys > w.row.hi);
+#pragma unroll
+        for (int i = 0; i < kKeys * S::kRowChunks / kLoaders; ++i) {
+          const int c = i * kLoaders + lt, row = c / S::kRowChunks;
+          uint4 x = ld_shared_v4(from + c * 16);
+          // Positions that no query sees: their V rows must be zeros.
+          if (edge && (j0 + row < w.row.lo || j0 + row >= w.row.hi)) x = make_uint4(0, 0, 0, 0);
+          ld.widen(to, row, c % S::kRowChunks, x);
         }
-      } else {
-        // Pieces through registers, two in flight: K and V of each tile in turn.
-        queries();
+        mbar_arrive(&sh.raw_empty[raw.stage]);
+        raw.step();
+        publish();
+        return true;
+      };
+      for (bool more = w.seek(c0, c1, prefix, p); more && ok; more = w.next(prefix, p), ++u_n) {
+        for (int k = w.k0; k < w.k1 && ok; ++k) {
+          ok = widen(w, k, false);
+          if (ok && k == w.k0 && !p.q_box) {
+            ok = wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead);
+            if (!ok) break;
+            ld.load_q(w, u_n & 1);
+            publish_q(false);
+          }
+          ok = ok && widen(w, k, true);
+        }
+      }
+      if (ok && !p.q_box && wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead)) publish_q(true);
+    } else if (!boxes) {
+      // Pieces through registers, two in flight: K and V of each tile in turn.
+      // The loaders wait and give up together.
+      constexpr int kPer = 2 * S::kPieces;
+      uint4 ra[S::kPieceChunks], rb[S::kPieceChunks];
+      for (bool more = w.seek(c0, c1, prefix, p); more; more = w.next(prefix, p), ++u_n) {
+        ok = loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead));
         if (!ok) break;
-        constexpr int kPer = 2 * S::kPieces;
+        ld.load_q(w, u_n & 1);
+        publish_q(false);
+        const int64_t head = w.g * p.c_head;
         const int pieces = (w.k1 - w.k0) * kPer;
-        uint4 ra[S::kPieceChunks], rb[S::kPieceChunks];
         auto fetch = [&](uint4 (&r)[S::kPieceChunks], int x) {
           const int k = w.k0 + x / kPer, in = x % kPer;
           if (in == 0) ld.look_up(w.row, w.unit.tile + k, k & 1);
@@ -721,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto put = [&](const uint4 (&r)[S::kPieceChunks], int x) {
           const int in = x % S::kPieces;
-          if (in == 0) ok = claim();
+          if (in == 0) ok = loaders_all(wait_for(&sh.kv_empty[kv.stage], kv.phase ^ 1, dead));
           if (!ok) return;
           ld.store(r, kv.stage, in);
           if (in == S::kPieces - 1) publish();
@@ -736,99 +707,221 @@ __global__ void __launch_bounds__(kThreads, 1)
           put(rb, x + 1);
           if (!ok) break;
         }
+        if (!ok) break;
       }
-    }
-    if (ok) {
-      ok = loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead));
-      if (lt == 0) sh.unit[u_n & 1] = make_int2(0, 0);
-      mbar_arrive(&sh.q_full);
-    }
-    if (!ok) {
-      // The tensor-map loads still on their way write shared memory: see them in.
-      volatile int no = 0;
-      for (uint32_t n = issued > S::kStages ? issued - S::kStages : 0; n < issued; ++n)
-        wait_for(&sh.kv_full[n % S::kStages], (n / S::kStages) & 1, &no);
-      wait_for(&sh.q_full, u_n & 1, &no);
+      if (ok && loaders_all(wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead))) publish_q(true);
     }
   } else {
     // ---------------------------------------------------------------- MMA
     regs_shrink<kMmaRegs>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 13) {
+      // ---- the loading warp: a lane per box
+      Walk w;
+      bool more = w.seek(c0, c1, prefix, p);
+      if (lane == 0) {
+        // Where this run's start cuts a unit, and is the first to do so, the
+        // unit's parts are joined in this worker's name.
+        int4 j = make_int4(-1, 0, 0, 0);
+        if (more && w.k0 > 0 && split_worker(w.u0 + kUnitCost, total, workers) + 1 == me)
+          j = make_int4(w.b, w.g, w.unit.query,
+                        static_cast<int>(split_worker(w.u0 + kUnitCost + w.unit.tiles - 1, total, workers)));
+        ws.joins[me] = j;
+      }
+      if (boxes) {
+        constexpr int kSlots = kFp8 ? S::kRawTiles : S::kStages;
+        constexpr int kBytes = kFp8 ? S::kRaw : S::kStage;
+        constexpr int kRow = kFp8 ? D : 128;  // bytes of a key in a panel
+        uint64_t* const full = kFp8 ? sh.raw_full : sh.kv_full;
+        uint64_t* const empty = kFp8 ? sh.raw_empty : sh.kv_empty;
+        const uint32_t base = kFp8 ? ring + S::kStages * S::kStage : ring;
+        const bool mine = lane < kKeys / p.box_keys;
+        RingAt<kSlots ? kSlots : 1> kv;
+        uint32_t u_n = 0, issued = 0, edges = 0;
+        bool ok = true;
+        auto reached = [&](uint64_t* bar, uint32_t phase) {
+          return __all_sync(kFullMask, wait_for(bar, phase, dead));
+        };
+        // This lane's block of a tile, -1 where no query sees it.
+        auto find = [&](int tile) {
+          const int j = tile * kKeys + lane * p.box_keys;
+          int32_t e = -1;
+          if (mine && j + p.box_keys > w.row.lo && j < w.row.hi)
+            e = __ldg(p.table + w.row.state * p.table_stride + div_any(static_cast<uint32_t>(j), p.div_page));
+          return e;
+        };
+        auto load = [&](int tile, int32_t e, bool v, uint64_t* bar) {
+          const uint32_t dst = base + kv.stage * kBytes + lane * p.box_keys * kRow;
+          if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+          // A block that is not there is past the last page: it reads zeros.
+          int page = static_cast<int>(p.num_pages), in_page = 0;
+          if (e >= 0 && e < p.num_pages) {
+            const int j = tile * kKeys + lane * p.box_keys;
+            page = e;
+            in_page = j - static_cast<int>(div_any(static_cast<uint32_t>(j), p.div_page) * p.page_size);
+          }
+          if (mine) {
+#pragma unroll
+            for (int x = 0; x < (kFp8 ? 1 : S::kPanels); ++x)
+              tensor_load_4d(dst + x * S::kPanel, v ? &v_map : &k_map, x * 64, w.g, in_page, page, bar);
+          }
+          ++issued;
+        };
+        for (; more && ok; more = w.next(prefix, p), ++u_n) {
+          int32_t e = find(w.unit.tile + w.k0);
+          for (int k = w.k0; k < w.k1; ++k) {
+            const int tile = w.unit.tile + k;
+            const int32_t later = k + 1 < w.k1 ? find(tile + 1) : -1;
+            if (!(ok = reached(&empty[kv.stage], kv.phase ^ 1))) break;
+            load(tile, e, false, &full[kv.stage]);
+            kv.step();
+            if (k == w.k0 && p.q_box) {
+              // The first K tile does not wait for the queries' buffer.  Rows past
+              // the unit's last query bring others', and are not written.
+              if (!(ok = reached(&sh.q_empty, (u_n & 1) ^ 1))) break;
+              if (lane == 0) {
+                sh.unit[u_n & 1] = make_int2(w.unit.queries, w.k1 - w.k0);
+                const int halves = w.unit.queries > p.half_queries ? 2 : 1;
+                mbar_arrive_expect_tx(&sh.q_full, halves * S::kPanels * p.half_queries * p.group * 128);
+                for (int h = 0; h < halves; ++h)
+#pragma unroll
+                  for (int x = 0; x < S::kPanels; ++x)
+                    tensor_load_3d(q_at + h * S::kStage + x * S::kPanel, &q_map, x * 64, w.g * p.group,
+                                   w.row.q0 + w.unit.query + h * p.half_queries, &sh.q_full);
+              }
+            }
+            if (!(ok = reached(&empty[kv.stage], kv.phase ^ 1))) break;
+            const int lo = w.row.lo - tile * kKeys, hi = w.row.hi - tile * kKeys;
+            if (!kFp8 && (lo > 0 || hi < kKeys)) {
+              // Positions that no query sees: once the tile is here, their rows
+              // become zeros.
+              load(tile, e, true, &sh.edge);
+              if (!(ok = reached(&sh.edge, edges & 1))) break;
+              ++edges;
+              const uint32_t at = base + kv.stage * kBytes;
+              for (int c = lane; c < kKeys * S::kPanels * 8; c += kWarp) {
+                const int key = (c >> 3) & (kKeys - 1);  // panel by panel, 8 chunks a key
+                if (key < lo || key >= hi) st_shared_v4(at + c * 16, make_uint4(0, 0, 0, 0));
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&full[kv.stage]);
+            } else {
+              load(tile, e, true, &full[kv.stage]);
+            }
+            kv.step();
+            e = later;
+          }
+        }
+        if (ok && p.q_box) {
+          ok = reached(&sh.q_empty, (u_n & 1) ^ 1);
+          if (ok && lane == 0) {
+            sh.unit[u_n & 1] = make_int2(0, 0);
+            mbar_arrive(&sh.q_full);
+          }
+        }
+        if (!ok) {
+          // What is still on its way writes shared memory: see it in.
+          volatile int no = 0;
+          for (uint32_t n = issued > kSlots ? issued - kSlots : 0; n < issued; ++n)
+            wait_for(&full[n % (kSlots ? kSlots : 1)], (n / (kSlots ? kSlots : 1)) & 1, &no);
+          wait_for(&sh.edge, edges & 1, &no);
+          wait_for(&sh.q_full, u_n & 1, &no);
+        }
+      }
+      __syncwarp();
+    }
+    if (warp == 12) {
+      // The whole warp walks along, so that addresses and descriptors stay in
+      // uniform registers; one elected lane issues.
       constexpr uint32_t kQk = mma_shape(kBf16, kHalf, kKeys, false);
       constexpr uint32_t kPv = mma_shape(kBf16, kHalf, D, true);
       constexpr uint32_t kHi = mma_desc_hi(1024);
+      auto reached = [&](uint64_t* bar, uint32_t phase) {
+        const bool got = __all_sync(kFullMask, wait_for(bar, phase, dead));
+        tc_fence_after();
+        return got;
+      };
       auto qk = [&](int half, uint32_t stage) {
         const uint32_t a = mma_desc_lo(q_at + half * S::kStage, 16);
         const uint32_t b = mma_desc_lo(ring + stage * S::kStage, 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t o = ((x / 4) * S::kPanel + (x % 4) * 32) >> 4;
-          mma_smem<kHi>(tmem + half * kKeys, a + o, b + o, kQk, x > 0);
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t o = ((x / 4) * S::kPanel + (x % 4) * 32) >> 4;
+            mma_smem<kHi>(tmem + half * kKeys, a + o, b + o, kQk, x > 0);
+          }
+          mma_commit(&sh.s_full[half]);
         }
-        mma_commit(&sh.s_full[half]);
+        __syncwarp();
       };
-      auto pv = [&](int half, uint32_t stage, bool add) {
+      // O += P V as the weights come, 64 keys at a time.
+      auto pv = [&](int half, uint32_t stage, bool add, uint32_t phase) {
         const uint32_t b = mma_desc_lo(ring + stage * S::kStage, S::kPanel);
+        constexpr int kPart = kKeys / 32;
 #pragma unroll
-        for (int x = 0; x < kKeys / 16; ++x)
-          mma_tmem<kHi>(tmem + 256 + half * D, tmem + half * kKeys + x * 8, b + x * 128, kPv, add || x > 0);
+        for (int part = 0; part < 2; ++part) {
+          if (!reached(part ? &sh.p_full[half] : &sh.p_half[half], phase)) return false;
+          if (elect_one()) {
+#pragma unroll
+            for (int x = part * kPart; x < (part + 1) * kPart; ++x)
+              mma_tmem<kHi>(tmem + 256 + half * D, tmem + half * kKeys + x * 8, b + x * 128, kPv,
+                            add || x > 0);
+          }
+          __syncwarp();
+        }
+        return true;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
       };
       uint32_t u_n = 0, p0 = 0, p1 = 0;
       RingAt<S::kStages> kv;
-      auto arrived = [&]() {
-        const bool got = wait_for(&sh.kv_full[kv.stage], kv.phase, dead);
-        tc_fence_after();
-        return got;
-      };
-      auto weights = [&](int half, uint32_t& phase) {
-        const bool got = wait_for(&sh.p_full[half], phase, dead);
-        phase ^= 1;
-        tc_fence_after();
-        return got;
-      };
+      auto arrived = [&]() { return reached(&sh.kv_full[kv.stage], kv.phase); };
       bool ok = true;
       for (; ok; ++u_n) {
-        if (!(ok = wait_for(&sh.q_full, u_n & 1, dead))) break;
-        const bool two = sh.unit[u_n & 1].x > kHalf;
-        int left = sh.unit[u_n & 1].y;
+        if (!(ok = reached(&sh.q_full, u_n & 1))) break;
+        const bool two = __shfl_sync(kFullMask, sh.unit[u_n & 1].x, 0) > p.half_queries;
+        int left = __shfl_sync(kFullMask, sh.unit[u_n & 1].y, 0);
         if (left == 0 || !(ok = arrived())) break;
         qk(0, kv.stage);
         if (two) qk(1, kv.stage);
-        mma_commit(&sh.kv_empty[kv.stage]);
+        commit(&sh.kv_empty[kv.stage]);
         kv.step();
-        if (left == 1) mma_commit(&sh.q_empty);
+        if (left == 1) commit(&sh.q_empty);
         for (bool add = false; left > 0; add = true) {
           // The ring holds this tile's V and the next one's K.
           --left;
-          if (!(ok = arrived() && weights(0, p0))) break;
           const uint32_t v = kv.stage;
+          if (!(ok = arrived())) break;
           kv.step();
-          pv(0, v, add);
-          if (left == 0) {
-            mma_commit(&sh.o_full[0]);
-          } else {
-            if (!(ok = arrived())) break;
+          if (!(ok = pv(0, v, add, p0))) break;
+          p0 ^= 1;
+          if (left > 0 && !(ok = arrived())) break;
+          if (left == 0)
+            commit(&sh.o_full[0]);
+          else
             qk(0, kv.stage);  // over P, after the product that reads it: in issue order
-          }
           if (two) {
-            if (!(ok = weights(1, p1))) break;
-            pv(1, v, add);
+            if (!(ok = pv(1, v, add, p1))) break;
+            p1 ^= 1;
           }
-          mma_commit(&sh.kv_empty[v]);
           if (left == 0) {
-            if (two) mma_commit(&sh.o_full[1]);
+            if (two) commit(&sh.o_full[1]);
+            commit(&sh.kv_empty[v]);
             break;
           }
           if (two) qk(1, kv.stage);
-          mma_commit(&sh.kv_empty[kv.stage]);
-          if (left == 1) mma_commit(&sh.q_empty);
+          commit(&sh.kv_empty[v]);
+          commit(&sh.kv_empty[kv.stage]);
+          if (left == 1) commit(&sh.q_empty);
           kv.step();
         }
       }
       if (!ok) {
         // Give what was issued a while to end before tensor memory is freed.
         volatile int no = 0;
-        mma_commit(&sh.drain);
+        commit(&sh.drain);
         wait_for(&sh.drain, 0, &no);
       }
     }
@@ -866,11 +959,12 @@ __global__ void __launch_bounds__(kTilesJoinThreads)
   if (j.x < 0) return;
   const AttnRow row = attn_row(p, j.x);
   const int w0 = w - 1, w1 = j.w;
-  const int rows = min(kUnitRows, row.n * p.group - j.z * kUnitRows);
   const float vs = p.scale[1] ? __ldg(p.scale[1]) : 1.0f;
   const int lane = threadIdx.x % kLanes;
   const int first = (blockIdx.x % kBlocks) * kJoinRows;
-  for (int m = first + threadIdx.x / kLanes; m < min(rows, first + kJoinRows); m += kAtOnce) {
+  for (int m = first + threadIdx.x / kLanes; m < first + kJoinRows; m += kAtOnce) {
+    const int r = m % kHalf, in = r / p.group, i = j.z + (m / kHalf) * p.half_queries + in;
+    if (in >= p.half_queries || i >= row.n) continue;
     auto part = [&](int x) {
       return ws.slots + static_cast<int64_t>(2 * x + (x == w0 ? 1 : 0)) * tiles_slot_floats(D);
     };
@@ -889,7 +983,7 @@ __global__ void __launch_bounds__(kTilesJoinThreads)
       acc.w += add * o.w;
     }
     const float f = top == -INFINITY ? 0.f : vs / l;
-    const int r = j.z * kUnitRows + m, i = r / p.group, head = j.y * p.group + (r - i * p.group);
+    const int head = j.y * p.group + r - in * p.group;
     const int64_t tok = row.q0 + i;
     constexpr bool kB = kIn == HS_DT_BF16;
     *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + lane * 8) =
@@ -908,7 +1002,7 @@ struct TilesKernels {
 template <int kIn, bool kFp8, int D>
 TilesKernels tiles_kernels() {
   return TilesKernels{attn_tiles_kernel<kIn, kFp8, D>, attn_tiles_join_kernel<kIn, D>,
-                      TilesShape<kIn, kFp8, D>::kRing + 1024};
+                      TilesShape<kIn, kFp8, D>::kRing + TilesShape<kIn, kFp8, D>::kOut + 1024};
 }
 TilesKernels tiles_pick(int in_dtype, bool fp8, int dim) {
   if (in_dtype == HS_DT_BF16) {
@@ -957,18 +1051,20 @@ hs_err tiles_setup(const DeviceInfo& dev) {
   return HS_OK;
 }
 
-// A cache as [pages][page][heads][dim], read in boxes of `keys` rows of 64 dims
-// of one head, swizzled as the MMA wants it.
-bool encode_cache(CUtensorMap* map, const AttnParams& p, int which, bool bf16, int keys) {
+// A cache as [pages][page][heads][dim], read in boxes of `keys` rows of one head:
+// 64 dims at a time, swizzled as the MMA wants them, or whole rows of bytes.
+bool encode_cache(CUtensorMap* map, const AttnParams& p, int which, bool fp8, bool bf16, int keys) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.kv_heads),
                               p.page_size, static_cast<cuuint64_t>(p.num_pages)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.c_head), static_cast<cuuint64_t>(p.c_off),
                                  static_cast<cuuint64_t>(p.c_page)};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(keys), 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(fp8 ? p.dim : 64), 1, static_cast<cuuint32_t>(keys), 1};
   const cuuint32_t steps[4] = {1, 1, 1, 1};
-  return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  const_cast<unsigned char*>(p.cache[which]), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return g_encode(map,
+                  fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                      : (bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16),
+                  4, const_cast<unsigned char*>(p.cache[which]), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1009,24 +1105,21 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   TilesParams tp;
   static_cast<AttnParams&>(tp) = p;
   const uint32_t group = static_cast<uint32_t>(p.group);
+  const bool bf16 = in_dtype == HS_DT_BF16;
   tp.by_group = FastDiv{fastdiv_magic(group), group};
-  tp.unit_query = kUnitRows / p.group;
-  tp.unit_rem = kUnitRows % p.group;
-  tp.box_keys = tp.box_queries = 0;
+  tp.half_queries = kHalf / p.group;
+  tp.box_keys = 0;
   CUtensorMap maps[3] = {};
-  if (!fp8) {
-    if (p.page_size % kKeys == 0)
-      tp.box_keys = kKeys;
-    else if (p.page_size % 8 == 0 && kKeys % p.page_size == 0)
-      tp.box_keys = static_cast<int>(p.page_size);
-    if (p.num_pages < 1 || p.num_pages >= INT32_MAX) tp.box_keys = 0;
-    // Strides that a tensor map cannot hold go through registers.
-    for (int i = 0; tp.box_keys > 0 && i < 2; ++i)
-      if (!encode_cache(&maps[i], p, i, in_dtype == HS_DT_BF16, tp.box_keys)) tp.box_keys = 0;
-  }
-  if (kHalf % p.group == 0 && !(fp8 && in_dtype == HS_DT_BF16) &&
-      encode_queries(&maps[2], p, in_dtype == HS_DT_BF16))
-    tp.box_queries = kHalf / p.group;
+  if (p.page_size % kKeys == 0)
+    tp.box_keys = kKeys;
+  else if (p.page_size % 8 == 0 && kKeys % p.page_size == 0)
+    tp.box_keys = static_cast<int>(p.page_size);
+  if (p.num_pages < 1 || p.num_pages >= INT32_MAX) tp.box_keys = 0;
+  // Strides that a tensor map cannot hold go through registers.
+  for (int i = 0; tp.box_keys > 0 && i < 2; ++i)
+    if (!encode_cache(&maps[i], p, i, fp8, bf16, tp.box_keys)) tp.box_keys = 0;
+  tp.q_box = tp.box_keys > 0 && !(fp8 && bf16) && encode_queries(&maps[2], p, bf16);
+  if (!fp8 && !tp.q_box) tp.box_keys = 0;
   k.main<<<dev.sm_count, kThreads, k.smem + (p.batch + 1) * 4, stream>>>(tp, ws, maps[0], maps[1], maps[2]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention launch: %s", cudaGetErrorString(e));
