@@ -593,10 +593,10 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  * some of its queries see and others do not may make either kind NaN.
  * Scores, sums and outputs are accumulated in fp32.  For 16-bit inputs with
  * head_dim 64 or 128 the products run on the tensor cores, with the softmax
- * weights rounded to the cache's compute type (in_dtype, fp16 for HS_DT_E4M3);
- * with HS_DT_E4M3 bf16 queries are multiplied by a power of two per row and
- * taken as fp16.  Results do not depend on what else is in the batch, except
- * through the order of fp32 sums.
+ * weights rounded to in_dtype, or to fp16 for HS_DT_E4M3, whose values are
+ * widened exactly; bf16 queries are then taken as fp16 after a power of two per
+ * row, exact to 2^-22 of the row's largest.  Results do not depend on what else
+ * is in the batch, except through the order of fp32 sums.
  * Limits: head_dim <= 512, num_heads a multiple of num_kv_heads, batch <= 2048,
  * L <= INT32_MAX (else HS_ERR_UNSUPPORTED, or HS_ST_BAD_STATE for L).
  */

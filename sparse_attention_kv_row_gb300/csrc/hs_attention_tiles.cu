@@ -53,8 +53,7 @@ constexpr int kUnitCost = 3;
 struct TilesParams : AttnParams {
   FastDiv by_group;
   int half_queries;  // whole queries in 128 rows
-  int box_keys;      // keys per tensor-map box of the cache, 0: through registers
-  bool q_box;        // the queries come by tensor map too
+  int box_keys;      // keys per tensor-map box of the cache, 0: all through registers
 };
 
 struct TilesSpace {
@@ -180,6 +179,7 @@ struct Shared {
   uint32_t tmem;
   volatile int dead;
   int2 unit[2];  // for the MMA warp: queries and tiles of a unit, no tiles at the end
+  uint64_t q_raw;  // bf16 queries for an FP8 cache, before they become fp16
   float q_factor[2][kUnitRows];
   int64_t offs[2][kKeys];
 };
@@ -337,8 +337,43 @@ struct Loader {
                             : -1;
     loaders_sync();
   }
-  // The unit's queries, zeros past its last; bf16 ones times a power of two a
-  // row, as fp16, where the cache is FP8.
+  // Eight bf16 values times `up` as fp16.
+  __device__ __forceinline__ static uint4 to_f16(uint4 x, float up) {
+    uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = pack2t<false>(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  // The larger of `top` and the magnitudes (as bits) of eight bf16 values.
+  __device__ __forceinline__ static uint32_t largest(uint32_t top, uint4 x) {
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
+    return top;
+  }
+  // Turns the unit's bf16 queries, where the tensor map has put them, into fp16:
+  // a row a thread, times a power of two.
+  __device__ __forceinline__ void halve_q(const Walk& w, int buf) {
+    const int halves = w.unit.queries > p.half_queries ? 2 : 1;
+#pragma unroll 1
+    for (int h = 0; h < halves; ++h) {
+      const uint32_t at = q_at + h * S::kStage;
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        top = largest(top, ld_shared_v4(at + (c / 8) * S::kPanel + in_panel(tid, c % 8)));
+      const float up = f16_factor(top);
+      sh.q_factor[buf][h * kHalf + tid] = 1.0f / up;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t x = at + (c / 8) * S::kPanel + in_panel(tid, c % 8);
+        st_shared_v4(x, to_f16(ld_shared_v4(x), up));
+      }
+    }
+  }
+  // The unit's queries through registers, zeros past its last; bf16 ones to fp16
+  // for an FP8 cache.
   __device__ __forceinline__ void load_q(const Walk& w, int buf) {
     const int halves = w.unit.queries > p.half_queries ? 2 : 1;
     constexpr int kC = D / 8, kBatch = 8;
@@ -359,19 +394,12 @@ struct Loader {
       for (int i = 0; i < kBatch; ++i) {
         const int c = c0 + i * kLoaders + tid, m = c / kC, ch = c % kC;
         if constexpr (kFp8 && kIn == HS_DT_BF16) {
-          // A row is kC neighbouring lanes'.
-          uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, top = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
+          uint32_t top = largest(0, x[i]);  // a row is kC neighbouring lanes'
 #pragma unroll
           for (int j = kC / 2; j > 0; j >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, j));
           const float up = f16_factor(top);
           if (ch == 0) sh.q_factor[buf][m] = 1.0f / up;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = pack2t<false>(__uint_as_float(v[j] << 16) * up,
-                                 __uint_as_float(v[j] & 0xFFFF0000u) * up);
-          x[i] = make_uint4(v[0], v[1], v[2], v[3]);
+          x[i] = to_f16(x[i], up);
         }
         st_shared_v4(q_at + (m / kHalf) * S::kStage + (ch / 8) * S::kPanel + in_panel(m % kHalf, ch % 8),
                      x[i]);
@@ -406,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap q_map) {
   using S = TilesShape<kIn, kFp8, D>;
   constexpr bool kBf16 = kIn == HS_DT_BF16 && !kFp8;  // type of the products
+  constexpr bool kHalve = kIn == HS_DT_BF16 && kFp8;  // the queries become fp16
   // fp16 weights reach 2^(6 + 8) and keep what is 2^-30 of the reference.
   constexpr float kBias = kBf16 ? 0.f : 6.f;
   extern __shared__ unsigned char smem_raw[];
@@ -417,10 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const bool boxes = p.box_keys > 0;
   if (tid == 0) {
-    mbar_init(&sh.q_full, p.q_box ? 1 : kLoaders);
+    mbar_init(&sh.q_full, boxes && !kHalve ? 1 : kLoaders);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.drain, 1);
     mbar_init(&sh.edge, 1);
+    mbar_init(&sh.q_raw, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_half[i], kHalf);
@@ -482,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_ph ^= 1;
         tc_fence_after();
-        if constexpr (kFp8 && kIn == HS_DT_BF16)
+        if constexpr (kHalve)
           if (k == w.k0) sc *= sh.q_factor[u_n & 1][half * kHalf + r];  // there before the product was issued
         uint32_t s[4][32];
 #pragma unroll
@@ -663,16 +693,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool more = w.seek(c0, c1, prefix, p); more && ok; more = w.next(prefix, p), ++u_n) {
         for (int k = w.k0; k < w.k1 && ok; ++k) {
           ok = widen(w, k, false);
-          if (ok && k == w.k0 && !p.q_box) {
-            ok = wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead);
-            if (!ok) break;
-            ld.load_q(w, u_n & 1);
+          if (kHalve && ok && k == w.k0) {
+            if (!(ok = wait_for(&sh.q_raw, u_n & 1, dead))) break;
+            ld.halve_q(w, u_n & 1);
             publish_q(false);
           }
           ok = ok && widen(w, k, true);
         }
       }
-      if (ok && !p.q_box && wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead)) publish_q(true);
+      if (kHalve && ok && wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead)) publish_q(true);
     } else if (!boxes) {
       // Pieces through registers, two in flight: K and V of each tile in turn.
       // The loaders wait and give up together.
@@ -774,19 +803,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = reached(&empty[kv.stage], kv.phase ^ 1))) break;
             load(tile, e, false, &full[kv.stage]);
             kv.step();
-            if (k == w.k0 && p.q_box) {
+            if (k == w.k0) {
               // The first K tile does not wait for the queries' buffer.  Rows past
               // the unit's last query bring others', and are not written.
               if (!(ok = reached(&sh.q_empty, (u_n & 1) ^ 1))) break;
               if (lane == 0) {
-                sh.unit[u_n & 1] = make_int2(w.unit.queries, w.k1 - w.k0);
+                uint64_t* bar = kHalve ? &sh.q_raw : &sh.q_full;
+                if (!kHalve) sh.unit[u_n & 1] = make_int2(w.unit.queries, w.k1 - w.k0);
                 const int halves = w.unit.queries > p.half_queries ? 2 : 1;
-                mbar_arrive_expect_tx(&sh.q_full, halves * S::kPanels * p.half_queries * p.group * 128);
+                mbar_arrive_expect_tx(bar, halves * S::kPanels * p.half_queries * p.group * 128);
                 for (int h = 0; h < halves; ++h)
 #pragma unroll
                   for (int x = 0; x < S::kPanels; ++x)
                     tensor_load_3d(q_at + h * S::kStage + x * S::kPanel, &q_map, x * 64, w.g * p.group,
-                                   w.row.q0 + w.unit.query + h * p.half_queries, &sh.q_full);
+                                   w.row.q0 + w.unit.query + h * p.half_queries, bar);
               }
             }
             if (!(ok = reached(&empty[kv.stage], kv.phase ^ 1))) break;
@@ -812,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             e = later;
           }
         }
-        if (ok && p.q_box) {
+        if (ok && !kHalve) {
           ok = reached(&sh.q_empty, (u_n & 1) ^ 1);
           if (ok && lane == 0) {
             sh.unit[u_n & 1] = make_int2(0, 0);
@@ -825,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t n = issued > kSlots ? issued - kSlots : 0; n < issued; ++n)
             wait_for(&full[n % (kSlots ? kSlots : 1)], (n / (kSlots ? kSlots : 1)) & 1, &no);
           wait_for(&sh.edge, edges & 1, &no);
-          wait_for(&sh.q_full, u_n & 1, &no);
+          wait_for(kHalve ? &sh.q_raw : &sh.q_full, u_n & 1, &no);
         }
       }
       __syncwarp();
@@ -1118,8 +1148,7 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   // Strides that a tensor map cannot hold go through registers.
   for (int i = 0; tp.box_keys > 0 && i < 2; ++i)
     if (!encode_cache(&maps[i], p, i, fp8, bf16, tp.box_keys)) tp.box_keys = 0;
-  tp.q_box = tp.box_keys > 0 && !(fp8 && bf16) && encode_queries(&maps[2], p, bf16);
-  if (!fp8 && !tp.q_box) tp.box_keys = 0;
+  if (tp.box_keys > 0 && !encode_queries(&maps[2], p, bf16)) tp.box_keys = 0;
   k.main<<<dev.sm_count, kThreads, k.smem + (p.batch + 1) * 4, stream>>>(tp, ws, maps[0], maps[1], maps[2]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention launch: %s", cudaGetErrorString(e));

@@ -143,6 +143,33 @@ def test_fp8_keeps_small_and_huge_queries(dev, lens):
 
 
 @pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,page,tensor_cores", [(128, 16, True), (64, 48, True), (40, 16, False)])
+def test_every_fp8_code(dev, lens, dtype, dim, page, tensor_cores):
+    """Caches of random codes: subnormals, both zeros, the largest; then NaN codes, which make
+    the rows that see them NaN and leave the others alone."""
+    x = PagedInputs(lens, heads=4, kv_heads=2, dim=dim, dtype=dtype, cache="fp8", page=page, seed=4,
+                    scales=(0.003, 0.02))
+    g = torch.Generator().manual_seed(1)
+    for c in (x.kc, x.vc):
+        codes = torch.randint(0, 256, c.shape, generator=g, dtype=torch.uint8)
+        codes[(codes & 0x7F) == 0x7F] = 0x81
+        c.view(torch.uint8).copy_(torch.where(c.float().isnan(), c.view(torch.uint8), codes))
+    x.check(_hs(), dev, tensor_cores)
+    for which in ("kc", "vc"):
+        y = PagedInputs(lens, heads=4, kv_heads=2, dim=dim, dtype=dtype, cache="fp8", page=page, seed=4)
+        b = 5  # a request of one token over 500 or 700
+        getattr(y, which).view(torch.uint8)[y.table[y.req[3 if lens is CHUNKS else b], 100 // page],
+                                            100 % page, 1, 7] = 0xFF
+        out, _, _ = y.call(_hs(), dev)
+        row = int(y.cu[3 if lens is CHUNKS else b])
+        bad = out.float().isnan().any(-1).cpu()
+        want = torch.zeros_like(bad)
+        want[row, 2:] = True
+        assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
 @pytest.mark.parametrize("cache", ["same", "fp8"])
 def test_views_and_layouts(dev, lens, cache):
     """q a slice of a packed projection, out strided, K and V interleaved in one cache."""
