@@ -497,13 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int in = div_any(r, p.by_group);                 // query of the half
       const int i = w.unit.query + half * p.half_queries + in;  // of the request
       const int before = w.row.len - w.row.n;
-      // Rows past the last query are computed like the others and not written.
+      // Rows past the last query are computed like the last one and not written.
       const bool live = in < p.half_queries && i < w.row.n;
-      const int vis_hi = live ? before + i + 1 : INT_MAX, vis_lo = live ? seen_lo(p, before + i) : 0;
-      // Keys that every row of this half sees need no mask.
       const int i0 = w.unit.query + half * p.half_queries;
-      const int all_hi = before + i0 + 1;
-      const int all_lo = seen_lo(p, before + min(i0 + p.half_queries, w.row.n) - 1);
+      const int i1 = min(i0 + p.half_queries, w.row.n) - 1;
+      const int vis_hi = before + min(i, i1) + 1, vis_lo = seen_lo(p, before + min(i, i1));
+      // Keys that every row of this half sees need no mask.
+      const int all_hi = before + i0 + 1, all_lo = seen_lo(p, before + i1);
       float sc = p.softmax_scale * kLog2e * ks;
       float top = -INFINITY, ref = -kBias, l = 0.f;  // ref: what scores are taken relative to
       bool ok = true;
@@ -522,13 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 4; ++q) tmem_pin(s[q]);
         const int j0 = (w.unit.tile + k) * kKeys;
         if (j0 + kKeys > all_hi || j0 < all_lo) {
+          // The rows of a warp end within a few keys of each other: of the 32-key
+          // parts most are seen by all of them or by none.
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 4; ++q) {
+            const int hi = vis_hi - j0 - q * 32, lo = vis_lo - j0 - q * 32;
+            if (!__all_sync(kFullMask, hi >= 32 && lo <= 0)) {
+              const uint32_t seen = (hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u) &
+                                    (lo <= 0 ? ~0u : lo >= 32 ? 0u : ~0u << lo);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int j = j0 + q * 32 + c;
-              if (j >= vis_hi || j < vis_lo) s[q][c] = 0xFF800000u;  // -inf
+              for (int c = 0; c < 32; ++c)
+                if (!(seen & (1u << c))) s[q][c] = 0xFF800000u;  // -inf
             }
+          }
         }
         float mx[4];
 #pragma unroll
@@ -613,34 +619,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : reinterpret_cast<unsigned char*>(part + (half * kHalf + rr) * D)) + (lane & 3) * 16;
       }
       const uint32_t mine_at = out_at + lane * 64, swap = (lane >> 1) & 3;
-      const int cols = whole ? 32 : 16;
-#pragma unroll 1
-      for (int d = 0; d < D; d += cols) {
-        uint32_t o[32];
-        if (whole)
-          tmem_ld32(o, o_at + d);
-        else
-          tmem_ld16(*reinterpret_cast<uint32_t(*)[16]>(o), o_at + d);
-        tmem_wait_ld();
-        tmem_pin(o);
+      uint32_t o[D / 32][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[4];
+      for (int q = 0; q < D / 32; ++q) tmem_ld32(o[q], o_at + q * 32);
+      tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = whole ? pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[c * 8 + e * 2]) * f,
-                                                     __uint_as_float(o[c * 8 + e * 2 + 1]) * f)
-                         : __float_as_uint(__uint_as_float(o[c * 4 + e]) * f);
-          st_shared_v4(mine_at + ((c ^ swap) << 4), make_uint4(x[0], x[1], x[2], x[3]));
-        }
+      for (int q = 0; q < D / 32; ++q) tmem_pin(o[q]);
+      auto send = [&](const uint32_t (&x)[16], int at) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          st_shared_v4(mine_at + ((c ^ swap) << 4), make_uint4(x[c * 4], x[c * 4 + 1], x[c * 4 + 2], x[c * 4 + 3]));
         __syncwarp();
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int rr = x * 8 + (lane >> 2);
           const uint4 v = ld_shared_v4(out_at + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-          if (to[x] != nullptr) *reinterpret_cast<uint4*>(to[x] + d * (whole ? 2 : 4)) = v;
+          if (to[x] != nullptr) *reinterpret_cast<uint4*>(to[x] + at) = v;
         }
         __syncwarp();
+      };
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t x[16];
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            x[c] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[q][2 * c]) * f,
+                                             __uint_as_float(o[q][2 * c + 1]) * f);
+          send(x, q * 64);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(o[q][h * 16 + c]) * f);
+            send(x, q * 128 + h * 64);
+          }
+        }
       }
       if (live && !whole) part[kUnitRows * D + half * kHalf + r] = lse;
       if (live && whole && p.lse)
@@ -828,9 +842,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = reached(&sh.edge, edges & 1))) break;
               ++edges;
               const uint32_t at = base + kv.stage * kBytes;
-              for (int c = lane; c < kKeys * S::kPanels * 8; c += kWarp) {
-                const int key = (c >> 3) & (kKeys - 1);  // panel by panel, 8 chunks a key
-                if (key < lo || key >= hi) st_shared_v4(at + c * 16, make_uint4(0, 0, 0, 0));
+              const int gone = max(0, min(lo, kKeys)), from = max(gone, min(hi, kKeys));
+              const int rows = gone + kKeys - from;
+              for (int c = lane; c < rows * S::kPanels * 8; c += kWarp) {
+                const int x = c / (S::kPanels * 8), in = c % (S::kPanels * 8);
+                const int key = x < gone ? x : from + x - gone;
+                st_shared_v4(at + (in / 8) * S::kPanel + in_panel(key, in % 8), make_uint4(0, 0, 0, 0));
               }
               fence_proxy_async_smem();
               __syncwarp();
