@@ -595,9 +595,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.p_full[half]);
       }
       if (!ok) break;
-      if (!__all_sync(kFullMask, wait_for(&sh.o_full[half], o_ph, dead))) break;
-      o_ph ^= 1;
-      tc_fence_after();
       const bool whole = w.k0 == 0 && w.k1 == w.unit.tiles;
       const bool none = top == -INFINITY;
       const float inv = none ? 0.f : 1.0f / l;
@@ -619,6 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : reinterpret_cast<unsigned char*>(part + (half * kHalf + rr) * D)) + (lane & 3) * 16;
       }
       const uint32_t mine_at = out_at + lane * 64, swap = (lane >> 1) & 3;
+      // (the above while the last product runs)
+      if (!__all_sync(kFullMask, wait_for(&sh.o_full[half], o_ph, dead))) break;
+      o_ph ^= 1;
+      tc_fence_after();
       uint32_t o[D / 32][32];
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) tmem_ld32(o[q], o_at + q * 32);

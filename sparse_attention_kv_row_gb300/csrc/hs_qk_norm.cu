@@ -10,7 +10,7 @@
 // norm_rope_rows: a head is held by a group of 8, 16 or 32 lanes, one 16-byte
 // chunk each, so the sum is a shuffle reduction within the group and the other
 // half of a rotated pair is either in the same chunk (interleaved) or one
-// shuffle away.  A warp takes kRounds such rounds of heads, all loads first.
+// shuffle away.  A warp takes kRounds such rounds of one token's heads.
 // norm_rope_general: any strides, alignment, head and rotation size; a warp per
 // head with the head staged in shared memory.
 #include <cuda_bf16.h>
@@ -44,6 +44,7 @@ struct NormParams {
   int64_t num_slots;
   uint32_t page_size;
   FastDiv div_page, div_heads;               // div_heads: by num_heads + 2 num_kv_heads
+  FastDiv div_units;                         // (rows kernel) by a token's units
   const int64_t* loc;
   const float* scale[2];
   int32_t* status;
@@ -51,7 +52,7 @@ struct NormParams {
   float eps, inv_dim;
   bool interleaved;
   int64_t t_begin;                           // first token of this launch
-  uint32_t rows;                             // heads (of all three kinds) of this launch
+  uint32_t rows;                             // heads (general) or units (rows) of this launch
 };
 
 template <int kDtype>
@@ -146,40 +147,86 @@ __device__ __forceinline__ unsigned char* slot_at(int64_t L, int kind, int head,
          (L - page * p.page_size) * p.c_off + static_cast<int64_t>(head) * p.c_head;
 }
 
-// G lanes per head, one 16-byte chunk per lane (lanes past the head idle).
-template <int kDtype, bool kFp8, int G>
+// E angles of a lane's chunk, cosines or sines (16-byte aligned).
+template <int kN>
+__device__ __forceinline__ void load_angles(float (&x)[kN], const float* p) {
+#pragma unroll
+  for (int i = 0; i < kN; i += 4) {
+    if constexpr (kN >= 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+      x[i] = v.x;
+      x[i + 1] = v.y;
+      x[i + 2] = v.z;
+      x[i + 3] = v.w;
+    } else {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+      x[0] = v.x;
+      x[1] = v.y;
+    }
+  }
+}
+
+// A warp takes kPer * kRounds heads of one token; G lanes per head, one 16-byte
+// chunk per lane (lanes past the head idle).  The token's angles are in
+// registers for all of them, and every load of the unit is on its way before
+// the first value is used.
+template <int kDtype, bool kFp8, int G, bool kInter>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_rows(const NormParams p) {
   using T = Elem<kDtype>;
   constexpr int E = T::kChunk;
-  constexpr int kPer = kWarp / G;  // heads of a warp in one round
+  constexpr int kPer = kWarp / G;               // heads of a warp in one round
+  constexpr int kAngles = kInter ? E / 2 : E;   // pairs that a lane turns
   const int lane = threadIdx.x & 31;
   const int c = lane & (G - 1);
   const bool in_head = c * E < p.dim;
   const int half = p.rot >> 1;
-  const uint32_t unit = (blockIdx.x * kNormWarps + (threadIdx.x >> 5)) * (kPer * kRounds);
+  const uint32_t unit = blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+  if (unit >= p.rows) return;
+  const uint32_t tok = div_any(unit, p.div_units);
+  const int64_t t = p.t_begin + tok;
+  const int h0 = static_cast<int>(unit - tok * p.div_units.d) * (kPer * kRounds) + lane / G;
+  const int all = p.heads + 2 * p.kv_heads;
+  const bool has_kv = h0 - lane / G + kPer * kRounds > p.heads;
+
+  const int64_t pos = p.rot > 0 ? __ldg(p.positions + t) : 0;
+  const int64_t loc = has_kv ? __ldg(p.loc + t) : 0;
   uint4 raw[kRounds];
-  int64_t pos[kRounds], loc[kRounds];
-  HeadAt at[kRounds];
 #pragma unroll
   for (int j = 0; j < kRounds; ++j) {
-    const uint32_t r = unit + j * kPer + lane / G;
+    const int h = h0 + j * kPer;
     raw[j] = make_uint4(0, 0, 0, 0);
-    pos[j] = loc[j] = 0;
-    at[j].kind = -1;
-    if (r >= p.rows) continue;
-    at[j] = head_at(r, p);
-    const int k = at[j].kind;
-    if (in_head)
-      raw[j] = ld_stream_v4((k == 0 ? p.in[0] : (k == 1 ? p.in[1] : p.in[2])) +
-                            at[j].token * (k == 0 ? p.in_token[0] : (k == 1 ? p.in_token[1] : p.in_token[2])) +
-                            at[j].head * (k == 0 ? p.in_head[0] : (k == 1 ? p.in_head[1] : p.in_head[2])) +
-                            c * 16);
-    if (p.rot > 0) pos[j] = __ldg(p.positions + at[j].token);
-    if (k > 0) loc[j] = __ldg(p.loc + at[j].token);
+    if (in_head && h < all) {
+      const int kind = h < p.heads ? 0 : (h < p.heads + p.kv_heads ? 1 : 2);
+      const int head = h - (kind > 0 ? p.heads : 0) - (kind > 1 ? p.kv_heads : 0);
+      raw[j] = ld_stream_v4(
+          (kind == 0 ? p.in[0] : (kind == 1 ? p.in[1] : p.in[2])) +
+          t * (kind == 0 ? p.in_token[0] : (kind == 1 ? p.in_token[1] : p.in_token[2])) +
+          head * (kind == 0 ? p.in_head[0] : (kind == 1 ? p.in_head[1] : p.in_head[2])) + c * 16);
+    }
   }
+  const bool pos_ok = p.rot == 0 || (pos >= 0 && pos < p.max_pos);
+  const int hc = kInter ? 0 : half / E;  // chunks of half the rotated dims (split halves)
+  const bool first = c < hc, turns = kInter ? c * E < p.rot : c < 2 * hc;
+  const int partner = kInter ? lane : (lane & ~(G - 1)) + (turns ? (first ? c + hc : c - hc) : c);
+  float co[kAngles], si[kAngles];
+  if (turns && pos_ok) {
+    const float* cs = p.cos_sin + pos * p.rot + (kInter ? c * kAngles : (first ? c : c - hc) * E);
+    load_angles(co, cs);
+    load_angles(si, cs + half);
+    if (!kInter && first) {
+#pragma unroll
+      for (int i = 0; i < kAngles; ++i) si[i] = -si[i];  // x cos + partner * (-+ sin)
+    }
+  }
+  const bool loc_ok = loc >= 0 && loc < p.num_slots;
+  const int64_t page = loc_ok ? div_any(static_cast<uint32_t>(loc), p.div_page) : 0;
+  const int64_t slot = page * p.c_page + (loc - page * p.page_size) * p.c_off;
+
 #pragma unroll
   for (int j = 0; j < kRounds; ++j) {
-    const int kind = at[j].kind;
+    const int h = h0 + j * kPer;
+    const int kind = h < p.heads ? 0 : (h < p.heads + p.kv_heads ? 1 : 2);
+    const int head = h - (kind > 0 ? p.heads : 0) - (kind > 1 ? p.kv_heads : 0);
     float x[E];
     unpack<kDtype>(raw[j], x);
     const unsigned char* w = kind == 0 ? p.weight[0] : (kind == 1 ? p.weight[1] : nullptr);
@@ -196,56 +243,32 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_rows(const NormParams 
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = x[i] * inv * wf[i];
     }
-    bool ok = kind >= 0;
-    if (p.rot > 0) {
-      const bool turned = kind == 0 || kind == 1;
-      const bool pos_ok = pos[j] >= 0 && pos[j] < p.max_pos;
-      if (turned && !pos_ok) {
-        ok = false;
-        if (c == 0 && at[j].head == 0 && p.status) atomicOr(p.status, HS_ST_BAD_INDEX);
+    bool ok = in_head && h < all;
+    if (kInter) {
+      if (kind < 2 && turns && pos_ok) {
+#pragma unroll
+        for (int i = 0; i < kAngles; ++i) {
+          const float u = x[2 * i], v = x[2 * i + 1];
+          x[2 * i] = u * co[i] - v * si[i];
+          x[2 * i + 1] = v * co[i] + u * si[i];
+        }
       }
-      const float* cs = p.cos_sin + (pos_ok ? pos[j] : 0) * p.rot;
-      if (p.interleaved) {
-        if (turned && pos_ok) {
+    } else if (hc > 0) {
 #pragma unroll
-          for (int i = 0; i < E; i += 2) {
-            const int d = c * E + i;
-            if (d < p.rot) {
-              const float co = __ldg(cs + (d >> 1)), si = __ldg(cs + half + (d >> 1));
-              const float a = x[i], b = x[i + 1];
-              x[i] = a * co - b * si;
-              x[i + 1] = b * co + a * si;
-            }
-          }
-        }
-      } else {
-        // half is a multiple of E: the partner of this chunk is one whole chunk
-        const int hc = half / E;
-        const bool first = c < hc, turns = c < 2 * hc;
-        const int partner = (lane & ~(G - 1)) + (turns ? (first ? c + hc : c - hc) : c);
-        float y[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) y[i] = __shfl_sync(kFullMask, x[i], partner);
-        if (turned && pos_ok && turns) {
-          const float* ca = cs + (first ? c : c - hc) * E;
-#pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const float co = __ldg(ca + i), si = __ldg(ca + half + i);
-            x[i] = first ? x[i] * co - y[i] * si : x[i] * co + y[i] * si;
-          }
-        }
+      for (int i = 0; i < E; ++i) {
+        const float y = __shfl_sync(kFullMask, x[i], partner);
+        if (kind < 2 && turns && pos_ok) x[i] = x[i] * co[i] + y * si[i];
       }
     }
-    if (kind > 0 && ok && (loc[j] < 0 || loc[j] >= p.num_slots)) {
+    if (ok && ((kind < 2 && !pos_ok) || (kind > 0 && !loc_ok))) {
       ok = false;
-      if (c == 0 && at[j].head == 0 && p.status) atomicOr(p.status, HS_ST_BAD_INDEX);
+      if (c == 0 && head == 0 && p.status) atomicOr(p.status, HS_ST_BAD_INDEX);
     }
-    if (!ok || !in_head) continue;
+    if (!ok) continue;
     if (kind == 0) {
-      *reinterpret_cast<uint4*>(p.q_out + at[j].token * p.out_token + at[j].head * p.out_head +
-                                c * 16) = pack<kDtype>(x);
+      *reinterpret_cast<uint4*>(p.q_out + t * p.out_token + head * p.out_head + c * 16) = pack<kDtype>(x);
     } else {
-      unsigned char* d = slot_at(loc[j], kind, at[j].head, p);
+      unsigned char* d = (kind == 1 ? p.cache[0] : p.cache[1]) + slot + head * p.c_head;
       if constexpr (kFp8) {
         const float* sp = kind == 1 ? p.scale[0] : p.scale[1];
         if (sp != nullptr) {
@@ -340,15 +363,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_general(const NormPara
 
 using NormFn = void (*)(const NormParams);
 
-template <int kDtype, bool kFp8>
-NormFn rows_fn(int lanes) {
-  return lanes <= 8 ? norm_rope_rows<kDtype, kFp8, 8>
-                    : (lanes <= 16 ? norm_rope_rows<kDtype, kFp8, 16>
-                                   : norm_rope_rows<kDtype, kFp8, 32>);
+template <int kDtype, bool kFp8, bool kInter>
+NormFn lanes_fn(int group) {
+  return group == 8 ? norm_rope_rows<kDtype, kFp8, 8, kInter>
+                    : (group == 16 ? norm_rope_rows<kDtype, kFp8, 16, kInter>
+                                   : norm_rope_rows<kDtype, kFp8, 32, kInter>);
 }
 template <int kDtype>
-NormFn pick_fn(bool fp8, bool rows, int lanes) {
-  if (rows) return fp8 ? rows_fn<kDtype, true>(lanes) : rows_fn<kDtype, false>(lanes);
+NormFn pick_fn(bool fp8, bool rows, int group, bool inter) {
+  if (rows && inter) return fp8 ? lanes_fn<kDtype, true, true>(group) : lanes_fn<kDtype, false, true>(group);
+  if (rows) return fp8 ? lanes_fn<kDtype, true, false>(group) : lanes_fn<kDtype, false, false>(group);
   return fp8 ? norm_rope_general<kDtype, true> : norm_rope_general<kDtype, false>;
 }
 
@@ -452,27 +476,31 @@ extern "C" hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* a, hs_stream
   p.inv_dim = 1.0f / static_cast<float>(a->head_dim);
   p.interleaved = a->flags & HS_ROPE_INTERLEAVED;
 
-  // The row kernel needs whole 16-byte chunks of a head on both sides, at most
-  // a warp of them, and (split halves) whole chunks as rotation partners.
+  // The rows kernel needs whole 16-byte chunks of a head on both sides, at most a
+  // warp of them, whole chunks turned, and aligned angles.
   const int E = static_cast<int>(16 / esz);
   const int64_t cbytes = a->cache_dtype == HS_DT_E4M3 ? E : 16;
   const bool rows = al % 16 == 0 && cal % cbytes == 0 && a->head_dim % E == 0 &&
-                    a->head_dim / E <= kWarp && (p.interleaved || (a->rot_dim / 2) % E == 0);
+                    a->head_dim / E <= kWarp && a->rot_dim % 8 == 0 &&
+                    (p.interleaved || (a->rot_dim / 2) % E == 0) &&
+                    reinterpret_cast<uintptr_t>(a->cos_sin) % 16 == 0;
   const int lanes = a->head_dim / E;
+  const int group = lanes <= 8 ? 8 : (lanes <= 16 ? 16 : 32);
   const bool fp8 = a->cache_dtype == HS_DT_E4M3;
   const NormFn fn = a->in_dtype == HS_DT_F32
-                        ? pick_fn<HS_DT_F32>(fp8, rows, lanes)
-                        : (a->in_dtype == HS_DT_F16 ? pick_fn<HS_DT_F16>(fp8, rows, lanes)
-                                                    : pick_fn<HS_DT_BF16>(fp8, rows, lanes));
-  const int group = lanes <= 8 ? 8 : (lanes <= 16 ? 16 : 32);
-  const int64_t per_block = static_cast<int64_t>(kNormWarps) * (rows ? kWarp / group * kRounds : 1);
+                        ? pick_fn<HS_DT_F32>(fp8, rows, group, p.interleaved)
+                        : (a->in_dtype == HS_DT_F16 ? pick_fn<HS_DT_F16>(fp8, rows, group, p.interleaved)
+                                                    : pick_fn<HS_DT_BF16>(fp8, rows, group, p.interleaved));
+  const uint32_t heads_per_unit = static_cast<uint32_t>(kWarp / group * kRounds);
+  const uint32_t per_token = rows ? (all + heads_per_unit - 1) / heads_per_unit : all;
+  p.div_units = FastDiv{fastdiv_magic(per_token), per_token};
   // 32-bit row indices: at most 2^31 heads at a time.
-  const int64_t max_tok = (1ll << 31) / all;
+  const int64_t max_tok = (1ll << 31) / per_token;
   for (int64_t begin = 0; begin < a->n_tokens; begin += max_tok) {
     const int64_t nt = a->n_tokens - begin < max_tok ? a->n_tokens - begin : max_tok;
     p.t_begin = begin;
-    p.rows = static_cast<uint32_t>(nt * all);
-    int64_t blocks = (p.rows + per_block - 1) / per_block;
+    p.rows = static_cast<uint32_t>(nt * per_token);
+    int64_t blocks = (static_cast<int64_t>(p.rows) + kNormWarps - 1) / kNormWarps;
     if (!rows && blocks > dev.sm_count * 6ll) blocks = dev.sm_count * 6ll;
     fn<<<static_cast<unsigned>(blocks), kNormThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
