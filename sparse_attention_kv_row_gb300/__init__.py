@@ -19,6 +19,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -668,14 +669,16 @@ def _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens
         table_stride, states, req_p, cu_p, seq_p, ks_p, vs_p, st_p)
 
 
-def _attention_workspace(dev, fields) -> int:
-    block = _capi.PAGED_ATTENTION.pack(*fields, 0, 0)
-    fn = _lib().hs_paged_attention_workspace_bytes
-    if torch._C._cuda_getDevice() == dev:
-        n = fn(block)
-    else:
-        with torch.cuda.device(dev):
-            n = fn(block)
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(dev, batch, heads, kv_heads, dim, dtype, code, max_q_len, tokens) -> int:
+    """Bytes of workspace for these sizes on this device (it depends on nothing else)."""
+    block = _capi.PagedAttentionArgs(
+        batch=batch, num_heads=heads, num_kv_heads=kv_heads, head_dim=dim, in_dtype=dtype,
+        cache_dtype=code, page_size=1, max_q_len=max_q_len, scale=1.0, n_tokens=tokens,
+        q_stride_head=dim, out_stride_head=dim, cache_stride_head=4 * dim, cache_stride_offset=1,
+        cache_stride_page=1)
+    with torch.cuda.device(dev):
+        n = int(_lib().hs_paged_attention_workspace_bytes(C.byref(block)))
     if n < 0:
         _capi.check(-n, "hs_paged_attention_workspace_bytes")
     return n
@@ -684,9 +687,9 @@ def _attention_workspace(dev, fields) -> int:
 def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
                                     out, *, max_q_len, window=0, page_size=16) -> int:
     """Bytes of workspace that ``paged_attention`` needs for tensors of these shapes and types."""
-    return _attention_workspace(*_attention_block(
-        q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, max_q_len, None, window,
-        None, None, page_size, None, None))
+    dev, f = _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out,
+                              max_q_len, None, window, None, None, page_size, None, None)
+    return _attention_workspace(dev, *f[:6], max_q_len, f[12])
 
 
 def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, *, max_q_len,
@@ -709,9 +712,9 @@ def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
         space_p = _vector(workspace, torch.uint8, n, "workspace")
         _device_of(q, workspace)
     else:
-        n = _attention_workspace(dev, fields)
+        n = _attention_workspace(dev, *fields[:6], max_q_len, fields[12])
         if n > 0:
-            workspace = q.new_empty(n, dtype=torch.uint8)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
             space_p = workspace.data_ptr()
             if stream is not None and raw != torch._C._cuda_getCurrentRawStream(dev):
                 # the allocator must not hand it out again before that stream is done
