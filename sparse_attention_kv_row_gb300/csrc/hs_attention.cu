@@ -225,7 +225,8 @@ extern "C" int64_t hs_paged_attention_workspace_bytes(const hs_paged_attention_a
   DeviceInfo dev;
   if (current_device(&dev) != HS_OK) return -static_cast<int64_t>(HS_ERR_CUDA);
   if (form == AttnForm::kTiles) return tiles_workspace(a->head_dim, dev);
-  return split_workspace(a->in_dtype, a->cache_dtype == HS_DT_E4M3, a->head_dim, dev);
+  return split_workspace(a->in_dtype, a->cache_dtype == HS_DT_E4M3, a->head_dim,
+                         a->max_q_len * (a->num_heads / a->num_kv_heads), dev);
 }
 
 extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream_t stream) {

@@ -4,9 +4,11 @@
 // With at most 16 query rows (new tokens x query heads of one kv head) every
 // key and value byte is used for a handful of products, so the bound is the HBM
 // bandwidth of reading the cache once.  The batch's work is the flattened list
-// of (request, kv head, tile of 32 keys).  It is cut into equal runs, one per
-// warp of the grid, wherever the cuts fall: ragged lengths need no scheduling,
-// and one long request fills the GPU like many short ones.  A warp streams its
+// of (request, block of kv heads, tile of 32 keys).  It is cut into equal runs,
+// one per team of warps, wherever the cuts fall: ragged lengths need no
+// scheduling, and one long request fills the GPU like many short ones.  A warp of
+// a team has one head of the block, so that the heads of a token, which lie side
+// by side, are read at the same time.  A warp streams its
 // tiles through a ring of its own in shared memory (16-byte asynchronous copies,
 // no barrier wider than the warp), multiplies them with m16n8k16 tensor
 // instructions (16 rows do not fill a 128-row tcgen05 tile, and the memory, not
@@ -17,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "hs_attention_split.cuh"
 
@@ -73,10 +76,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// A place in the flattened work: a request, a kv head and a tile, with what the
-// loads of that tile need.
+// A lane's pair of an 8x8 matrix of 16-bit values, transposed across the warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// A place in the flattened work: a request, a block of kv heads and a tile, with
+// what the loads of that tile need.
 struct Cursor {
-  int b, g;
+  int b, block;
   int tile, tile_end;
   int lo, hi;
   const int32_t* bt;
@@ -104,28 +114,28 @@ __device__ __forceinline__ Cursor cursor_at(uint32_t t, const uint32_t* prefix, 
   c.b = a;
   enter_row(c, p);
   const uint32_t per = c.tile_end - c.tile, off = t - prefix[a];
-  c.g = off / per;
-  c.tile += off - c.g * per;
+  c.block = off / per;
+  c.tile += off - c.block * per;
   return c;
 }
-__device__ __forceinline__ void step(Cursor& c, const uint32_t* prefix, const AttnParams& p) {
+__device__ __forceinline__ void step(Cursor& c, int blocks, const uint32_t* prefix, const AttnParams& p) {
   if (++c.tile < c.tile_end) return;
-  if (++c.g < p.kv_heads) {
+  if (++c.block < blocks) {
     c.tile = c.lo / kTile;
     return;
   }
-  c.g = 0;
+  c.block = 0;
   do ++c.b;
   while (c.b < p.batch && prefix[c.b + 1] == prefix[c.b]);
   if (c.b < p.batch) enter_row(c, p);
 }
 
-template <int kIn, bool kFp8, int D>
+template <int kIn, bool kFp8, int D, bool kNarrow>
 struct SplitShape {
   static constexpr int kRowBytes = kFp8 ? D : 2 * D;
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kStage = 2 * kTile * kRowBytes;  // K then V
-  static constexpr int kWarps = kStage >= 16384 ? 4 : 8;
+  static constexpr int kWarps = kStage >= 16384 ? 4 : (kStage >= 8192 || !kNarrow ? 8 : 16);
   // About 190 KB in flight per SM: at 45 GB/s per SM, four microseconds of HBM traffic.
   static constexpr int kStages = 196608 / (kStage * kWarps);
   static constexpr int kRing = kStage * kWarps * kStages;
@@ -139,25 +149,407 @@ __device__ __forceinline__ uint32_t at_chunk(int row, int ch) {
   return static_cast<uint32_t>(row * kChunks + (ch ^ x)) * 16u;
 }
 
+// Where the results of a unit, or of a part of one, go.
+struct SplitOut {
+  bool whole;
+  float* part;  // o [16][D], then log2-sum-exp [16]
+  float factor; // of v, where whole
+};
+
+// Query rows of one (request, kv head) with their running softmax; the lanes of
+// a warp hold them together.  Lane = 4 * r0 + c4.  In both forms the dims of a
+// query and of a key are multiplied in the order that suits the 8-bit rows: an
+// 8x8 matrix load gives a lane four neighbouring bytes of a row at once.
 template <int kIn, bool kFp8, int D>
-__global__ void __launch_bounds__(SplitShape<kIn, kFp8, D>::kWarps * kWarp, 1)
-    attn_split_kernel(const AttnParams p, const SplitSpace ws) {
-  using S = SplitShape<kIn, kFp8, D>;
-  constexpr bool kBf16 = kIn == HS_DT_BF16 && !kFp8;  // type of the products
-  constexpr int kSteps = D / 16;
+struct SplitTypes {
+  static constexpr bool kBf16 = kIn == HS_DT_BF16 && !kFp8;  // type of the products
+  static constexpr int kSteps = D / 16;
+  static constexpr int kChunks = (kFp8 ? D : 2 * D) / 16;
   // fp16 weights are 2^10 times as large, so that one 2^-34 of the largest still counts.
-  constexpr float kBias = kBf16 ? 0.f : 10.f;
+  static constexpr float kBias = kBf16 ? 0.f : 10.f;
+};
+// The two registers of a query's dims [16 s, 16 s + 16) that a lane holds.
+template <bool kFp8>
+__device__ __forceinline__ uint2 query_pair(const unsigned char* src, int s, int c4) {
+  if constexpr (kFp8) return __ldg(reinterpret_cast<const uint2*>(src + s * 32 + c4 * 8));
+  return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(src + s * 32 + c4 * 4)),
+                    __ldg(reinterpret_cast<const uint32_t*>(src + s * 32 + c4 * 4 + 16)));
+}
+
+// Up to 16 rows: S = Q K^T and O = P V.  A lane's rows are r0 and r0 + 8.
+template <int kIn, bool kFp8, int D>
+struct WideRows : SplitTypes<kIn, kFp8, D> {
+  using Y = SplitTypes<kIn, kFp8, D>;
+  static constexpr int kSteps = Y::kSteps, kChunks = Y::kChunks;
+  static constexpr bool kBf16 = Y::kBf16;
+  static constexpr float kBias = Y::kBias;
+  uint32_t q[kSteps][4];
+  float sc[2], o[D / 8][4], m_run[2], l_run[2];
+  int vis_hi[2], vis_lo[2];
+
+  __device__ __forceinline__ void begin(const AttnParams& p, const AttnRow& row, int g, float s_unit,
+                                        int lane) {
+    const int r0 = lane >> 2, c4 = lane & 3, rows = row.n * p.group;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = r0 + 8 * h, i = m / p.group, pos = row.len - row.n + i;
+      vis_hi[h] = m < rows ? pos + 1 : row.hi;
+      vis_lo[h] = m < rows ? seen_lo(p, pos) : row.lo;
+      const unsigned char* src = p.q + static_cast<int64_t>(row.q0 + i) * p.q_token +
+                                 static_cast<int64_t>(g * p.group + (m - i * p.group)) * p.q_head;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint2 w = make_uint2(0, 0);
+        if (m < rows) w = query_pair<kFp8>(src, s, c4);
+        q[s][h] = w.x;
+        q[s][h + 2] = w.y;
+      }
+      sc[h] = s_unit;
+      if constexpr (kFp8 && kIn == HS_DT_BF16) sc[h] *= rows_to_f16(q, h, h + 2);
+      m_run[h] = -INFINITY;
+      l_run[h] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  }
+
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int j0, bool edge, int lane) {
+    const int c4 = lane & 3;
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      uint32_t r[4];
+      if constexpr (kFp8) {
+        ldsm4(r, kt + at_chunk<kChunks>(lane, st));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma16816<false>(s[i], q[st], e4m3_to_f16(r[i] & 0xFFFF), e4m3_to_f16(r[i] >> 16));
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ldsm4(r, kt + at_chunk<kChunks>(h * 16 + (lane & 7) + ((lane >> 4) << 3), st * 2 + ((lane >> 3) & 1)));
+          mma16816<kBf16>(s[2 * h], q[st], r[0], r[1]);
+          mma16816<kBf16>(s[2 * h + 1], q[st], r[2], r[3]);
+        }
+      }
+    }
+    float mx[2] = {m_run[0], m_run[1]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int h = e >> 1, j = j0 + i * 8 + c4 * 2 + (e & 1);
+        s[i][e] *= sc[h];
+        if (edge && (j >= vis_hi[h] || j < vis_lo[h])) s[i][e] = -INFINITY;
+        mx[h] = fmaxf(mx[h], s[i][e]);
+      }
+    float back[2], ref[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 2));
+      // No key seen yet: a finite reference keeps 2^(s - ref) at 0.
+      ref[h] = (mx[h] == -INFINITY ? 0.f : mx[h]) - kBias;
+      back[h] = fast_exp2(m_run[h] - kBias - ref[h]);
+      m_run[h] = mx[h];
+      l_run[h] *= back[h];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = fast_exp2(s[i][e] - ref[e >> 1]);
+        l_run[e >> 1] += s[i][e];
+      }
+    if (!__all_sync(kFullMask, back[0] == 1.f && back[1] == 1.f)) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= back[0];
+        o[i][1] *= back[0];
+        o[i][2] *= back[1];
+        o[i][3] *= back[1];
+      }
+    }
+    // The weights are rounded to the products' type (half a step each).
+    uint32_t w[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h][0] = pack2<kBf16>(s[2 * h][0], s[2 * h][1]);
+      w[h][1] = pack2<kBf16>(s[2 * h][2], s[2 * h][3]);
+      w[h][2] = pack2<kBf16>(s[2 * h + 1][0], s[2 * h + 1][1]);
+      w[h][3] = pack2<kBf16>(s[2 * h + 1][2], s[2 * h + 1][3]);
+    }
+#pragma unroll
+    for (int dp = 0; dp < D / 16; ++dp) {
+      uint32_t r[4];
+      if constexpr (kFp8) {
+        // 16 dims of 32 keys; a lane gets two dims of two neighbouring keys.
+        ldsm4_t(r, vt + at_chunk<kChunks>(lane, dp));
+        uint32_t even[4], odd[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = __byte_perm(r[i], 0, 0x3120);
+          even[i] = e4m3_to_f16(x & 0xFFFF);
+          odd[i] = e4m3_to_f16(x >> 16);
+        }
+        mma16816<false>(o[2 * dp], w[0], even[0], even[1]);
+        mma16816<false>(o[2 * dp + 1], w[0], odd[0], odd[1]);
+        mma16816<false>(o[2 * dp], w[1], even[2], even[3]);
+        mma16816<false>(o[2 * dp + 1], w[1], odd[2], odd[3]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ldsm4_t(r, vt + at_chunk<kChunks>(h * 16 + (lane & 15), dp * 2 + (lane >> 4)));
+          mma16816<kBf16>(o[2 * dp], w[h], r[0], r[1]);
+          mma16816<kBf16>(o[2 * dp + 1], w[h], r[2], r[3]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish(const AttnParams& p, const AttnRow& row, int g, const SplitOut& to,
+                                         int lane) {
+    const int r0 = lane >> 2, c4 = lane & 3, rows = row.n * p.group;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float l = l_run[h];
+      l += __shfl_xor_sync(kFullMask, l, 1);
+      l += __shfl_xor_sync(kFullMask, l, 2);
+      const bool none = m_run[h] == -INFINITY;
+      const float f = (none ? 0.f : 1.0f / l) * to.factor;
+      const float lse = none ? -INFINITY : m_run[h] - kBias + log2f(l);
+      const int m = r0 + 8 * h;
+      if (m >= rows) continue;
+      const int i = m / p.group, head = g * p.group + (m - i * p.group);
+      const int64_t tok = row.q0 + i;
+      unsigned char* dst = p.out + tok * p.out_token + head * p.out_head;
+      if constexpr (kFp8) {
+#pragma unroll
+        for (int dp = 0; dp < D / 16; ++dp) {
+          const float x0 = o[2 * dp][2 * h] * f, x1 = o[2 * dp + 1][2 * h] * f;
+          const float x2 = o[2 * dp][2 * h + 1] * f, x3 = o[2 * dp + 1][2 * h + 1] * f;
+          const int d = dp * 16 + c4 * 4;
+          if (to.whole)
+            *reinterpret_cast<uint2*>(dst + d * 2) =
+                make_uint2(pack2<kIn == HS_DT_BF16>(x0, x1), pack2<kIn == HS_DT_BF16>(x2, x3));
+          else
+            *reinterpret_cast<float4*>(to.part + m * D + d) = make_float4(x0, x1, x2, x3);
+        }
+      } else {
+#pragma unroll
+        for (int dt = 0; dt < D / 8; ++dt) {
+          const float x0 = o[dt][2 * h] * f, x1 = o[dt][2 * h + 1] * f;
+          const int d = dt * 8 + c4 * 2;
+          if (to.whole)
+            *reinterpret_cast<uint32_t*>(dst + d * 2) = pack2<kIn == HS_DT_BF16>(x0, x1);
+          else
+            *reinterpret_cast<float2*>(to.part + m * D + d) = make_float2(x0, x1);
+        }
+      }
+      if (c4 == 0) {
+        if (!to.whole)
+          to.part[kRows * D + m] = lse;
+        else if (p.lse)
+          p.lse[tok * p.heads + head] = lse * kLn2;
+      }
+    }
+  }
+};
+
+// Up to 8 rows, the other way round: S^T = K Q^T and O^T = V^T P^T, with keys and
+// dims along the 16 rows of an instruction and the queries along its 8 columns:
+// half the products and half the registers of the wide form.  A lane's rows are
+// 2 c4 and 2 c4 + 1; of the queries it holds row r0.
+template <int kIn, bool kFp8, int D>
+struct NarrowRows : SplitTypes<kIn, kFp8, D> {
+  using Y = SplitTypes<kIn, kFp8, D>;
+  static constexpr int kSteps = Y::kSteps, kChunks = Y::kChunks;
+  static constexpr bool kBf16 = Y::kBf16;
+  static constexpr float kBias = Y::kBias;
+  uint32_t q[kSteps][2];
+  float sc[2], o[D / 16][4], m_run[2], l_run[2];
+  int vis_hi[2], vis_lo[2];
+
+  __device__ __forceinline__ void begin(const AttnParams& p, const AttnRow& row, int g, float s_unit,
+                                        int lane) {
+    const int r0 = lane >> 2, c4 = lane & 3, rows = row.n * p.group;
+    const int iq = r0 / p.group;
+    const unsigned char* src = p.q + static_cast<int64_t>(row.q0 + iq) * p.q_token +
+                               static_cast<int64_t>(g * p.group + (r0 - iq * p.group)) * p.q_head;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      uint2 w = make_uint2(0, 0);
+      if (r0 < rows) w = query_pair<kFp8>(src, s, c4);
+      q[s][0] = w.x;
+      q[s][1] = w.y;
+    }
+    sc[0] = sc[1] = s_unit;
+    if constexpr (kFp8 && kIn == HS_DT_BF16) {
+      const float f = rows_to_f16(q, 0, 1);
+      sc[0] *= __shfl_sync(kFullMask, f, c4 * 8);
+      sc[1] *= __shfl_sync(kFullMask, f, c4 * 8 + 4);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = 2 * c4 + h, pos = row.len - row.n + m / p.group;
+      vis_hi[h] = m < rows ? pos + 1 : row.hi;
+      vis_lo[h] = m < rows ? seen_lo(p, pos) : row.lo;
+      m_run[h] = -INFINITY;
+      l_run[h] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  }
+
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int j0, bool edge, int lane) {
+    const int r0 = lane >> 2;
+    float s[2][4];  // 16 keys each: (key r0, both rows), (key r0 + 8, both rows)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      uint32_t r[4];
+      if constexpr (kFp8) {
+        ldsm4(r, kt + at_chunk<kChunks>(lane, st));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a[4] = {e4m3_to_f16(r[2 * i] & 0xFFFF), e4m3_to_f16(r[2 * i + 1] & 0xFFFF),
+                                 e4m3_to_f16(r[2 * i] >> 16), e4m3_to_f16(r[2 * i + 1] >> 16)};
+          mma16816<false>(s[i], a, q[st][0], q[st][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ldsm4(r, kt + at_chunk<kChunks>(i * 16 + (lane & 15), st * 2 + (lane >> 4)));
+          mma16816<kBf16>(s[i], r, q[st][0], q[st][1]);
+        }
+      }
+    }
+    float mx[2] = {m_run[0], m_run[1]};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int h = e & 1, j = j0 + i * 16 + r0 + (e >> 1) * 8;
+        s[i][e] *= sc[h];
+        if (edge && (j >= vis_hi[h] || j < vis_lo[h])) s[i][e] = -INFINITY;
+        mx[h] = fmaxf(mx[h], s[i][e]);
+      }
+    float back[2], ref[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int d = 4; d < kWarp; d <<= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], d));
+      ref[h] = (mx[h] == -INFINITY ? 0.f : mx[h]) - kBias;
+      back[h] = fast_exp2(m_run[h] - kBias - ref[h]);
+      m_run[h] = mx[h];
+      l_run[h] *= back[h];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = fast_exp2(s[i][e] - ref[e & 1]);
+        l_run[e & 1] += s[i][e];
+      }
+    if (!__all_sync(kFullMask, back[0] == 1.f && back[1] == 1.f)) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        o[i][0] *= back[0];
+        o[i][1] *= back[1];
+        o[i][2] *= back[0];
+        o[i][3] *= back[1];
+      }
+    }
+    // The weights, rounded to the products' type, turned from (key, rows) to (row, keys).
+    uint32_t w[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i][0] = transposed(pack2<kBf16>(s[i][0], s[i][1]));
+      w[i][1] = transposed(pack2<kBf16>(s[i][2], s[i][3]));
+    }
+#pragma unroll
+    for (int dp = 0; dp < D / 16; ++dp) {
+      uint32_t r[4];
+      if constexpr (kFp8) {
+        // A lane gets two dims of two neighbouring keys: the even dims are an
+        // instruction's rows 0 to 7, the odd ones its rows 8 to 15.
+        ldsm4_t(r, vt + at_chunk<kChunks>(lane, dp));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = __byte_perm(r[2 * i], 0, 0x3120), y = __byte_perm(r[2 * i + 1], 0, 0x3120);
+          const uint32_t a[4] = {e4m3_to_f16(x & 0xFFFF), e4m3_to_f16(x >> 16),
+                                 e4m3_to_f16(y & 0xFFFF), e4m3_to_f16(y >> 16)};
+          mma16816<false>(o[dp], a, w[i][0], w[i][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ldsm4_t(r, vt + at_chunk<kChunks>(i * 16 + (lane & 7) + ((lane >> 4) << 3), dp * 2 + ((lane >> 3) & 1)));
+          mma16816<kBf16>(o[dp], r, w[i][0], w[i][1]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish(const AttnParams& p, const AttnRow& row, int g, const SplitOut& to,
+                                         int lane) {
+    const int r0 = lane >> 2, c4 = lane & 3, rows = row.n * p.group;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float l = l_run[h];
+#pragma unroll
+      for (int d = 4; d < kWarp; d <<= 1) l += __shfl_xor_sync(kFullMask, l, d);
+      const bool none = m_run[h] == -INFINITY;
+      const float f = (none ? 0.f : 1.0f / l) * to.factor;
+      const float lse = none ? -INFINITY : m_run[h] - kBias + log2f(l);
+      const int m = 2 * c4 + h;
+      if (m >= rows) continue;
+      const int i = m / p.group, head = g * p.group + (m - i * p.group);
+      const int64_t tok = row.q0 + i;
+      unsigned char* dst = p.out + tok * p.out_token + head * p.out_head;
+#pragma unroll
+      for (int dp = 0; dp < D / 16; ++dp) {
+        const float x0 = o[dp][h] * f, x1 = o[dp][2 + h] * f;
+        const int d0 = dp * 16 + (kFp8 ? 2 * r0 : r0), d1 = kFp8 ? d0 + 1 : d0 + 8;
+        if (!to.whole) {
+          to.part[m * D + d0] = x0;
+          to.part[m * D + d1] = x1;
+        } else {
+          attn_store<kIn>(dst + d0 * 2, x0);
+          attn_store<kIn>(dst + d1 * 2, x1);
+        }
+      }
+      if (r0 == 0) {
+        if (!to.whole)
+          to.part[kRows * D + m] = lse;
+        else if (p.lse)
+          p.lse[tok * p.heads + head] = lse * kLn2;
+      }
+    }
+  }
+};
+
+template <int kIn, bool kFp8, int D, bool kNarrow>
+__global__ void __launch_bounds__(SplitShape<kIn, kFp8, D, kNarrow>::kWarps * kWarp, 1)
+    attn_split_kernel(const AttnParams p, const SplitSpace ws) {
+  using S = SplitShape<kIn, kFp8, D, kNarrow>;
   extern __shared__ __align__(128) unsigned char smem[];
   uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + S::kRing);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int blocks = p.kv_heads / ws.team;
   const uint32_t total = attn_prefix(p, prefix, [&](const AttnRow& r) {
-    return static_cast<uint32_t>(attn_tiles(r, kTile)) * p.kv_heads;
+    return static_cast<uint32_t>(attn_tiles(r, kTile)) * blocks;
   });
   grid_dep_launch_dependents();
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= p.batch; b += blockDim.x) ws.prefix[b] = prefix[b];
-  const uint32_t workers = min(gridDim.x * S::kWarps, total);
-  const uint32_t me = blockIdx.x * S::kWarps + warp;
+  const uint32_t workers = min(ws.workers, total);
+  // Neighbouring runs on different SMs: a short list then spreads over all of them.
+  const uint32_t me = warp / ws.team * gridDim.x + blockIdx.x;
+  const int mate = warp % ws.team;
   if (me >= workers) return;
   const uint32_t t0 = split_begin(me, total, workers), t1 = split_begin(me + 1, total, workers);
   const uint32_t ring = smem_addr(smem) + warp * (S::kStage * S::kStages);
@@ -191,9 +583,9 @@ __global__ void __launch_bounds__(SplitShape<kIn, kFp8, D>::kWarps * kWarp, 1)
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) {
     if (next < t1) {
-      issue(off, ld.g, s);
+      issue(off, ld.block * ws.team + mate, s);
       if (++next < t1) {
-        step(ld, prefix, p);
+        step(ld, blocks, prefix, p);
         off = look_up(ld);
       }
     }
@@ -202,222 +594,42 @@ __global__ void __launch_bounds__(SplitShape<kIn, kFp8, D>::kWarps * kWarp, 1)
 
   const float ks = p.scale[0] ? __ldg(p.scale[0]) : 1.0f, vs = p.scale[1] ? __ldg(p.scale[1]) : 1.0f;
   const float s_unit = p.softmax_scale * kLog2e * ks;
-  const int r0 = lane >> 2, c4 = lane & 3;  // rows r0 and r0 + 8 of the 16; column group
-
   Cursor cu = cursor_at(t0, prefix, p);
   uint32_t t = t0;
   int slot = 0;
   while (t < t1) {
-    // ---- one (request, kv head)
+    // ---- one (request, kv head), or this run's part of it
     const AttnRow row = attn_row(p, cu.b);
-    const int rows = row.n * p.group;
-    const bool whole_front = cu.tile == row.lo / kTile;
-    uint32_t q[kSteps][4];
-    float sc[2] = {s_unit, s_unit};
-    int vis_hi[2], vis_lo[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = r0 + 8 * h;
-      const int i = m / p.group;
-      const int pos = row.len - row.n + i;
-      vis_hi[h] = m < rows ? pos + 1 : row.hi;
-      vis_lo[h] = m < rows ? seen_lo(p, pos) : row.lo;
-      const unsigned char* src = p.q + static_cast<int64_t>(row.q0 + i) * p.q_token +
-                                 static_cast<int64_t>(cu.g * p.group + (m - i * p.group)) * p.q_head;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if constexpr (kFp8) {
-          // An 8-bit tile row gives a lane four neighbouring dims at once; the
-          // queries take the same order (a permutation of the sum's terms).
-          uint2 w = make_uint2(0, 0);
-          if (m < rows) w = __ldg(reinterpret_cast<const uint2*>(src + s * 32 + c4 * 8));
-          q[s][h] = w.x;
-          q[s][h + 2] = w.y;
-        } else {
-          q[s][h] = q[s][h + 2] = 0;
-          if (m < rows) {
-            q[s][h] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 32 + c4 * 4));
-            q[s][h + 2] = __ldg(reinterpret_cast<const uint32_t*>(src + s * 32 + c4 * 4 + 16));
-          }
-        }
-      }
-      if constexpr (kFp8 && kIn == HS_DT_BF16) sc[h] *= rows_to_f16<kSteps>(q, h);
-    }
-    float o[D / 8][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    const int all_hi = row.len - row.n + 1, all_lo = seen_lo(p, row.len - 1);
-
-    for (;;) {
+    const bool from_start = cu.tile == row.lo / kTile;
+    const int g = cu.block * ws.team + mate, all_hi = row.len - row.n + 1, all_lo = seen_lo(p, row.len - 1);
+    typename std::conditional<kNarrow, NarrowRows<kIn, kFp8, D>, WideRows<kIn, kFp8, D>>::type rows;
+    rows.begin(p, row, g, s_unit, lane);
+    for (bool last = false; !last && t < t1; ++t) {
       // The tile that arrives, and the one that takes the slot freed last.
       cp_async_wait_group<S::kStages - 2>();
       __syncwarp();
-      {
-        const int to = slot == 0 ? S::kStages - 1 : slot - 1;
-        if (next < t1) {
-          issue(off, ld.g, to);
-          if (++next < t1) {
-            step(ld, prefix, p);
-            off = look_up(ld);
-          }
-        }
-        cp_async_commit();
-      }
-      const uint32_t kt = ring + slot * S::kStage, vt = kt + kTile * S::kRowBytes;
-      float s[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        uint32_t r[4];
-        if constexpr (kFp8) {
-          ldsm4(r, kt + at_chunk<S::kChunks>(lane, st));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma16816<false>(s[i], q[st], e4m3_to_f16(r[i] & 0xFFFF), e4m3_to_f16(r[i] >> 16));
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ldsm4(r, kt + at_chunk<S::kChunks>(h * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                               st * 2 + ((lane >> 3) & 1)));
-            mma16816<kBf16>(s[2 * h], q[st], r[0], r[1]);
-            mma16816<kBf16>(s[2 * h + 1], q[st], r[2], r[3]);
-          }
+      if (next < t1) {
+        issue(off, ld.block * ws.team + mate, slot == 0 ? S::kStages - 1 : slot - 1);
+        if (++next < t1) {
+          step(ld, blocks, prefix, p);
+          off = look_up(ld);
         }
       }
+      cp_async_commit();
+      const uint32_t kt = ring + slot * S::kStage;
       const int j0 = cu.tile * kTile;
-      const bool edge = j0 + kTile > all_hi || j0 < all_lo;
-      float mx[2] = {m_run[0], m_run[1]};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = e >> 1, j = j0 + i * 8 + c4 * 2 + (e & 1);
-          s[i][e] *= sc[h];
-          if (edge && (j >= vis_hi[h] || j < vis_lo[h])) s[i][e] = -INFINITY;
-          mx[h] = fmaxf(mx[h], s[i][e]);
-        }
-      float back[2], ref[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 2));
-        // No key seen yet: a finite reference keeps 2^(s - ref) at 0.
-        ref[h] = (mx[h] == -INFINITY ? 0.f : mx[h]) - kBias;
-        back[h] = fast_exp2(m_run[h] - kBias - ref[h]);
-        m_run[h] = mx[h];
-        l_run[h] *= back[h];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[i][e] = fast_exp2(s[i][e] - ref[e >> 1]);
-          l_run[e >> 1] += s[i][e];
-        }
-      if (!__all_sync(kFullMask, back[0] == 1.f && back[1] == 1.f)) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= back[0];
-          o[i][1] *= back[0];
-          o[i][2] *= back[1];
-          o[i][3] *= back[1];
-        }
-      }
-      // The weights are rounded to the products' type (half a step each).
-      uint32_t w[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        w[h][0] = pack2<kBf16>(s[2 * h][0], s[2 * h][1]);
-        w[h][1] = pack2<kBf16>(s[2 * h][2], s[2 * h][3]);
-        w[h][2] = pack2<kBf16>(s[2 * h + 1][0], s[2 * h + 1][1]);
-        w[h][3] = pack2<kBf16>(s[2 * h + 1][2], s[2 * h + 1][3]);
-      }
-#pragma unroll
-      for (int dp = 0; dp < D / 16; ++dp) {
-        uint32_t r[4];
-        if constexpr (kFp8) {
-          // 16 dims of 32 keys; a lane gets two dims of two neighbouring keys.
-          ldsm4_t(r, vt + at_chunk<S::kChunks>(lane, dp));
-          uint32_t even[4], odd[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = __byte_perm(r[i], 0, 0x3120);
-            even[i] = e4m3_to_f16(x & 0xFFFF);
-            odd[i] = e4m3_to_f16(x >> 16);
-          }
-          mma16816<false>(o[2 * dp], w[0], even[0], even[1]);
-          mma16816<false>(o[2 * dp + 1], w[0], odd[0], odd[1]);
-          mma16816<false>(o[2 * dp], w[1], even[2], even[3]);
-          mma16816<false>(o[2 * dp + 1], w[1], odd[2], odd[3]);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ldsm4_t(r, vt + at_chunk<S::kChunks>(h * 16 + (lane & 15), dp * 2 + (lane >> 4)));
-            mma16816<kBf16>(o[2 * dp], w[h], r[0], r[1]);
-            mma16816<kBf16>(o[2 * dp + 1], w[h], r[2], r[3]);
-          }
-        }
-      }
+      rows.tile(kt, kt + kTile * S::kRowBytes, j0, j0 + kTile > all_hi || j0 < all_lo, lane);
       __syncwarp();  // every lane has read this slot
       slot = slot + 1 == S::kStages ? 0 : slot + 1;
-      ++t;
-      const int g = cu.g;
-      const bool last_tile = cu.tile + 1 == cu.tile_end;
-      step(cu, prefix, p);
-      if (last_tile || t == t1) {
-        // ---- the end of the unit, or of this warp's part of it
-        const bool whole = whole_front && last_tile;
-        float inv[2], lse[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 1);
-          l_run[h] += __shfl_xor_sync(kFullMask, l_run[h], 2);
-          const bool none = m_run[h] == -INFINITY;
-          inv[h] = none ? 0.f : 1.0f / l_run[h];
-          lse[h] = none ? -INFINITY : m_run[h] - kBias + log2f(l_run[h]);
-        }
-        float* part = ws.slots + static_cast<int64_t>(2 * me + (whole_front ? 1 : 0)) * split_slot_floats(D);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int m = r0 + 8 * h;
-          if (m >= rows) continue;
-          const int i = m / p.group, head = g * p.group + (m - i * p.group);
-          const int64_t tok = row.q0 + i;
-          unsigned char* dst = p.out + tok * p.out_token + head * p.out_head;
-          const float f = whole ? inv[h] * vs : inv[h];
-          if constexpr (kFp8) {
-#pragma unroll
-            for (int dp = 0; dp < D / 16; ++dp) {
-              const float x0 = o[2 * dp][2 * h] * f, x1 = o[2 * dp + 1][2 * h] * f;
-              const float x2 = o[2 * dp][2 * h + 1] * f, x3 = o[2 * dp + 1][2 * h + 1] * f;
-              const int d = dp * 16 + c4 * 4;
-              if (whole)
-                *reinterpret_cast<uint2*>(dst + d * 2) =
-                    make_uint2(pack2<kIn == HS_DT_BF16>(x0, x1), pack2<kIn == HS_DT_BF16>(x2, x3));
-              else
-                *reinterpret_cast<float4*>(part + m * D + d) = make_float4(x0, x1, x2, x3);
-            }
-          } else {
-#pragma unroll
-            for (int dt = 0; dt < D / 8; ++dt) {
-              const float x0 = o[dt][2 * h] * f, x1 = o[dt][2 * h + 1] * f;
-              const int d = dt * 8 + c4 * 2;
-              if (whole)
-                *reinterpret_cast<uint32_t*>(dst + d * 2) = pack2<kIn == HS_DT_BF16>(x0, x1);
-              else
-                *reinterpret_cast<float2*>(part + m * D + d) = make_float2(x0, x1);
-            }
-          }
-          if (c4 == 0) {
-            if (!whole)
-              part[kRows * D + m] = lse[h];
-            else if (p.lse)
-              p.lse[tok * p.heads + head] = lse[h] * kLn2;
-          }
-        }
-        break;
+      last = cu.tile + 1 == cu.tile_end;
+      if (last || t + 1 == t1) {
+        SplitOut to;
+        to.whole = from_start && last;
+        to.factor = to.whole ? vs : 1.0f;
+        to.part = ws.slots + (2ll * (me * ws.team + mate) + (from_start ? 1 : 0)) * split_slot_floats(D);
+        rows.finish(p, row, g, to, lane);
       }
+      step(cu, blocks, prefix, p);
     }
   }
   cp_async_wait_all();
@@ -444,16 +656,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
   grid_dep_wait();  // in every block: this grid must not be done before the first kernel is
   if (row.state < 0 || m >= row.n * p.group) return;
   const uint32_t first = ws.prefix[b], total = ws.prefix[p.batch];
-  const uint32_t per = (ws.prefix[b + 1] - first) / p.kv_heads;
+  const uint32_t per = (ws.prefix[b + 1] - first) / (p.kv_heads / ws.team);
   const uint32_t workers = min(ws.workers, total);
-  const uint32_t u0 = first + g * per, u1 = u0 + per;
+  const uint32_t u0 = first + g / ws.team * per, u1 = u0 + per;
+  const int mate = g % ws.team;
   const uint32_t w0 = split_worker(u0, total, workers), w1 = split_worker(u1 - 1, total, workers);
   if (w0 == w1) return;  // one warp had the whole unit and wrote it
   const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   float mx = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (uint32_t w = w0 + grp; w <= w1; w += kGroups) {
-    const float* part = ws.slots + static_cast<int64_t>(2 * w + (w == w0 ? 1 : 0)) * split_slot_floats(D);
+    const float* part = ws.slots + (2ll * (w * ws.team + mate) + (w == w0 ? 1 : 0)) * split_slot_floats(D);
     const float lse = part[kRows * D + m];
     const float4 x = *reinterpret_cast<const float4*>(part + m * D + lane * 4);
     const float top = fmaxf(mx, lse), ref = top == -INFINITY ? 0.f : top;
@@ -502,47 +715,47 @@ struct SplitKernels {
   void (*join)(const AttnParams, const SplitSpace, int);
   int warps, ring;
 };
-template <int kIn, bool kFp8, int D>
+template <int kIn, bool kFp8, int D, bool kNarrow>
 SplitKernels kernels() {
-  using S = SplitShape<kIn, kFp8, D>;
-  return SplitKernels{attn_split_kernel<kIn, kFp8, D>, attn_join_kernel<kIn, D>, S::kWarps, S::kRing};
+  using S = SplitShape<kIn, kFp8, D, kNarrow>;
+  return SplitKernels{attn_split_kernel<kIn, kFp8, D, kNarrow>, attn_join_kernel<kIn, D>, S::kWarps, S::kRing};
 }
-SplitKernels pick(int in_dtype, bool fp8, int dim) {
-  if (in_dtype == HS_DT_BF16) {
-    if (dim == 128) return fp8 ? kernels<HS_DT_BF16, true, 128>() : kernels<HS_DT_BF16, false, 128>();
-    return fp8 ? kernels<HS_DT_BF16, true, 64>() : kernels<HS_DT_BF16, false, 64>();
-  }
-  if (dim == 128) return fp8 ? kernels<HS_DT_F16, true, 128>() : kernels<HS_DT_F16, false, 128>();
-  return fp8 ? kernels<HS_DT_F16, true, 64>() : kernels<HS_DT_F16, false, 64>();
+template <int kIn, bool kFp8>
+SplitKernels pick_form(int dim, bool narrow) {
+  if (dim == 128) return narrow ? kernels<kIn, kFp8, 128, true>() : kernels<kIn, kFp8, 128, false>();
+  return narrow ? kernels<kIn, kFp8, 64, true>() : kernels<kIn, kFp8, 64, false>();
+}
+SplitKernels pick(int in_dtype, bool fp8, int dim, bool narrow) {
+  if (in_dtype == HS_DT_BF16)
+    return fp8 ? pick_form<HS_DT_BF16, true>(dim, narrow) : pick_form<HS_DT_BF16, false>(dim, narrow);
+  return fp8 ? pick_form<HS_DT_F16, true>(dim, narrow) : pick_form<HS_DT_F16, false>(dim, narrow);
 }
 
 std::mutex g_mu;
 bool g_ready[64] = {false};
 
-template <int kIn, bool kFp8, int D>
-cudaError_t opt_in() {
-  return cudaFuncSetAttribute(attn_split_kernel<kIn, kFp8, D>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              SplitShape<kIn, kFp8, D>::kRing + kPrefixBytes);
-}
 // The kernels' shared memory needs an opt-in, once per device.
 hs_err split_setup(const DeviceInfo& dev) {
   std::lock_guard<std::mutex> lock(g_mu);
   if (g_ready[dev.device]) return HS_OK;
-  const cudaError_t e[] = {
-      opt_in<HS_DT_BF16, true, 128>(), opt_in<HS_DT_BF16, false, 128>(), opt_in<HS_DT_BF16, true, 64>(),
-      opt_in<HS_DT_BF16, false, 64>(), opt_in<HS_DT_F16, true, 128>(),  opt_in<HS_DT_F16, false, 128>(),
-      opt_in<HS_DT_F16, true, 64>(),   opt_in<HS_DT_F16, false, 64>()};
-  for (cudaError_t x : e)
-    if (x != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention: %s", cudaGetErrorString(x));
+  for (int dt : {HS_DT_F16, HS_DT_BF16})
+    for (bool fp8 : {false, true})
+      for (int dim : {64, 128})
+        for (bool narrow : {false, true}) {
+          const SplitKernels k = pick(dt, fp8, dim, narrow);
+          const cudaError_t e =
+              cudaFuncSetAttribute(reinterpret_cast<const void*>(k.main),
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, k.ring + kPrefixBytes);
+          if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention: %s", cudaGetErrorString(e));
+        }
   g_ready[dev.device] = true;
   return HS_OK;
 }
 
 }  // namespace
 
-int64_t split_workspace(int in_dtype, bool fp8, int dim, const DeviceInfo& dev) {
-  const SplitKernels k = pick(in_dtype, fp8, dim);
+int64_t split_workspace(int in_dtype, bool fp8, int dim, int rows, const DeviceInfo& dev) {
+  const SplitKernels k = pick(in_dtype, fp8, dim, rows <= kSplitNarrow);
   return kPrefixBytes + 2ll * dev.sm_count * k.warps * split_slot_floats(dim) * 4;
 }
 
@@ -550,15 +763,19 @@ hs_err split_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
                     const DeviceInfo& dev, cudaStream_t stream) {
   const hs_err err = split_setup(dev);
   if (err != HS_OK) return err;
-  const SplitKernels k = pick(in_dtype, fp8, p.dim);
+  const int row_blocks = p.max_q * p.group;
+  const SplitKernels k = pick(in_dtype, fp8, p.dim, row_blocks <= kSplitNarrow);
   SplitSpace ws;
   ws.prefix = static_cast<uint32_t*>(workspace);
   ws.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kPrefixBytes);
-  ws.workers = static_cast<uint32_t>(dev.sm_count) * k.warps;
+  // The kv heads of a token lie side by side: as many warps of a block as divide
+  // both the heads and the warps read them together, tile by tile.
+  ws.team = 1;
+  while (ws.team * 2 <= k.warps && p.kv_heads % (ws.team * 2) == 0) ws.team *= 2;
+  ws.workers = static_cast<uint32_t>(dev.sm_count * (k.warps / ws.team));
   k.main<<<dev.sm_count, k.warps * kWarp, k.ring + (p.batch + 1) * 4, stream>>>(p, ws);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention launch: %s", cudaGetErrorString(e));
-  const int row_blocks = p.max_q * p.group;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.batch * p.kv_heads * row_blocks + (p.status ? p.batch : 0)));
   cfg.blockDim = dim3(kJoinThreads);

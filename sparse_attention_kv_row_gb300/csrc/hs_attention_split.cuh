@@ -7,13 +7,15 @@
 namespace hs {
 
 constexpr int kSplitRows = 16;    // query rows of a split unit
+constexpr int kSplitNarrow = 8;   // up to which the narrow form is taken
 constexpr int kJoinThreads = 128;
 constexpr int kPrefixBytes = (kAttnMaxBatch + 64) * 4;  // per-row tile counts, summed
 
 struct SplitSpace {
   uint32_t* prefix;  // [batch + 1] tiles before each batch row
-  float* slots;      // two per worker: o [rows][D], then log2-sum-exp [rows]
-  uint32_t workers;  // runs that the grid can take
+  float* slots;      // two per warp: o [rows][D], then log2-sum-exp [rows]
+  uint32_t workers;  // runs that the grid can take, one a team
+  int team;          // warps of a team, a kv head each
 };
 __host__ __device__ constexpr int split_slot_floats(int dim) { return kSplitRows * (dim + 1); }
 
@@ -91,18 +93,16 @@ __device__ __forceinline__ float f16_factor(uint32_t top) {
   return __uint_as_float(static_cast<uint32_t>(262 - min(max(e, 73), 254)) << 23);
 }
 
-// Turns row half h of a 16-row fragment of bf16 queries into fp16 by that
-// factor and returns what undoes it.  The four lanes of a row group call it together.
-template <int kSteps>
-__device__ __forceinline__ float rows_to_f16(uint32_t (&q)[kSteps][4], int h) {
+// Turns a row of bf16 queries, held by the four lanes of a row group in the
+// registers lo and hi of every step, into fp16 by that factor and returns what
+// undoes it.
+template <int kSteps, int kRegs>
+__device__ __forceinline__ float rows_to_f16(uint32_t (&q)[kSteps][kRegs], int lo, int hi) {
   uint32_t top = 0;  // largest magnitude: bf16 bits order like whole numbers
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t w = q[s][h + 2 * e] & 0x7FFF7FFFu;
-      top = max(top, max(w & 0xFFFFu, w >> 16));
-    }
+    const uint32_t a = q[s][lo] & 0x7FFF7FFFu, b = q[s][hi] & 0x7FFF7FFFu;
+    top = max(top, max(max(a & 0xFFFFu, a >> 16), max(b & 0xFFFFu, b >> 16)));
   }
   top = max(top, __shfl_xor_sync(kFullMask, top, 1));
   top = max(top, __shfl_xor_sync(kFullMask, top, 2));
@@ -111,11 +111,9 @@ __device__ __forceinline__ float rows_to_f16(uint32_t (&q)[kSteps][4], int h) {
   for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint32_t w = q[s][h + 2 * x];
+      uint32_t& w = q[s][x ? hi : lo];
       const float a = __uint_as_float(w << 16) * up, b = __uint_as_float(w & 0xFFFF0000u) * up;
-      uint32_t r;
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-      q[s][h + 2 * x] = r;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
     }
   }
   return 1.0f / up;
@@ -140,7 +138,7 @@ __device__ __forceinline__ void attn_write_status(const AttnParams& p, int b, in
 }
 
 // hs_attention_split.cu: few queries per request.
-int64_t split_workspace(int in_dtype, bool fp8, int dim, const DeviceInfo& dev);
+int64_t split_workspace(int in_dtype, bool fp8, int dim, int rows, const DeviceInfo& dev);
 hs_err split_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace,
                     const DeviceInfo& dev, cudaStream_t stream);
 // hs_attention_tiles.cu: chunks of many queries.
