@@ -487,9 +487,10 @@ def _matrix(t, dtype, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {list(t.shape)}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    stride, last = t.stride()
+    if cols > 1 and last != 1:
         raise ValueError(f"{name} rows must be contiguous")
-    return t.data_ptr(), t.stride(0), rows, cols
+    return t.data_ptr(), stride if rows > 1 else cols, rows, cols
 
 
 def _lens(t, n, name):
@@ -557,6 +558,13 @@ def _paged_cache(k_cache, v_cache, dtype, page_size):
         raise ValueError("caches must be 3-D or 4-D")
     if dim > 1 and last != 1:
         raise ValueError("caches need contiguous dims")
+    # (an axis of one entry may have any stride)
+    if heads == 1:
+        head = dim
+    if page_size == 1:
+        off = heads * head
+    if pages <= 1:
+        page = page_size * off
     if kind is dtype:
         size = 4 if dtype is torch.float32 else 2
         return _FP8_IN[dtype], heads, dim, page * size, off * size, head * size, pages
@@ -570,8 +578,12 @@ def _heads(t, dtype, name, tokens, heads, dim):
     if t.shape != (tokens, heads, dim) or (dim > 1 and t.stride(2) != 1):
         raise ValueError(f"{name} must be {[tokens, heads, dim]} with a contiguous last dim, got "
                          f"{list(t.shape)}")
-    strides = t.stride()
-    return t.data_ptr(), strides[0], strides[1]
+    token, head, _ = t.stride()
+    if heads == 1:
+        head = dim
+    if tokens <= 1:
+        token = heads * head
+    return t.data_ptr(), token, head
 
 
 def _cache_scale(t, code, name):
@@ -605,7 +617,7 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k
     k_a = _heads(k, dt, "k", T, kv_heads, dim)
     v_a = _heads(v, dt, "v", T, kv_heads, dim)
     o_a = _heads(q_out, dt, "q_out", T, heads, dim)
-    if o_a[0] == q_a[0] and o_a != q_a:
+    if o_a[0] == q_a[0] and o_a != q_a and T > 0:
         raise ValueError("q_out may be q itself, not another view of its memory")
     qw_p = 0 if q_weight is None else _vector(q_weight, dt, dim, "q_weight")
     kw_p = 0 if k_weight is None else _vector(k_weight, dt, dim, "k_weight")

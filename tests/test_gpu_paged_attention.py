@@ -325,3 +325,20 @@ def test_empty_calls(dev):
     hs.paged_attention(q, kc, kc, torch.zeros(0, 0, dtype=torch.int32, device=dev), i32(), i32(0),
                        i32(), q.clone(), max_q_len=0)
     torch.cuda.synchronize()
+
+
+def test_axes_of_one_entry_may_have_any_stride(dev):
+    """One request, one token, one head, one page: torch gives such axes strides that mean nothing."""
+    hs = _hs()
+    g = torch.Generator(device=dev).manual_seed(1)
+    for dim in (128, 40):
+        q = torch.randn(dim, generator=g, device=dev).to(torch.bfloat16).as_strided((1, 1, dim), (0, 3, 1))
+        kv = torch.randn(2, 1, 16, 1, dim, generator=g, device=dev).to(torch.bfloat16)
+        kc, vc = (c.as_strided((1, 16, 1, dim), (1, dim, 1, 1), c.storage_offset()) for c in kv)
+        table = torch.zeros(1, dtype=torch.int32, device=dev).as_strided((1, 1), (0, 0))
+        out = torch.zeros(dim, dtype=torch.bfloat16, device=dev).as_strided((1, 1, dim), (7, 0, 1))
+        i = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+        hs.paged_attention(q, kc, vc, table, i(0), i(0, 1), i(9), out, max_q_len=1)
+        k, v = kv[0, 0, :9, 0].double(), kv[1, 0, :9, 0].double()
+        w = torch.softmax(k @ q[0, 0].double() * dim ** -0.5, 0)
+        assert bool(((out[0, 0].double() - w @ v).abs() <= 2.0 ** -6).all())
