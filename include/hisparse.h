@@ -597,8 +597,15 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  * widened exactly; bf16 queries are then taken as fp16 after a power of two per
  * row, exact to 2^-22 of the row's largest.  Results do not depend on what else
  * is in the batch, except through the order of fp32 sums.
- * Limits: head_dim <= 512, num_heads a multiple of num_kv_heads, batch <= 2048,
- * L <= INT32_MAX (else HS_ERR_UNSUPPORTED, or HS_ST_BAD_STATE for L).
+ * Time-out: the waits of the kernel for long chunks are bounded.  If one runs out
+ * (the GPU did not complete a copy or a product within two seconds), every row
+ * reports HS_ST_TIMEOUT and the outputs of the call are undefined; treat the
+ * context as suspect.
+ * Limits: head_dim <= 512, num_heads a multiple of num_kv_heads, batch <= 2048
+ * (else HS_ERR_UNSUPPORTED); L at most 2^30, and so short that 32-bit whole numbers
+ * count the batch's tiles: batch * num_kv_heads * L < 2^36, and (n_tokens *
+ * max(1, num_heads / num_kv_heads / 128) / 256 + batch) * num_kv_heads * L < 2^38
+ * are enough (HS_ST_BAD_STATE for a longer row).
  */
 typedef struct hs_paged_attention_args {
   int32_t batch, num_heads, num_kv_heads, head_dim;
@@ -626,6 +633,18 @@ typedef struct hs_paged_attention_args {
 int64_t hs_paged_attention_workspace_bytes(const hs_paged_attention_args* args);
 
 hs_err hs_paged_attention(const hs_paged_attention_args* args, hs_stream_t stream);
+
+/*
+ * hs_paged_attention_timeout_selftest -- hs_paged_attention with every bounded
+ * wait that is not over at once made to run out, so that the time-out path runs
+ * without any GPU fault or hang: what is in flight is still waited out before a
+ * block ends.  Every row must report HS_ST_TIMEOUT beside its other bits, and the
+ * next call must be right.  Defined by this library.  Errors: those of
+ * hs_paged_attention, and HS_ERR_ARG for a call whose kernels have no such wait
+ * (at most 16 query rows a kv head, or not for the tensor cores).
+ */
+hs_err hs_paged_attention_timeout_selftest(const hs_paged_attention_args* args,
+                                           hs_stream_t stream);
 
 /*
  * hs_probe_read -- measurement utility, not part of the method: stream-read

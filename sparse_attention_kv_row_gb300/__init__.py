@@ -33,7 +33,8 @@ __all__ = ["swap_in", "swap_in_args", "make_swap_in_args", "gather_misses", "fp8
            "swap_in_layers", "swap_in_layers_timeout_selftest", "layer_args_array",
            "store_kv", "transfer_kv",
            "transfer_kv_layers", "probe_read", "assign_slots", "qk_norm_rope_store",
-           "paged_attention", "paged_attention_workspace_bytes", "swap_in_smem_bytes", "library_path",
+           "paged_attention", "paged_attention_workspace_bytes",
+           "paged_attention_timeout_selftest", "swap_in_smem_bytes", "library_path",
            "HisparseError", "SwapInArgs"]
 
 
@@ -714,6 +715,23 @@ def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
     last ``window`` keys only; ``lse`` [T, heads] gets the softmax's log-sum-exp.  ``workspace``
     (uint8, 256-byte aligned, ``paged_attention_workspace_bytes`` of it) may be passed to keep
     one for a captured graph; otherwise one is allocated for the call."""
+    _attend("hs_paged_attention", _lib().hs_paged_attention, q, k_cache, v_cache, block_table,
+            req_state, cu_q, seq_lens, out, max_q_len, scale, window, k_scale, v_scale, page_size,
+            lse, status, workspace, stream)
+
+
+def paged_attention_timeout_selftest(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
+                                     out, *, max_q_len, k_scale=None, v_scale=None, page_size=16,
+                                     status=None, stream=None) -> None:
+    """hs_paged_attention with every bounded wait made to run out at once: every row must
+    report HS_ST_TIMEOUT, and later calls be right."""
+    _attend("hs_paged_attention_timeout_selftest", _lib().hs_paged_attention_timeout_selftest, q,
+            k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, max_q_len, None, 0,
+            k_scale, v_scale, page_size, None, status, None, stream)
+
+
+def _attend(where, fn, q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, max_q_len,
+            scale, window, k_scale, v_scale, page_size, lse, status, workspace, stream) -> None:
     dev, fields = _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
                                    out, max_q_len, scale, window, k_scale, v_scale, page_size,
                                    lse, status)
@@ -731,5 +749,4 @@ def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
             if stream is not None and raw != torch._C._cuda_getCurrentRawStream(dev):
                 # the allocator must not hand it out again before that stream is done
                 workspace.record_stream(torch.cuda.ExternalStream(raw, device=dev))
-    _launch(dev, "hs_paged_attention", _lib().hs_paged_attention,
-            _capi.PAGED_ATTENTION.pack(*fields, space_p, n), raw)
+    _launch(dev, where, fn, _capi.PAGED_ATTENTION.pack(*fields, space_p, n), raw)

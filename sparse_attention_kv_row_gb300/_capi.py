@@ -35,7 +35,8 @@ EXPORTS = ("hs_swap_in", "hs_swap_in_smem_bytes", "hs_store_kv", "hs_transfer_kv
            "hs_gather_misses", "hs_fp8_store_kv", "hs_invalidate_tokens", "hs_probe_read", "hs_err_string", "hs_status_string", "hs_last_error",
            "hs_abi_version", "hs_wait_selftest", "hs_swap_in_timeout_selftest",
            "hs_swap_in_layers", "hs_swap_in_layers_timeout_selftest", "hs_assign_slots",
-           "hs_qk_norm_rope_store", "hs_paged_attention", "hs_paged_attention_workspace_bytes")
+           "hs_qk_norm_rope_store", "hs_paged_attention", "hs_paged_attention_workspace_bytes",
+           "hs_paged_attention_timeout_selftest")
 
 
 class SwapInArgs(C.Structure):
@@ -180,6 +181,8 @@ def load() -> C.CDLL:
         lib.hs_qk_norm_rope_store.restype = C.c_int
         lib.hs_paged_attention.argtypes = [vp, vp]
         lib.hs_paged_attention.restype = C.c_int
+        lib.hs_paged_attention_timeout_selftest.argtypes = [vp, vp]
+        lib.hs_paged_attention_timeout_selftest.restype = C.c_int
         lib.hs_paged_attention_workspace_bytes.argtypes = [vp]
         lib.hs_paged_attention_workspace_bytes.restype = i64
         lib.hs_err_string.argtypes = [i32]

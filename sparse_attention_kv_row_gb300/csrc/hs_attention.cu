@@ -161,6 +161,7 @@ AttnForm attn_form(const hs_paged_attention_args* a) {
 
 // Whether every address that the tensor-core kernels form allows 16-byte accesses.
 bool attn_aligned(const AttnParams& p) {
+  if (p.num_pages == 0) return false;  // no cache to form addresses in
   const uintptr_t all =
       reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out) |
       reinterpret_cast<uintptr_t>(p.cache[0]) | reinterpret_cast<uintptr_t>(p.cache[1]) |
@@ -208,6 +209,17 @@ AttnParams make_params(const hs_paged_attention_args* a) {
   p.max_q = a->max_q_len;
   p.window = a->window;
   p.n_tokens = a->n_tokens;
+  // Whole numbers of 32 bits count the batch's tiles: of 32 keys for every row and
+  // kv head, or of 128 (and a unit's fixed ones) for every unit of whole queries
+  // in two halves of 128 rows.
+  const int64_t most = (1ll << 31) - 1, rows = a->batch > 0 ? a->batch : 1;
+  const int64_t per_unit = 2 * (p.group < 128 ? 128 / p.group : 1);
+  const int64_t units = a->n_tokens / per_unit + rows;
+  const int64_t split = most / (rows * p.kv_heads) * 32 - 32;
+  const int64_t tiles = (most / (units * p.kv_heads) - 8) * 128;
+  p.max_len = 1ll << 30;
+  if (split < p.max_len) p.max_len = split;
+  if (tiles < p.max_len) p.max_len = tiles;
   p.softmax_scale = a->scale;
   return p;
 }
@@ -229,9 +241,9 @@ extern "C" int64_t hs_paged_attention_workspace_bytes(const hs_paged_attention_a
                          a->max_q_len * (a->num_heads / a->num_kv_heads), dev);
 }
 
-extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream_t stream) {
-  hs::CallRange range("hs_paged_attention");
-  using namespace hs;
+namespace hs {
+namespace {
+hs_err attend(const hs_paged_attention_args* a, bool give_up, hs_stream_t stream) {
   clear_error();
   hs_err err = check_args(a);
   if (err != HS_OK) return err;
@@ -260,8 +272,12 @@ extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = a->cache_dtype == HS_DT_E4M3;
   const AttnForm form = attn_aligned(p) ? attn_form(a) : AttnForm::kGeneral;
-  if (form == AttnForm::kSplit) return split_launch(p, a->in_dtype, fp8, a->workspace, dev, st);
-  if (form == AttnForm::kTiles) return tiles_launch(p, a->in_dtype, fp8, a->workspace, dev, st);
+  if (form == AttnForm::kSplit && !give_up)
+    return split_launch(p, a->in_dtype, fp8, a->workspace, dev, st);
+  if (form == AttnForm::kTiles)
+    return tiles_launch(p, a->in_dtype, fp8, a->workspace, give_up, dev, st);
+  if (give_up)
+    return fail(HS_ERR_ARG, "hs_paged_attention_timeout_selftest: this call has no bounded waits");
   if (a->n_tokens > 0 && a->max_q_len > 0) {
     const GenFn fn = a->in_dtype == HS_DT_F32
                          ? general_fn<HS_DT_F32>(fp8, p.dim)
@@ -277,4 +293,18 @@ extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream
   if (e != cudaSuccess)
     return fail(HS_ERR_CUDA, "hs_paged_attention launch: %s", cudaGetErrorString(e));
   return HS_OK;
+}
+
+}  // namespace
+}  // namespace hs
+
+extern "C" hs_err hs_paged_attention(const hs_paged_attention_args* a, hs_stream_t stream) {
+  hs::CallRange range("hs_paged_attention");
+  return hs::attend(a, false, stream);
+}
+
+extern "C" hs_err hs_paged_attention_timeout_selftest(const hs_paged_attention_args* a,
+                                                      hs_stream_t stream) {
+  hs::CallRange range("hs_paged_attention_timeout_selftest");
+  return hs::attend(a, true, stream);
 }

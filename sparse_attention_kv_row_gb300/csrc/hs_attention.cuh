@@ -38,7 +38,7 @@ struct AttnParams {
   int32_t* status;
   int32_t batch, heads, kv_heads, group, dim, flags;
   int32_t max_q, window;
-  int64_t n_tokens;
+  int64_t n_tokens, max_len;
   float softmax_scale;
 };
 
@@ -59,7 +59,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b) {
   const int64_t q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
   if (state < 0) return r;
   if (state >= p.num_states || q0 < 0 || q1 < q0 || q1 > p.n_tokens || q1 - q0 > p.max_q ||
-      len > static_cast<int64_t>(p.table_blocks) * p.page_size || len > INT32_MAX) {
+      len > static_cast<int64_t>(p.table_blocks) * p.page_size || len > p.max_len) {
     r.status = HS_ST_BAD_STATE;
     return r;
   }
@@ -78,7 +78,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b) {
 // The keys [lo, hi) that the query at position pos sees; hi <= lo for none.
 __device__ __forceinline__ int seen_hi(int pos) { return pos + 1; }
 __device__ __forceinline__ int seen_lo(const AttnParams& p, int pos) {
-  return p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+  return p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
 }
 
 // Byte offset of key j of table row `bt` in either cache, head excluded; -1

@@ -143,7 +143,7 @@ hs_err split_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
                     const DeviceInfo& dev, cudaStream_t stream);
 // hs_attention_tiles.cu: chunks of many queries.
 int64_t tiles_workspace(int dim, const DeviceInfo& dev);
-hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace,
+hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace, bool give_up,
                     const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace hs

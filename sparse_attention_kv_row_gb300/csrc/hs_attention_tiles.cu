@@ -54,6 +54,7 @@ struct TilesParams : AttnParams {
   FastDiv by_group;
   int half_queries;  // whole queries in 128 rows
   int box_keys;      // keys per tensor-map box of the cache, 0: all through registers
+  int give_up;       // (self-test) every wait that is not over at once runs out
 };
 
 struct TilesSpace {
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.raw_empty[i], kLoaders);
     }
     fence_mbar_init();
-    sh.dead = 0;
+    sh.dead = p.give_up;
   }
   if (warp == 12) tmem_alloc(&sh.tmem, 512);
   const uint32_t total = attn_prefix(p, prefix, [&](const AttnRow& r) { return row_cost(p, r); });
@@ -780,7 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t base = kFp8 ? ring + S::kStages * S::kStage : ring;
         const bool mine = lane < kKeys / p.box_keys;
         RingAt<kSlots ? kSlots : 1> kv;
-        uint32_t u_n = 0, issued = 0, edges = 0;
+        uint32_t u_n = 0, edges = 0;
+        uint32_t out = 0, out_phase = 0;  // slots with loads to see in, and their phases
+        bool edge_out = false, q_out = false;
+        uint32_t q_phase = 0;
         bool ok = true;
         auto reached = [&](uint64_t* bar, uint32_t phase) {
           return __all_sync(kFullMask, wait_for(bar, phase, dead));
@@ -808,7 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < (kFp8 ? 1 : S::kPanels); ++x)
               tensor_load_4d(dst + x * S::kPanel, v ? &v_map : &k_map, x * 64, w.g, in_page, page, bar);
           }
-          ++issued;
+          if (bar == &sh.edge) {
+            edge_out = true;
+          } else {
+            out |= 1u << kv.stage;
+            out_phase = (out_phase & ~(1u << kv.stage)) | kv.phase << kv.stage;
+          }
         };
         for (; more && ok; more = w.next(prefix, p), ++u_n) {
           int32_t e = find(w.unit.tile + w.k0);
@@ -822,6 +831,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               // The first K tile does not wait for the queries' buffer.  Rows past
               // the unit's last query bring others', and are not written.
               if (!(ok = reached(&sh.q_empty, (u_n & 1) ^ 1))) break;
+              q_out = true;
+              q_phase = u_n & 1;
               if (lane == 0) {
                 uint64_t* bar = kHalve ? &sh.q_raw : &sh.q_full;
                 if (!kHalve) sh.unit[u_n & 1] = make_int2(w.unit.queries, w.k1 - w.k0);
@@ -842,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               load(tile, e, true, &sh.edge);
               if (!(ok = reached(&sh.edge, edges & 1))) break;
               ++edges;
+              edge_out = false;
               const uint32_t at = base + kv.stage * kBytes;
               const int gone = max(0, min(lo, kKeys)), from = max(gone, min(hi, kKeys));
               const int rows = gone + kKeys - from;
@@ -870,10 +882,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) {
           // What is still on its way writes shared memory: see it in.
           volatile int no = 0;
-          for (uint32_t n = issued > kSlots ? issued - kSlots : 0; n < issued; ++n)
-            wait_for(&full[n % (kSlots ? kSlots : 1)], (n / (kSlots ? kSlots : 1)) & 1, &no);
-          wait_for(&sh.edge, edges & 1, &no);
-          wait_for(kHalve ? &sh.q_raw : &sh.q_full, u_n & 1, &no);
+          for (int i = 0; i < kSlots; ++i)
+            if (out >> i & 1u) wait_for(&full[i], out_phase >> i & 1u, &no);
+          if (edge_out) wait_for(&sh.edge, edges & 1, &no);
+          if (q_out) wait_for(kHalve ? &sh.q_raw : &sh.q_full, q_phase, &no);
         }
       }
       __syncwarp();
@@ -1138,7 +1150,7 @@ int64_t tiles_workspace(int dim, const DeviceInfo& dev) {
   return kTilesHead + 2ll * dev.sm_count * tiles_slot_floats(dim) * 4;
 }
 
-hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace,
+hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace, bool give_up,
                     const DeviceInfo& dev, cudaStream_t stream) {
   if (dev.sm_count > 2048) return fail(HS_ERR_UNSUPPORTED, "hs_paged_attention: %d SMs", dev.sm_count);
   const hs_err err = tiles_setup(dev);
@@ -1157,6 +1169,7 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   tp.by_group = FastDiv{fastdiv_magic(group), group};
   tp.half_queries = kHalf / p.group;
   tp.box_keys = 0;
+  tp.give_up = give_up;
   CUtensorMap maps[3] = {};
   if (p.page_size % kKeys == 0)
     tp.box_keys = kKeys;

@@ -342,3 +342,44 @@ def test_axes_of_one_entry_may_have_any_stride(dev):
         k, v = kv[0, 0, :9, 0].double(), kv[1, 0, :9, 0].double()
         w = torch.softmax(k @ q[0, 0].double() * dim ** -0.5, 0)
         assert bool(((out[0, 0].double() - w @ v).abs() <= 2.0 ** -6).all())
+
+
+@pytest.mark.parametrize("dtype,cache,page,dim", [("bf16", "same", 16, 128), ("f16", "same", 48, 64),
+                                                  ("bf16", "fp8", 64, 128), ("f16", "fp8", 3, 128)])
+def test_waits_that_run_out_hand_control_back(dev, dtype, cache, page, dim):
+    """Every bounded wait of the long-chunk kernel gives up at once: all rows report the
+    time-out, and the calls that follow are right."""
+    hs = _hs()
+    x = PagedInputs(CHUNKS, heads=8, kv_heads=2, dim=dim, dtype=dtype, cache=cache, page=page, seed=3)
+    t = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    sc = [torch.tensor([v], device=dev) if x.fp8 else None for v in (x.ks, x.vs)]
+    args = (x.q.to(dev), x.kc.to(dev), x.vc.to(dev), t(x.table), t(x.req), t(x.cu), t(x.seq))
+    for _ in range(3):
+        status = torch.zeros(len(CHUNKS), dtype=torch.int32, device=dev)
+        hs.paged_attention_timeout_selftest(*args, torch.zeros_like(args[0]), max_q_len=x.max_q,
+                                            k_scale=sc[0], v_scale=sc[1], page_size=page, status=status)
+        assert status.tolist() == [16] * len(CHUNKS)
+        x.check(hs, dev, True)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_longest_rows_are_bounded(dev, n):
+    """A length past 2^30 is refused, for its row alone."""
+    hs = _hs()
+    x = PagedInputs([(20, 1), (30, 1), (9, n)], heads=2, kv_heads=1, dim=64, dtype="bf16",
+                    page=1 << 15, seed=3)
+    wide = np.zeros((x.table.shape[0], 1 << 16), np.int32)
+    wide[:, :1] = x.table
+    x.table = wide
+    x.seq[1] = (1 << 30) + 1
+    t = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    status = torch.zeros(3, dtype=torch.int32, device=dev)
+    out = torch.full(x.q.shape, -7.0, dtype=torch.bfloat16, device=dev)
+    hs.paged_attention(x.q.to(dev), x.kc.to(dev), x.vc.to(dev), t(x.table), t(x.req), t(x.cu), t(x.seq),
+                       out, max_q_len=n, page_size=1 << 15, status=status)
+    assert status.tolist() == [0, 32, 0]
+    x.req[1] = -1
+    ref = x.plain()
+    tol, _ = x.tolerance(ref, True)
+    assert bool(((out.cpu().double() - ref[0]).abs() <= tol)[ref[5]].all())
+    assert bool((out[1] == -7).all())
