@@ -457,12 +457,18 @@ def _device_of(first, *others) -> int:
     return dev
 
 
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else (
+    torch.cuda.current_device)
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
 def _raw_stream(stream, dev) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 def _launch(dev, where, fn, *args) -> None:
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         code = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -475,7 +481,7 @@ def _vector(t, dtype, n, name):
     """A contiguous 1-D tensor of n entries; returns its address."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} entries, got "
                          f"{list(t.shape)}")
     return t.data_ptr()
@@ -485,9 +491,10 @@ def _matrix(t, dtype, name):
     """A 2-D tensor with contiguous rows; returns its address, row stride, rows and columns."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {list(t.shape)}")
-    rows, cols = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {list(shape)}")
+    rows, cols = shape
     stride, last = t.stride()
     if cols > 1 and last != 1:
         raise ValueError(f"{name} rows must be contiguous")
@@ -576,10 +583,10 @@ def _heads(t, dtype, name, tokens, heads, dim):
     """Address, token and head strides of [tokens, heads, dim] with contiguous dims."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (tokens, heads, dim) or (dim > 1 and t.stride(2) != 1):
+    token, head, last = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.shape != (tokens, heads, dim) or (dim > 1 and last != 1):
         raise ValueError(f"{name} must be {[tokens, heads, dim]} with a contiguous last dim, got "
                          f"{list(t.shape)}")
-    token, head, _ = t.stride()
     if heads == 1:
         head = dim
     if tokens <= 1:
@@ -746,7 +753,7 @@ def _attend(where, fn, q, k_cache, v_cache, block_table, req_state, cu_q, seq_le
         if n > 0:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
             space_p = workspace.data_ptr()
-            if stream is not None and raw != torch._C._cuda_getCurrentRawStream(dev):
+            if stream is not None and raw != _current_stream(dev):
                 # the allocator must not hand it out again before that stream is done
                 workspace.record_stream(torch.cuda.ExternalStream(raw, device=dev))
     _launch(dev, where, fn, _capi.PAGED_ATTENTION.pack(*fields, space_p, n), raw)

@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(SplitShape<kIn, kFp8, D, kNarrow>::kWarps * kW
   const uint32_t ring = smem_addr(smem) + warp * (S::kStage * S::kStages);
 
   // ---- loads: lane l looks up key l of a tile; then every lane copies chunks
-  Cursor ld = cursor_at(t0, prefix, p);
+  Cursor cu = cursor_at(t0, prefix, p), ld = cu;
   auto look_up = [&](const Cursor& c) -> int64_t {
     const int j = c.tile * kTile + lane;
     return j >= c.lo && j < c.hi ? key_offset(p, c.bt, j) : -1;
@@ -594,7 +594,6 @@ __global__ void __launch_bounds__(SplitShape<kIn, kFp8, D, kNarrow>::kWarps * kW
 
   const float ks = p.scale[0] ? __ldg(p.scale[0]) : 1.0f, vs = p.scale[1] ? __ldg(p.scale[1]) : 1.0f;
   const float s_unit = p.softmax_scale * kLog2e * ks;
-  Cursor cu = cursor_at(t0, prefix, p);
   uint32_t t = t0;
   int slot = 0;
   while (t < t1) {
