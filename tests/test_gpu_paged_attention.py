@@ -246,10 +246,12 @@ def test_one_long_context(dev):
 def test_many_short_requests(dev):
     lens = [(i % 7, 1 + i % 3) for i in range(700)]
     x = PagedInputs(lens, heads=2, kv_heads=1, dim=64, dtype="bf16", page=16, seed=6)
-    x.check(_hs(), dev, True)
+    _, _, status = x.check(_hs(), dev, True)
+    assert not bool(status.any())
     lens = [(i % 7, 20 + i % 30) for i in range(150)]
     x = PagedInputs(lens, heads=2, kv_heads=1, dim=64, dtype="bf16", page=16, seed=6)
-    x.check(_hs(), dev, True)
+    _, _, status = x.check(_hs(), dev, True)
+    assert not bool(status.any())
 
 
 def test_offsets_past_32_bits(dev):
@@ -360,6 +362,15 @@ def test_waits_that_run_out_hand_control_back(dev, dtype, cache, page, dim):
                                             k_scale=sc[0], v_scale=sc[1], page_size=page, status=status)
         assert status.tolist() == [16] * len(CHUNKS)
         x.check(hs, dev, True)
+
+
+@pytest.mark.parametrize("cache,page", [("same", 16), ("fp8", 16), ("same", 48)])
+def test_many_units_of_one_tile(dev, cache, page):
+    """Several short units per SM, with one half and with two in turn: no wait runs out."""
+    lens = [(0, 64 if i % 3 else 20) for i in range(70)]
+    x = PagedInputs(lens, heads=32, kv_heads=8, dim=64, dtype="bf16", cache=cache, page=page, seed=3)
+    _, _, status = x.check(_hs(), dev, True)
+    assert not bool(status.any())
 
 
 @pytest.mark.parametrize("n", [1, 40])
