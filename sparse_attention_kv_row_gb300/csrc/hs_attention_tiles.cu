@@ -47,13 +47,17 @@ static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 512, "65536 registers
 constexpr float kRaise = 8.f;      // log2 of how far weights may exceed 1
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// A unit's fixed cost in tiles: its queries' way in and its outputs' way out.
-constexpr int kUnitCost = 3;
+// A unit's fixed cost in tiles: its queries' way in and its outputs' way out
+// (about 4 us over a 16-bit cache and 6 over an FP8 one, to 1.6 and 1.8 a tile;
+// with 2 and 3 four 2048-token prompts took 117 and 119 us, a mixed FP8 batch 204
+// and 202).
+constexpr int unit_cost(bool fp8) { return fp8 ? 3 : 2; }
 
 struct TilesParams : AttnParams {
   FastDiv by_group;
   int half_queries;  // whole queries in 128 rows
   int box_keys;      // keys per tensor-map box of the cache, 0: all through registers
+  int unit_cost;     // see unit_cost()
   int give_up;       // (self-test) every wait that is not over at once runs out
 };
 
@@ -110,7 +114,7 @@ __device__ __forceinline__ bool next_unit(Unit& u, const TilesParams& p, const A
 __device__ __forceinline__ uint32_t row_cost(const TilesParams& p, const AttnRow& r) {
   uint32_t n = 0;
   Unit u = first_unit(p, r);
-  do n += u.tiles + kUnitCost;
+  do n += u.tiles + p.unit_cost;
   while (next_unit(u, p, r));
   return n * p.kv_heads;
 }
@@ -124,8 +128,8 @@ struct Walk {
   Unit unit;
   int k0, k1;         // this run's tiles of the unit (relative)
 
-  __device__ __forceinline__ void clip(uint32_t c0) {
-    const int64_t a = static_cast<int64_t>(c0) - u0 - kUnitCost, e = static_cast<int64_t>(c1) - u0 - kUnitCost;
+  __device__ __forceinline__ void clip(uint32_t c0, int cost) {
+    const int64_t a = static_cast<int64_t>(c0) - u0 - cost, e = static_cast<int64_t>(c1) - u0 - cost;
     k0 = a > 0 ? static_cast<int>(a) : 0;
     k1 = e < unit.tiles ? static_cast<int>(e) : unit.tiles;
   }
@@ -146,20 +150,20 @@ struct Walk {
     u0 = prefix[b];
     unit = first_unit(p, row);
     for (;;) {
-      const uint32_t all = static_cast<uint32_t>(unit.tiles + kUnitCost) * p.kv_heads;
+      const uint32_t all = static_cast<uint32_t>(unit.tiles + p.unit_cost) * p.kv_heads;
       if (c0 - u0 < all) break;
       u0 += all;
       next_unit(unit, p, row);
     }
-    g = (c0 - u0) / (unit.tiles + kUnitCost);
-    u0 += static_cast<uint32_t>(g) * (unit.tiles + kUnitCost);
-    clip(c0);
+    g = (c0 - u0) / (unit.tiles + p.unit_cost);
+    u0 += static_cast<uint32_t>(g) * (unit.tiles + p.unit_cost);
+    clip(c0, p.unit_cost);
     return k1 > k0 || next(prefix, p);
   }
   // The next unit with tiles in the run.
   __device__ __forceinline__ bool next(const uint32_t* prefix, const TilesParams& p) {
-    u0 += unit.tiles + kUnitCost;
-    if (u0 + kUnitCost >= c1) return false;
+    u0 += unit.tiles + p.unit_cost;
+    if (u0 + p.unit_cost >= c1) return false;
     if (++g == p.kv_heads) {
       g = 0;
       if (!next_unit(unit, p, row)) {
@@ -169,7 +173,7 @@ struct Walk {
         unit = first_unit(p, row);
       }
     }
-    clip(u0);
+    clip(u0, p.unit_cost);
     return true;
   }
 };
@@ -367,9 +371,13 @@ struct Loader {
       const float up = f16_factor(top);
       sh.q_factor[buf][h * kHalf + tid] = 1.0f / up;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t x = at + (c / 8) * S::kPanel + in_panel(tid, c % 8);
-        st_shared_v4(x, to_f16(ld_shared_v4(x), up));
+      for (int x = 0; x < S::kPanels; ++x) {
+        const uint32_t panel = at + x * S::kPanel;
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = ld_shared_v4(panel + in_panel(tid, c));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) st_shared_v4(panel + in_panel(tid, c), to_f16(v[c], up));
       }
     }
   }
@@ -693,13 +701,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t from = raw_at + raw.stage * S::kRaw, to = ring + kv.stage * S::kStage;
         const int j0 = (w.unit.tile + k) * kKeys;
         const bool edge = v && (j0 < w.row.lo || j0 + kKeys > w.row.hi);
+        // Loads ahead of conversions, kBatch chunks at a time.
+        constexpr int kAll = kKeys * S::kRowChunks / kLoaders, kBatch = kAll < 4 ? kAll : 4;
 #pragma unroll
-        for (int i = 0; i < kKeys * S::kRowChunks / kLoaders; ++i) {
-          const int c = i * kLoaders + lt, row = c / S::kRowChunks;
-          uint4 x = ld_shared_v4(from + c * 16);
-          // Positions that no query sees: their V rows must be zeros.
-          if (edge && (j0 + row < w.row.lo || j0 + row >= w.row.hi)) x = make_uint4(0, 0, 0, 0);
-          ld.widen(to, row, c % S::kRowChunks, x);
+        for (int i0 = 0; i0 < kAll; i0 += kBatch) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) x[i] = ld_shared_v4(from + ((i0 + i) * kLoaders + lt) * 16);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int c = (i0 + i) * kLoaders + lt, row = c / S::kRowChunks;
+            // Positions that no query sees: their V rows must be zeros.
+            if (edge && (j0 + row < w.row.lo || j0 + row >= w.row.hi)) x[i] = make_uint4(0, 0, 0, 0);
+            ld.widen(to, row, c % S::kRowChunks, x[i]);
+          }
         }
         mbar_arrive(&sh.raw_empty[raw.stage]);
         raw.step();
@@ -707,14 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       for (bool more = w.seek(c0, c1, prefix, p); more && ok; more = w.next(prefix, p), ++u_n) {
-        for (int k = w.k0; k < w.k1 && ok; ++k) {
-          ok = widen(w, k, false);
-          if (kHalve && ok && k == w.k0) {
+#pragma unroll 1
+        for (int x = 2 * w.k0; x < 2 * w.k1 && ok; ++x) {  // K and V of each tile in turn
+          ok = widen(w, x >> 1, x & 1);
+          if (kHalve && ok && x == 2 * w.k0) {
             if (!(ok = wait_for(&sh.q_raw, u_n & 1, dead))) break;
             ld.halve_q(w, u_n & 1);
             publish_q(false);
           }
-          ok = ok && widen(w, k, true);
         }
       }
       if (kHalve && ok && wait_for(&sh.q_empty, (u_n & 1) ^ 1, dead)) publish_q(true);
@@ -767,9 +782,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Where this run's start cuts a unit, and is the first to do so, the
         // unit's parts are joined in this worker's name.
         int4 j = make_int4(-1, 0, 0, 0);
-        if (more && w.k0 > 0 && split_worker(w.u0 + kUnitCost, total, workers) + 1 == me)
+        if (more && w.k0 > 0 && split_worker(w.u0 + p.unit_cost, total, workers) + 1 == me)
           j = make_int4(w.b, w.g, w.unit.query,
-                        static_cast<int>(split_worker(w.u0 + kUnitCost + w.unit.tiles - 1, total, workers)));
+                        static_cast<int>(split_worker(w.u0 + p.unit_cost + w.unit.tiles - 1, total, workers)));
         ws.joins[me] = j;
       }
       if (boxes) {
@@ -1169,6 +1184,7 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   tp.by_group = FastDiv{fastdiv_magic(group), group};
   tp.half_queries = kHalf / p.group;
   tp.box_keys = 0;
+  tp.unit_cost = unit_cost(fp8);
   tp.give_up = give_up;
   CUtensorMap maps[3] = {};
   if (p.page_size % kKeys == 0)
