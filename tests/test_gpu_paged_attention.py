@@ -193,6 +193,31 @@ def test_views_and_layouts(dev, lens, cache):
     assert bool((out[:, :, 1] == -7).all())
 
 
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS], ids=["decode", "chunks"])
+@pytest.mark.parametrize("cache,page", [("same", 16), ("same", 128), ("fp8", 16), ("same", 3)])
+def test_caches_with_a_page_per_head(dev, lens, cache, page):
+    """[pages, heads, page, dim] memory, seen as [pages, page, heads, dim]."""
+    x = PagedInputs(lens, heads=8, kv_heads=2, dim=128, dtype="bf16", cache=cache, page=page, seed=8)
+    x.kc, x.vc = (c.transpose(1, 2).contiguous().transpose(1, 2) for c in (x.kc, x.vc))
+    assert x.kc.to(dev).stride() == x.kc.stride()
+    _, _, status = x.check(_hs(), dev, True)
+    assert not bool(status.any())
+
+
+@pytest.mark.parametrize("max_q", [None, 64])
+def test_largest_batch(dev, max_q):
+    """2048 requests of a token each, by either kernel."""
+    x = PagedInputs([(i % 5, 1) for i in range(2048)], heads=2, kv_heads=1, dim=64, dtype="bf16", seed=3)
+    _, _, status = x.check(_hs(), dev, True, **({"max_q": max_q} if max_q else {}))
+    assert not bool(status.any())
+
+
+@pytest.mark.parametrize("heads,tensor_cores", [(100, True), (128, True), (200, False)])
+def test_many_query_heads_to_one(dev, heads, tensor_cores):
+    x = PagedInputs([(40, 1), (3, 5), (300, 2)], heads=heads, kv_heads=1, dim=64, dtype="bf16", seed=3)
+    x.check(_hs(), dev, tensor_cores)
+
+
 def test_unaligned_caches_and_queries(dev):
     """Addresses that allow no 16-byte loads."""
     hs = _hs()

@@ -214,3 +214,27 @@ def test_no_tokens(dev):
     hs.qk_norm_rope_store(x[:, :2], x[:, 2:3], x[:, 3:], None, None, None, None, x[:, :2], kc, kc.clone(),
                           torch.zeros(0, dtype=torch.int64, device=dev))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_caches_with_a_page_per_head(dev, fp8):
+    """[pages, heads, page, dim] memory, seen as [pages, page, heads, dim]."""
+    hs = _hs()
+    g = torch.Generator(device=dev).manual_seed(1)
+    T, HK, D, ps = 60, 3, 64, 16
+    x = torch.randn(T, 2 * HK + 1, D, generator=g, device=dev).to(torch.bfloat16)
+    loc = torch.randperm(5 * ps, generator=g, device=dev)[:T]
+    kind = torch.uint8 if fp8 else torch.bfloat16
+    one = torch.ones(1, device=dev) if fp8 else None
+    caches = []
+    for turned in (False, True):
+        kc, vc = (torch.zeros((5, HK, ps, D) if turned else (5, ps, HK, D), dtype=kind, device=dev)
+                  for _ in range(2))
+        if turned:
+            kc, vc = kc.transpose(1, 2), vc.transpose(1, 2)
+        hs.qk_norm_rope_store(x[:, :1], x[:, 1: 1 + HK], x[:, 1 + HK:], None, None, None, None,
+                              torch.empty_like(x[:, :1]), kc, vc, loc, k_scale=one, v_scale=one,
+                              page_size=ps)
+        caches.append((kc, vc))
+    for a, b in zip(*caches):
+        assert torch.equal(a, b) and bool(a.view(torch.uint8).any())
