@@ -42,7 +42,7 @@ constexpr int kHalf = 128;         // rows per MMA
 constexpr int kUnitRows = 2 * kHalf;
 constexpr int kThreads = 512;
 constexpr int kLoaders = 128;
-constexpr uint32_t kSoftmaxRegs = 176, kLoaderRegs = 96, kMmaRegs = 64;
+constexpr uint32_t kSoftmaxRegs = 168, kLoaderRegs = 112, kMmaRegs = 64;
 static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 512, "65536 registers per SM");
 constexpr float kRaise = 8.f;      // log2 of how far weights may exceed 1
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -629,41 +629,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(kFullMask, wait_for(&sh.o_full[half], o_ph, dead))) break;
       o_ph ^= 1;
       tc_fence_after();
-      uint32_t o[D / 32][32];
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) tmem_ld32(o[q], o_at + q * 32);
-      tmem_wait_ld();
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) tmem_pin(o[q]);
       auto send = [&](const uint32_t (&x)[16], int at) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           st_shared_v4(mine_at + ((c ^ swap) << 4), make_uint4(x[c * 4], x[c * 4 + 1], x[c * 4 + 2], x[c * 4 + 3]));
         __syncwarp();
+        uint4 v[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int rr = x * 8 + (lane >> 2);
-          const uint4 v = ld_shared_v4(out_at + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-          if (to[x] != nullptr) *reinterpret_cast<uint4*>(to[x] + at) = v;
+          v[x] = ld_shared_v4(out_at + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
         }
         __syncwarp();
-      };
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t x[16];
-        if (whole) {
+        for (int x = 0; x < 4; ++x)
+          if (to[x] != nullptr) *reinterpret_cast<uint4*>(to[x] + at) = v[x];
+      };
+      // Rolled: this code runs once a unit, and its instructions have to be fetched.
+      if (whole) {
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32], x[16];
+          tmem_ld32(o, o_at + d);
+          tmem_wait_ld();
+          tmem_pin(o);
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            x[c] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[q][2 * c]) * f,
-                                             __uint_as_float(o[q][2 * c + 1]) * f);
-          send(x, q * 64);
-        } else {
+            x[c] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[2 * c]) * f, __uint_as_float(o[2 * c + 1]) * f);
+          send(x, d * 2);
+        }
+      } else {
+#pragma unroll 1
+        for (int d = 0; d < D; d += 16) {
+          uint32_t x[16];
+          tmem_ld16(x, o_at + d);
+          tmem_wait_ld();
+          tmem_pin(x);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(o[q][h * 16 + c]) * f);
-            send(x, q * 128 + h * 64);
-          }
+          for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f);
+          send(x, d * 4);
         }
       }
       if (live && !whole) part[kUnitRows * D + half * kHalf + r] = lse;
