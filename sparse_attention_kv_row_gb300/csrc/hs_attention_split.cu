@@ -16,6 +16,9 @@
 // output of its rows in registers.  A (request, kv head) that one warp covers
 // alone is written at once; the others leave (o, log-sum-exp) per run in the
 // workspace, and a second kernel, launched early behind the first, joins them.
+// Measured (GB300, D = 128, 8 kv heads): 32 requests of 2 K to 16 K tokens over
+// bf16 178 us, 6.8 TB/s, the rate of a copy; 128 requests over E4M3 174 us, 6.3
+// TB/s; with a warp to a head on its own 188 and 213 us.
 #include <cuda_runtime.h>
 
 #include <mutex>

@@ -15,6 +15,11 @@
 // maximum is more than 2^8 above the old one: a larger weight is as good in the
 // products' type, and sums stay in fp32.
 //
+// Measured (GB300, D = 128, bf16): about 1.6 us for a pair of tiles and 4 us for a
+// unit's beginning and end; two chunks of 2048 queries over 16 K keys 645 us, 1.7
+// PFLOP/s at the power limit with the tensor pipe 77 % busy; four 2048-token
+// prompts 116 us; a mixed batch over E4M3 196 us.
+//
 // The flattened list of tiles of all units, each with one more for its fixed
 // cost, is cut into equal runs, one per SM.  A unit that a run covers alone is
 // written at once; the others leave their parts in the workspace, and a second

@@ -14,6 +14,8 @@
 // lane in paired fp32 operations, because the instructions of an earlier form
 // (one chunk a lane, partners by shuffle, 222 a round) kept it from the memory's
 // rate.  A warp takes kRounds rounds of one token's heads, loads first.
+// Measured (GB300): 16384 tokens of 48 bf16 heads of 128 in 72 us, 5.7 TB/s, 0.84
+// of a copy's rate; 89 us with the kinds mixed in a warp, 136 in the first form.
 // norm_rope_general: any strides, alignment, head and rotation size; a warp per
 // head with the head staged in shared memory.
 #include <cuda_bf16.h>

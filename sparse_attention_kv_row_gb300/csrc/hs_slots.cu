@@ -10,6 +10,8 @@
 // few loads per thread, no exchange between CTAs) and fills its share of the
 // tokens and blocks; one cluster barrier separates the reads of the lengths and
 // the stack height from their update, so that both may be updated in place.
+// Measured (GB300, in a graph): 34 rows of one token 4.8 us, 1024 rows with 128,000
+// tokens 12 us.
 #include <cuda_runtime.h>
 
 #include <climits>
