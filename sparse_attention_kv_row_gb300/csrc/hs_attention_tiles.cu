@@ -25,8 +25,8 @@
 // written at once; the others leave their parts in the workspace, and a second
 // kernel joins them.
 //
-// K and V tiles come by tensor-map loads, a box per page, where pages are a
-// power-of-two part or a multiple of 128 keys: one warp issues them, straight
+// K and V tiles come by tensor-map loads, in boxes of as many keys as divide a
+// page and a tile, where these are eight or more: one warp issues them, straight
 // into the ring for a 16-bit cache, or as bytes that a warpgroup widens to fp16
 // (exactly) for an FP8 one.  Other page sizes go through registers.  A V tile
 // with positions that no query sees gets zero rows there: 0 times what they hold
@@ -1196,10 +1196,11 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   tp.unit_cost = unit_cost(fp8);
   tp.give_up = give_up;
   CUtensorMap maps[3] = {};
-  if (p.page_size % kKeys == 0)
-    tp.box_keys = kKeys;
-  else if (p.page_size % 8 == 0 && kKeys % p.page_size == 0)
-    tp.box_keys = static_cast<int>(p.page_size);
+  // As many keys to a box as divide both a tile and a page; eight are one row of
+  // the swizzle.
+  int keys = kKeys;
+  while (p.page_size % keys != 0) keys /= 2;
+  if (keys >= 8) tp.box_keys = keys;
   if (p.num_pages < 1 || p.num_pages >= INT32_MAX) tp.box_keys = 0;
   // Strides that a tensor map cannot hold go through registers.
   for (int i = 0; tp.box_keys > 0 && i < 2; ++i)
