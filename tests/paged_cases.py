@@ -191,17 +191,24 @@ class PagedInputs:
         """Bounds on |out - plain| and |lse - plain|.  fp32 products and sums: a score is off by
         at most (D + 4) units of 2^-24 of sum |q k|; the two sums over n keys by n units; the
         weights' exponentials by 4 units.  On the tensor cores each weight is rounded to the
-        compute type (half a step), as is the output; fp16 outputs have an absolute half step."""
+        compute type (half a step), as is the output; fp16 outputs have an absolute half step.
+        fp16 weights have one too: they are kept as at least 2^6 times their share of a sum that
+        is then at least 2^6, so half a step of fp16's subnormals, 2^-25, is at most 2^-31 of a
+        value for each of n keys."""
         out, lse, size, unit, n, _ = ref
         D = self.q.shape[2]
         es = (D + 4) * U32 * unit  # [T, H]
         u = half_step(self.dtype)
-        up = 0.0
+        up, small = 0.0, 0.0
         if tensor_cores:
-            up = half_step(torch.float16 if self.fp8 else self.dtype)
+            kind = torch.float16 if self.fp8 else self.dtype
+            up = half_step(kind)
+            if kind == torch.float16:
+                v = self.vc.float().abs()
+                small = 2.0 ** -31 * float(v[v.isfinite()].max()) * self.vs if v.isfinite().any() else 0.0
         rel = 2 * es + (2 * n[:, None] + 16) * U32 + up
         tiny = 2.0 ** -25 if self.dtype == torch.float16 else 0.0
-        tol_out = 1.01 * (rel[..., None] * size + u * out.abs()) + tiny
+        tol_out = 1.01 * (rel[..., None] * size + u * out.abs() + small * n[:, None, None]) + tiny
         tol_lse = 1.01 * (es + (n[:, None] + 16) * U32 + 4 * U32 * lse.abs().nan_to_num(posinf=0.0))
         return tol_out, tol_lse
 
