@@ -437,10 +437,11 @@ hs_err hs_gather_misses(const uint64_t* pool_ptrs, const uint64_t* hot_ptrs, int
  *   token t = cu_new[b] + i (i < n) has position p = c + i:
  *   cache_loc[t] = block_table[r][p / bs] * bs + p % bs, positions[t] = p,
  *   token_row[t] = b
- * Entries from cu_new[batch] to max_tokens get -1 in all three.  cache_loc is
- * what hs_store_kv, hs_fp8_store_kv and hs_qk_norm_rope_store take, cu_new and
- * seq_lens what hs_paged_attention takes.  Defined by this library (the pages
- * leave block allocation to the caller).
+ * Entries from cu_new[batch] to max_tokens get -1 in all three (all of them for a
+ * batch of 0, which opens no block).  cache_loc is what hs_store_kv,
+ * hs_fp8_store_kv and hs_qk_norm_rope_store take, cu_new and seq_lens what
+ * hs_paged_attention takes.  Defined by this library (the pages leave block
+ * allocation to the caller).
  *
  * Rows that cannot be served open no block, keep seq_lens[b] = c and get
  * cache_loc -1 for their tokens (which still have their place in cu_new):

@@ -636,6 +636,8 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k
         cs_p, cs_stride, max_pos, rot = _matrix(cos_sin, torch.float32, "cos_sin")
         if cs_stride != rot and max_pos > 1:
             raise ValueError("cos_sin must be contiguous")
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
         pos_p = _vector(positions, torch.int64, T, "positions")
     loc_p = _vector(cache_loc, torch.int64, T, "cache_loc")
     ks_p, vs_p = _cache_scale(k_scale, code, "k_scale"), _cache_scale(v_scale, code, "v_scale")

@@ -248,7 +248,8 @@ hs_err attend(const hs_paged_attention_args* a, bool give_up, hs_stream_t stream
   hs_err err = check_args(a);
   if (err != HS_OK) return err;
   if (a->batch == 0) return HS_OK;
-  if (!a->req_state || !a->cu_q || !a->seq_lens || (!a->block_table && a->table_blocks > 0) ||
+  if (!a->req_state || !a->cu_q || !a->seq_lens ||
+      (!a->block_table && a->num_states > 0 && a->table_blocks > 0) ||
       (a->n_tokens > 0 && (!a->q || !a->out)) || (a->num_pages > 0 && (!a->k_cache || !a->v_cache)))
     return fail(HS_ERR_ARG, "hs_paged_attention: a required pointer is NULL");
   const uintptr_t esz = a->in_dtype == HS_DT_F32 ? 4 : 2;

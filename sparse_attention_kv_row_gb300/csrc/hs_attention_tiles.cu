@@ -1205,7 +1205,8 @@ hs_err tiles_launch(const AttnParams& p, int in_dtype, bool fp8, void* workspace
   // Strides that a tensor map cannot hold go through registers.
   for (int i = 0; tp.box_keys > 0 && i < 2; ++i)
     if (!encode_cache(&maps[i], p, i, fp8, bf16, tp.box_keys)) tp.box_keys = 0;
-  if (tp.box_keys > 0 && !encode_queries(&maps[2], p, bf16)) tp.box_keys = 0;
+  // (a query row repeated for every token, stride 0, is not a tensor map either)
+  if (tp.box_keys > 0 && (p.q_token <= 0 || !encode_queries(&maps[2], p, bf16))) tp.box_keys = 0;
   k.main<<<dev.sm_count, kThreads, k.smem + (p.batch + 1) * 4, stream>>>(tp, ws, maps[0], maps[1], maps[2]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_paged_attention launch: %s", cudaGetErrorString(e));

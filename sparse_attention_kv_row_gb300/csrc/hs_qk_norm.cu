@@ -501,7 +501,8 @@ extern "C" hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* a, hs_stream
   if (a->cache_dtype != HS_DT_E4M3 && (a->k_scale || a->v_scale))
     return fail(HS_ERR_ARG, "hs_qk_norm_rope_store: scales go with an E4M3 cache");
   if (a->n_tokens == 0) return HS_OK;
-  if (!a->q || !a->k || !a->v || !a->q_out || !a->k_cache || !a->v_cache || !a->cache_loc ||
+  if (!a->q || !a->k || !a->v || !a->q_out || !a->cache_loc ||
+      (a->num_slots > 0 && (!a->k_cache || !a->v_cache)) ||
       (a->rot_dim > 0 && (!a->cos_sin || !a->positions)))
     return fail(HS_ERR_ARG, "hs_qk_norm_rope_store: a required pointer is NULL");
   const int64_t esz = a->in_dtype == HS_DT_F32 ? 4 : 2;

@@ -301,9 +301,9 @@ extern "C" hs_err hs_assign_slots(const void* ctx_lens, const int32_t* new_lens,
   if (batch > kSlotMaxBatch || max_tokens > INT32_MAX || num_free > INT32_MAX)
     return fail(HS_ERR_UNSUPPORTED, "hs_assign_slots: batch <= %d, max_tokens and num_free "
                                     "<= INT32_MAX", kSlotMaxBatch);
-  if (batch == 0) return HS_OK;
-  if (!ctx_lens || !new_lens || !req_state || !block_table || !free_top || !free_top_out ||
-      !cu_new || !seq_lens || (!free_blocks && num_free > 0) || (!cache_loc && max_tokens > 0))
+  if ((batch > 0 && (!ctx_lens || !new_lens || !req_state || !seq_lens)) ||
+      (!block_table && num_states > 0 && table_blocks > 0) || !free_top || !free_top_out ||
+      !cu_new || (!free_blocks && num_free > 0) || (!cache_loc && max_tokens > 0))
     return fail(HS_ERR_ARG, "hs_assign_slots: a required pointer is NULL");
   DeviceInfo dev;
   hs_err err = current_device(&dev);

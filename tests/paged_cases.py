@@ -212,7 +212,7 @@ class PagedInputs:
         tol_lse = 1.01 * (es + (n[:, None] + 16) * U32 + 4 * U32 * lse.abs().nan_to_num(posinf=0.0))
         return tol_out, tol_lse
 
-    def call(self, hs, dev, *, out=None, lse=None, status=None, max_q=None, **kw):
+    def call(self, hs, dev, *, q=None, out=None, lse=None, status=None, max_q=None, **kw):
         """paged_attention on ``dev``; returns (out, lse, status) with untouched rows at -7."""
         t = lambda a, d=None: torch.from_numpy(np.ascontiguousarray(a)).to(dev) if d is None else \
             torch.from_numpy(np.ascontiguousarray(a)).to(d).to(dev)  # noqa: E731
@@ -225,7 +225,7 @@ class PagedInputs:
         status = torch.full((len(self.seq),), -1, dtype=torch.int32, device=dev) \
             if status is None else status
         sc = lambda x: torch.tensor([x], device=dev) if self.fp8 else None  # noqa: E731
-        inputs = (self.q.to(dev), kc, vc, t(self.table), t(self.req, i), t(self.cu), t(self.seq, i))
+        inputs = (self.q.to(dev) if q is None else q, kc, vc, t(self.table), t(self.req, i), t(self.cu), t(self.seq, i))
         if "stream" in kw:  # the uploads are on the current stream
             torch.cuda.synchronize()
         hs.paged_attention(*inputs, out, max_q_len=self.max_q if max_q is None else max_q,

@@ -184,3 +184,24 @@ def test_captured_decode_loop(dev):
         np.testing.assert_array_equal(g["st"].cpu().numpy(), ref["status"])
         assert int(g["top"]) == top
     assert 128 in ref["status"]
+
+
+def test_empty_batch(dev):
+    """No rows: the token count is 0, the stack keeps its height, every entry is -1."""
+    c = _case(1, 16, 10, 3, seed=5)
+    for n in (0, 1, 700):
+        for i64 in (True, False):
+            e = dict(c, ctx=c["ctx"][:0], new=c["new"][:0], req=c["req"][:0], top=2, max_tokens=n)
+            _run(dev, e, i64=i64)
+            _run(dev, e, i64=i64, in_place=True, optional=False)
+
+
+def test_empty_tables(dev):
+    """No states, no columns, no free blocks: every row with tokens is refused."""
+    for shape, code in (((0, 4), 32), ((9, 0), 32), ((9, 4), 128)):
+        c = _case(3, 16, 0, 3, seed=6)
+        c.update(table=np.full(shape, -1, np.int32), free=c["free"][:0], top=0)
+        c["new"][:] = 2
+        c["req"] = np.arange(3)
+        ref = _run(dev, c)
+        assert (ref["status"] & code == code).all()

@@ -419,3 +419,20 @@ def test_longest_rows_are_bounded(dev, n):
     tol, _ = x.tolerance(ref, True)
     assert bool(((out.cpu().double() - ref[0]).abs() <= tol)[ref[5]].all())
     assert bool((out[1] == -7).all())
+
+
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+@pytest.mark.parametrize("lens", [[(200, 1)] * 3, [(100, 3), (None, 0), (50, 200)]])
+def test_one_query_row_for_every_token(dev, lens, cache):
+    """q with a token stride of 0."""
+    x = PagedInputs(lens, heads=8, kv_heads=2, dim=128, dtype="bf16", cache=cache, seed=11)
+    x.q = x.q[:1].expand(x.T, 8, 128)
+    x.check(_hs(), dev, True, q=x.q[:1].to(dev).expand(x.T, 8, 128))
+
+
+def test_no_states(dev):
+    """A block table of no rows: every request is refused."""
+    x = PagedInputs([(20, 2), (5, 30)], heads=4, kv_heads=2, dim=64, dtype="f16", seed=12)
+    x.table = x.table[:0]
+    _, _, st = x.check(_hs(), dev, True)
+    assert st.tolist() == [32, 32]

@@ -238,3 +238,22 @@ def test_caches_with_a_page_per_head(dev, fp8):
         caches.append((kc, vc))
     for a, b in zip(*caches):
         assert torch.equal(a, b) and bool(a.view(torch.uint8).any())
+
+
+def test_no_slots_and_repeated_rows(dev):
+    """A cache of no pages takes no K or V and says so; one q row may stand for every token."""
+    hs = _hs()
+    g = torch.Generator(device=dev).manual_seed(3)
+    x = torch.randn(1, 4, 64, generator=g, device=dev).to(torch.bfloat16)
+    T, w = 37, torch.ones(64, dtype=torch.bfloat16, device=dev)
+    kc = torch.zeros(0, 16, 1, 64, dtype=torch.bfloat16, device=dev)
+    loc, st = torch.arange(T, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    got = []
+    for rows in (x.expand(T, 4, 64), x.repeat(T, 1, 1)):
+        out = torch.empty(T, 2, 64, dtype=torch.bfloat16, device=dev)
+        st.zero_()
+        hs.qk_norm_rope_store(rows[:, :2], rows[:, 2:3], rows[:, 3:], w, w, None, None, out, kc,
+                              kc.clone(), loc, status=st)
+        assert int(st) == 64
+        got.append(out)
+    assert torch.equal(*got)

@@ -35,7 +35,8 @@ def _slots(lib, **kw):
     (dict(batch=-1), 1), (dict(bs=0), 1), (dict(stride=3), 1), (dict(flags=4), 1), (dict(num_free=-1), 1),
     (dict(max_tokens=-1), 1), (dict(states=-1), 1), (dict(batch=4097), 2), (dict(max_tokens=1 << 31), 2),
     (dict(num_free=1 << 31), 2), (dict(ctx=None), 1), (dict(cu=None), 1), (dict(free=None), 1),
-    (dict(loc=None), 1), (dict(top_out=None), 1), (dict(batch=0, ctx=None), 0)])
+    (dict(loc=None), 1), (dict(top_out=None), 1), (dict(batch=0, top_out=None), 1),
+    (dict(batch=0, ctx=None, cu=None), 1), (dict(table=None), 1)])
 def test_assign_slots_rejects(lib, kw, code):
     assert _slots(lib, **kw) == code
     if code:
@@ -77,7 +78,7 @@ def _attn_args(**kw):
     a = dict(batch=2, num_heads=4, num_kv_heads=2, head_dim=48, in_dtype=2, cache_dtype=2, flags=0,
              page_size=16, max_q_len=2, window=0, scale=0.1, table_blocks=4, n_tokens=4, q=256,
              q_stride_token=192, q_stride_head=48, out=256, out_stride_token=192, out_stride_head=48,
-             k_cache=256, v_cache=256, cache_stride_page=3 * 1024, cache_stride_offset=192,
+             k_cache=256, v_cache=256, cache_stride_page=4096, cache_stride_offset=192,
              cache_stride_head=96, num_pages=8, block_table=256, block_table_stride=4, num_states=2,
              req_state=256, cu_q=256, seq_lens=256)
     a.update(kw)
@@ -93,7 +94,7 @@ def _attn_args(**kw):
     (dict(n_tokens=1 << 31), 2), (dict(q=None), 1), (dict(out=None), 1), (dict(block_table=None), 1),
     (dict(cu_q=None), 1), (dict(k_cache=None), 1), (dict(q_stride_head=47), 1),
     (dict(cache_stride_head=95), 1), (dict(q=257), 1), (dict(k_cache=257), 1),
-    (dict(cache_stride_page=3001), 1), (dict(batch=0, q=None), 0)])
+    (dict(cache_stride_page=4097), 1), (dict(batch=0, q=None), 0)])
 def test_paged_attention_rejects(lib, kw, code):
     assert lib.hs_paged_attention(_attn_args(**kw), None) == code
     if code:
@@ -149,7 +150,7 @@ def _norm_call(hs, **kw):
     (dict(q=_h(5, 4, 64, dtype=torch.float64)), TypeError), (dict(q=_h(5, 256)), ValueError),
     (dict(k=_h(5, 2, 64, dtype=torch.float16)), TypeError), (dict(v=_h(4, 2, 64)), ValueError),
     (dict(q_weight=_h(32)), ValueError), (dict(k_weight=torch.zeros(64)), TypeError),
-    (dict(cos_sin=_h(10, 64)), TypeError), (dict(positions=_i32(5)), TypeError), (dict(positions=_i64(4)), ValueError),
+    (dict(cos_sin=_h(10, 64)), TypeError), (dict(positions=_i32(5)), TypeError), (dict(positions=_i64(4)), ValueError), (dict(positions=None), ValueError),
     (dict(cache_loc=_i64(6)), ValueError), (dict(page_size=8), ValueError),
     (dict(v_cache=_h(3, 16, 2, 64, dtype=torch.float16)), TypeError), (dict(k_scale=torch.ones(1)), ValueError),
     (dict(k_cache=_h(2, 16, 2, 64)), ValueError), (dict(status=_i64(1)), TypeError), (dict(), ValueError)])
