@@ -753,9 +753,13 @@ def _attend(where, fn, q, k_cache, v_cache, block_table, req_state, cu_q, seq_le
     else:
         n = _attention_workspace(dev, *fields[:6], max_q_len, fields[12])
         if n > 0:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            if stream is None or raw == _current_stream(dev):
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            else:
+                # Memory in that stream's order: what the current stream has given back may
+                # still be in use there, and what is given back here is reused only behind
+                # this call.
+                with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=q.device)):
+                    workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
             space_p = workspace.data_ptr()
-            if stream is not None and raw != _current_stream(dev):
-                # the allocator must not hand it out again before that stream is done
-                workspace.record_stream(torch.cuda.ExternalStream(raw, device=dev))
     _launch(dev, where, fn, _capi.PAGED_ATTENTION.pack(*fields, space_p, n), raw)

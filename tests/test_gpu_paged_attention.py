@@ -436,3 +436,25 @@ def test_no_states(dev):
     x.table = x.table[:0]
     _, _, st = x.check(_hs(), dev, True)
     assert st.tolist() == [32, 32]
+
+
+@pytest.mark.parametrize("lens", [[(300, 1)] * 4, [(100, 90)] * 3], ids=["split", "tiles"])
+def test_own_workspaces_of_calls_at_the_same_time(dev, lens, monkeypatch):
+    """A call on another stream gets no workspace that a call before it, on the current stream,
+    may still be using."""
+    from sparse_attention_kv_row_gb300 import _capi
+
+    x = PagedInputs(lens, heads=8, kv_heads=2, dim=128, dtype="bf16", seed=13)
+    used = []
+
+    class Packer:
+        @staticmethod
+        def pack(*fields, block=_capi.PAGED_ATTENTION):
+            used.append(fields[-2])
+            return block.pack(*fields)
+
+    monkeypatch.setattr(_capi, "PAGED_ATTENTION", Packer)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for kw in ({}, dict(stream=side[0]), dict(stream=side[1].cuda_stream), {}):
+        x.check(_hs(), dev, True, **kw)
+    assert all(used) and len(set(used[:3])) == 3 and used[0] == used[3]
