@@ -458,3 +458,19 @@ def test_own_workspaces_of_calls_at_the_same_time(dev, lens, monkeypatch):
     for kw in ({}, dict(stream=side[0]), dict(stream=side[1].cuda_stream), {}):
         x.check(_hs(), dev, True, **kw)
     assert all(used) and len(set(used[:3])) == 3 and used[0] == used[3]
+
+
+@pytest.mark.parametrize("heads,kv_heads,dtype,cache", [
+    (4, 2, "bf16", "same"), (4, 4, "f16", "fp8"), (16, 2, "bf16", "same"), (16, 2, "bf16", "fp8"),
+    (2, 1, "f32", "same")])
+def test_tokens_far_apart(dev, heads, kv_heads, dtype, cache):
+    """Queries and outputs whose offsets pass 2^32 bytes."""
+    x = PagedInputs([(50, 1), (70, 3)], heads=heads, kv_heads=kv_heads, dim=64, dtype=dtype,
+                    cache=cache, seed=14)
+    step = 1_100_000_000 // (2 if dtype == "f32" else 1) // 8 * 8  # 2.2 GB a token
+    n = (x.T - 1) * step + heads * 64
+    far = [torch.empty(n, dtype=x.dtype, device=dev).as_strided((x.T, heads, 64), (step, 64, 1))
+           for _ in range(2)]
+    far[0].copy_(x.q.to(dev))
+    far[1].fill_(-7.0)
+    x.check(_hs(), dev, dtype != "f32", q=far[0], out=far[1])

@@ -257,3 +257,30 @@ def test_no_slots_and_repeated_rows(dev):
         assert int(st) == 64
         got.append(out)
     assert torch.equal(*got)
+
+
+@pytest.mark.parametrize("D,inter", [(128, False), (128, True), (18, False)])
+def test_tokens_far_apart(dev, D, inter):
+    """Inputs and outputs whose offsets pass 2^32 bytes: as near ones, bit for bit."""
+    hs = _hs()
+    g = torch.Generator(device=dev).manual_seed(4)
+    T, step = 4, 800_000_000  # 1.6 GB a token
+    x = torch.randn(T, 4, D, generator=g, device=dev).to(torch.bfloat16)
+    w = torch.randn(D, generator=g, device=dev).to(torch.bfloat16)
+    angle = torch.randn(T, D // 2, generator=g, device=dev)
+    cs = torch.cat([angle.cos(), angle.sin()], 1)
+    pos, loc = torch.arange(T, device=dev), torch.arange(T, device=dev).flip(0)
+
+    def far(heads):
+        return torch.empty((T - 1) * step + heads * D, dtype=torch.bfloat16, device=dev).as_strided(
+            (T, heads, D), (step, D, 1))
+
+    got = []
+    for make in (None, far):
+        src = x if make is None else make(4).copy_(x)
+        out = torch.empty_like(x[:, :2]) if make is None else make(2)
+        kc, vc = (torch.zeros(1, 16, 1, D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+        hs.qk_norm_rope_store(src[:, :2], src[:, 2:3], src[:, 3:], w, w, cs, pos, out, kc, vc, loc,
+                              interleaved=inter)
+        got.append((out, kc, vc))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
