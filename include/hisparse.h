@@ -559,7 +559,8 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  * num_kv_heads) and s_j = scale * k_scale * (q[t][h] . k_j[g]):
  *   out[t][h] = sum_j exp(s_j - lse) * v_scale * v_j[g],
  *   lse[t][h] = log(sum_j exp(s_j))     (natural logarithm)
- * A query that sees no key (p < 0) gives zeros and lse = -inf.  Chunks of one
+ * A query that sees no key (p < 0) gives zeros and lse = -inf, and so does one
+ * whose scores are all -inf; with a NaN among its scores both are NaN.  Chunks of one
  * token are a decode step, chunks as long as the sequence a whole prompt, and
  * one call mixes them freely.  Defined by this library: it reads the caches
  * that hs_store_kv, hs_fp8_store_kv and hs_qk_norm_rope_store write.

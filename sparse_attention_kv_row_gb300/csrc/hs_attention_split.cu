@@ -320,9 +320,10 @@ struct WideRows : SplitTypes<kIn, kFp8, D> {
       float l = l_run[h];
       l += __shfl_xor_sync(kFullMask, l, 1);
       l += __shfl_xor_sync(kFullMask, l, 2);
-      const bool none = m_run[h] == -INFINITY;
-      const float f = (none ? 0.f : 1.0f / l) * to.factor;
-      const float lse = none ? -INFINITY : m_run[h] - kBias + log2f(l);
+      // A sum of 0 is that of a row without keys: zeros, and -inf.  (The maximum does
+      // not tell: it drops NaN, which has to stay in the sum and in its logarithm.)
+      const float f = (l == 0.f ? 0.f : 1.0f / l) * to.factor;
+      const float lse = m_run[h] - kBias + log2f(l);
       const int m = r0 + 8 * h;
       if (m >= rows) continue;
       const int i = m / p.group, head = g * p.group + (m - i * p.group);
@@ -505,9 +506,10 @@ struct NarrowRows : SplitTypes<kIn, kFp8, D> {
       float l = l_run[h];
 #pragma unroll
       for (int d = 4; d < kWarp; d <<= 1) l += __shfl_xor_sync(kFullMask, l, d);
-      const bool none = m_run[h] == -INFINITY;
-      const float f = (none ? 0.f : 1.0f / l) * to.factor;
-      const float lse = none ? -INFINITY : m_run[h] - kBias + log2f(l);
+      // A sum of 0 is that of a row without keys: zeros, and -inf.  (The maximum does
+      // not tell: it drops NaN, which has to stay in the sum and in its logarithm.)
+      const float f = (l == 0.f ? 0.f : 1.0f / l) * to.factor;
+      const float lse = m_run[h] - kBias + log2f(l);
       const int m = 2 * c4 + h;
       if (m >= rows) continue;
       const int i = m / p.group, head = g * p.group + (m - i * p.group);
@@ -702,14 +704,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     acc.z += add * x.z;
     acc.w += add * x.w;
   }
-  const float f = mx == -INFINITY ? 0.f : vs / l;
+  const float f = l == 0.f ? 0.f : vs / l;  // (0: no key; NaN stays)
   const int i = m / p.group, head = g * p.group + (m - i * p.group);
   const int64_t tok = row.q0 + i;
   constexpr bool kB = kIn == HS_DT_BF16;
   *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + lane * 8) =
       make_uint2(pack2<kB>(acc.x * f, acc.y * f), pack2<kB>(acc.z * f, acc.w * f));
   if (lane == 0 && p.lse)
-    p.lse[tok * p.heads + head] = mx == -INFINITY ? -INFINITY : kLn2 * (mx + log2f(l));
+    p.lse[tok * p.heads + head] = kLn2 * (mx + log2f(l));
 }
 
 struct SplitKernels {

@@ -610,9 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const bool whole = w.k0 == 0 && w.k1 == w.unit.tiles;
-      const bool none = top == -INFINITY;
-      const float inv = none ? 0.f : 1.0f / l;
-      const float lse = none ? -INFINITY : ref + log2f(l);
+      // A sum of 0 is that of a row without keys: zeros, and -inf.  (The maximum does
+      // not tell: it drops NaN, which has to stay in the sum and in its logarithm.)
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      const float lse = ref + log2f(l);
       const float f = whole ? inv * vs : inv;
       float* part = ws.slots + static_cast<int64_t>(2 * me + (w.k0 == 0 ? 1 : 0)) * tiles_slot_floats(D);
       // 64 bytes of each of the warp's rows at a time through shared memory, so
@@ -1066,14 +1067,14 @@ __global__ void __launch_bounds__(kTilesJoinThreads)
       acc.z += add * o.z;
       acc.w += add * o.w;
     }
-    const float f = top == -INFINITY ? 0.f : vs / l;
+    const float f = l == 0.f ? 0.f : vs / l;  // (0: no key; NaN stays)
     const int head = j.y * p.group + r - in * p.group;
     const int64_t tok = row.q0 + i;
     constexpr bool kB = kIn == HS_DT_BF16;
     *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + lane * 8) =
         make_uint2(pack2t<kB>(acc.x * f, acc.y * f), pack2t<kB>(acc.z * f, acc.w * f));
     if (lane == 0 && p.lse)
-      p.lse[tok * p.heads + head] = top == -INFINITY ? -INFINITY : kLn2 * (top + log2f(l));
+      p.lse[tok * p.heads + head] = kLn2 * (top + log2f(l));
   }
 }
 

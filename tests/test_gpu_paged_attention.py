@@ -474,3 +474,79 @@ def test_tokens_far_apart(dev, heads, kv_heads, dtype, cache):
     far[0].copy_(x.q.to(dev))
     far[1].fill_(-7.0)
     x.check(_hs(), dev, dtype != "f32", q=far[0], out=far[1])
+
+
+def _check_with_nan(x, dev, tensor_cores, b=None):
+    """NaN where the plain statement has it, in outputs and log-sums alike; right elsewhere."""
+    out, lse, _ = x.call(_hs(), dev)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    ref = x.plain()
+    tol_out, tol_lse = x.tolerance(ref, tensor_cores)
+    nan = ref[1].isnan()
+    assert bool(nan.any()) and not bool(nan.all())
+    assert torch.equal(lse.isnan(), nan)
+    assert torch.equal(out.isnan(), nan[..., None].expand(out.shape))
+    some = ref[5][:, None] & ~nan & (ref[1] > -np.inf)
+    assert bool(((out - ref[0]).abs() <= tol_out)[some].all())
+    assert bool(((lse - ref[1]).abs() <= tol_lse)[some].all())
+    none = ref[5][:, None] & (ref[1] == -np.inf)
+    assert bool((lse[none] == -np.inf).all())
+
+
+NAN_FORMS = [(8, 2, 128, "bf16", "same", 16, True), (12, 1, 64, "f16", "same", 16, True),
+             (8, 2, 128, "bf16", "fp8", 16, True), (12, 1, 64, "f16", "fp8", 16, True),
+             (8, 2, 128, "bf16", "same", 3, True), (8, 2, 64, "bf16", "fp8", 3, True),
+             (4, 2, 40, "bf16", "same", 16, False)]
+
+
+@pytest.mark.parametrize("lens", [DECODE, DRAFTS, CHUNKS], ids=["decode", "drafts", "chunks"])
+@pytest.mark.parametrize("heads,kv_heads,dim,dtype,cache,page,tensor_cores", NAN_FORMS)
+def test_nan_queries_and_keys_in_the_log_sum(dev, lens, heads, kv_heads, dim, dtype, cache, page,
+                                             tensor_cores):
+    """A row whose scores are all NaN is not a row that sees no key: its log-sum is NaN too."""
+    kw = dict(heads=heads, kv_heads=kv_heads, dim=dim, dtype=dtype, cache=cache, page=page, seed=21)
+    x = PagedInputs(lens, **kw)
+    for t in range(0, x.T, 3):  # every third token, in one head
+        x.q[t, t % heads, t % dim] = np.nan
+    _check_with_nan(x, dev, tensor_cores)
+    x = PagedInputs(lens, **kw)
+    for b in (0, 1, 5):  # every key of some requests, in one kv head
+        pages = x.table[x.req[b]]
+        x.kc.view(torch.uint8 if x.fp8 else x.dtype)[pages[pages >= 0], :, kv_heads - 1, 1] = (
+            0x7F if x.fp8 else float("nan"))
+    _check_with_nan(x, dev, tensor_cores)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+def test_nan_in_one_part_of_a_long_context(dev, n, cache):
+    """Keys that are NaN for a stretch in the middle: whole parts of a split request."""
+    x = PagedInputs([(9000, n), (40, 1)], heads=4, kv_heads=2, dim=64, dtype="bf16", cache=cache,
+                    page=64, seed=22)
+    pages = x.table[x.req[0], 40:80]
+    x.kc.view(torch.uint8 if x.fp8 else x.dtype)[pages, :, 1] = 0x7F if x.fp8 else float("nan")
+    _check_with_nan(x, dev, True)
+
+
+@pytest.mark.parametrize("lens", [DECODE, DRAFTS, CHUNKS], ids=["decode", "drafts", "chunks"])
+@pytest.mark.parametrize("dim,page,tensor_cores", [(128, 16, True), (64, 3, True), (40, 16, False)])
+def test_scores_of_minus_infinity(dev, lens, dim, page, tensor_cores):
+    """Keys whose score is -inf weigh nothing; where every key's is, the row is zeros and -inf."""
+    hs = _hs()
+    x = PagedInputs(lens, heads=4, kv_heads=2, dim=dim, dtype="bf16", page=page, seed=26)
+    x.q[:, :, 1] = x.q[:, :, 1].abs() + 1
+    finite = x.kc.clone()
+    x.kc[..., 1, 1] = float("-inf")     # kv head 1: every key
+    x.kc[:, ::2, 0, 1] = float("-inf")  # kv head 0: every other place of a page
+    out, lse, _ = x.call(hs, dev)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    ref = list(x.plain())
+    seen = ref[5]
+    assert bool((out[seen, 2:] == 0).all()) and bool((lse[seen, 2:] == -np.inf).all())
+    some = seen[:, None] & (ref[1] > -np.inf)
+    assert bool(some[:, :2].any()) and not bool(some[:, 2:].any())
+    x.kc = finite
+    ref[3] = x.plain()[3]  # sum |q k| of the finite keys, which bounds those that weigh
+    tol_out, tol_lse = x.tolerance(ref, tensor_cores)
+    assert bool(((out - ref[0]).abs() <= tol_out)[some].all())
+    assert bool(((lse - ref[1]).abs() <= tol_lse)[some].all())
