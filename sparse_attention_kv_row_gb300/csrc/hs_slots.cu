@@ -56,8 +56,8 @@ struct SlotParams {
 // One row in shared memory: what a token needs to find its slot.
 struct __align__(16) SlotRow {
   int32_t state;  // block-table row, -1 when the row cannot be served
-  int32_t ctx;
-  int32_t held;   // blocks before this call
+  int32_t ctx;    // the low half of a length past 32 bits, which no served row has
+  int32_t held;   // blocks before this call; the length's high half where state is -1
   int32_t base;   // index, among the batch's opened blocks, of the row's first
 };
 
@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotPa
         taken = static_cast<int32_t>(end);
       }
     }
-    rows[b] = SlotRow{req[i], static_cast<int32_t>(ctx[i]), held[i],
+    rows[b] = SlotRow{req[i], static_cast<int32_t>(ctx[i]),
+                      req[i] < 0 ? static_cast<int32_t>(ctx[i] >> 32) : held[i],
                       static_cast<int32_t>(base < INT32_MAX ? base : INT32_MAX)};
     start[b] = static_cast<int32_t>(begin[i] < INT32_MAX ? begin[i] : INT32_MAX);
     if (rank == 0 && p.status) p.status[b] = st[i];
@@ -239,7 +240,10 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotPa
       b = row_from(b, p.batch, static_cast<int32_t>(t), [&](int i) { return start[i]; });
       who = b;
       const SlotRow row = rows[b];
-      pos = static_cast<int64_t>(row.ctx) + (t - static_cast<uint32_t>(start[b]));
+      const uint64_t from = row.state >= 0 ? static_cast<uint32_t>(row.ctx)
+                                           : static_cast<uint64_t>(row.held) << 32 |
+                                                 static_cast<uint32_t>(row.ctx);
+      pos = static_cast<int64_t>(from + (t - static_cast<uint32_t>(start[b])));
       if (row.state >= 0) {
         const uint32_t c = div_any(static_cast<uint32_t>(pos), p.div_block);
         const int32_t j = static_cast<int32_t>(c) - row.held;

@@ -205,3 +205,15 @@ def test_empty_tables(dev):
         c["req"] = np.arange(3)
         ref = _run(dev, c)
         assert (ref["status"] & code == code).all()
+
+
+def test_positions_of_refused_rows_past_32_bits(dev):
+    """A refused row's tokens keep their positions, also where these pass 32 bits."""
+    for ctx in (2 ** 31 + 5, 2 ** 32 + 3, 2 ** 40 + 7, -1, -2 ** 33 - 9):
+        c = _case(5, 16, 10, 3, seed=2, extra=20)
+        c["ctx"] = c["ctx"].astype(np.int64)
+        c["ctx"][1], c["new"][1] = ctx, 4
+        ref = _run(dev, c)
+        assert ref["status"][1] == 32
+        at = int(ref["cu_new"][1])
+        assert ref["positions"][at: at + 4].tolist() == [ctx + i for i in range(4)]
