@@ -517,7 +517,9 @@ hs_err hs_assign_slots(const void* ctx_lens, const int32_t* new_lens, const void
  *  status      int32 [1] or NULL: HS_ST_BAD_INDEX is OR-ed in when a token's
  *              slot is outside [0, num_slots) (its K and V are skipped) or its
  *              position outside [0, max_pos) (its q and K are skipped)
- * A token of length 0 head (x all zero) stays zero.  Limits: head_dim <= 1024,
+ * A head whose x are all zero stays zero, with eps = 0 too.  The sum of squares is
+ * held in fp32: a head with values past about 1e18 (whose sum overflows) becomes
+ * zeros, and with eps = 0 so does one below 1e-23.  Limits: head_dim <= 1024,
  * rot_dim even and <= head_dim, num_slots < 2^32, (num_heads + 2 *
  * num_kv_heads) * head_dim < 2^31 (else HS_ERR_UNSUPPORTED).
  * Preconditions (not checked): cache_loc values in range are distinct; no

@@ -154,6 +154,13 @@ __device__ __forceinline__ unsigned char* slot_at(int64_t L, int kind, int head,
          (L - page * p.page_size) * p.c_off + static_cast<int64_t>(head) * p.c_head;
 }
 
+// 1 / sqrt(mean square + eps); 0 where both are zero, so that a head of zeros stays
+// zero without eps too (0 times infinity would be NaN).
+__device__ __forceinline__ float inverse_norm(float sum_sq, const NormParams& p) {
+  const float ms = sum_sq * p.inv_dim + p.eps;
+  return ms == 0.f ? 0.f : rsqrtf(ms);
+}
+
 // Pairs of fp32 values and the paired operations on them.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_rows(const NormPara
       float ss = unpair(sq).x + unpair(sq).y;
 #pragma unroll
       for (int d = G / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(kFullMask, ss, d);
-      const float inv = rsqrtf(ss * p.inv_dim + p.eps);
+      const float inv = inverse_norm(ss, p);
       const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_general(const NormPara
     for (int d = kWarp / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(kFullMask, ss, d);
     __syncwarp();
     if (w != nullptr) {
-      const float inv = rsqrtf(ss * p.inv_dim + p.eps);
+      const float inv = inverse_norm(ss, p);
       for (int d = lane; d < p.dim; d += kWarp)
         y[d] = y[d] * inv * T::load(w + static_cast<int64_t>(d) * T::kBytes);
     }

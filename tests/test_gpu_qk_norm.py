@@ -284,3 +284,35 @@ def test_tokens_far_apart(dev, D, inter):
                               interleaved=inter)
         got.append((out, kc, vc))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,rot,inter", [(128, 128, False), (64, 32, True), (18, 10, False), (80, 0, True)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_heads_of_zeros_without_eps(dev, dtype, D, rot, inter, fp8):
+    """With eps = 0 a head of zeros stays zero; the others are normed as ever."""
+    hs = _hs()
+    g = torch.Generator().manual_seed(D)
+    T, H, HK, dt = 9, 3, 2, TORCH[dtype]
+    x = torch.randn(T, H + 2 * HK, D, generator=g).to(dt)
+    x[::2, 1] = 0   # a q head
+    x[::3, 3] = 0   # a k head
+    w = (1 + 0.3 * torch.randn(2, D, generator=g)).to(dt)
+    cs = _angles(50, rot) if rot else None
+    pos, loc = torch.arange(T) * 5, torch.arange(T).flip(0) * 2
+    d = lambda a: None if a is None else a.to(dev)  # noqa: E731
+    kc = torch.full((2, 16, HK, D), 3, dtype=torch.uint8 if fp8 else dt, device=dev)
+    out = torch.full((T, H, D), -7.0, dtype=dt, device=dev)
+    y = d(x)
+    hs.qk_norm_rope_store(y[:, :H], y[:, H: H + HK], y[:, H + HK:], d(w[0]), d(w[1]), d(cs), d(pos) if rot else None,
+                          out, kc, kc.clone(), d(loc), eps=0.0, interleaved=inter)
+    turn = cs[pos] if rot else None
+    zq, bq = (a.nan_to_num(nan=0.0) for a in norm_rope_plain(x[:, :H], w[0], turn, 0.0, inter))
+    zk, bk = (a.nan_to_num(nan=0.0) for a in norm_rope_plain(x[:, H: H + HK], w[1], turn, 0.0, inter))
+    _check(out, zq, bq, D, dt, True, "q")
+    assert bool((out[::2, 1] == 0).all())
+    got = kc.view(-1, HK, D)[d(loc)]
+    if fp8:
+        _check_fp8(got, zk, bk, D, 1.0, True, "k")
+    else:
+        _check(got, zk, bk, D, dt, True, "k")
