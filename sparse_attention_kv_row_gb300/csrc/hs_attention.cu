@@ -152,9 +152,10 @@ enum class AttnForm { kGeneral, kSplit, kTiles };
 AttnForm attn_form(const hs_paged_attention_args* a) {
   const int64_t rows = static_cast<int64_t>(a->max_q_len) * (a->num_heads / a->num_kv_heads);
   if (a->in_dtype == HS_DT_F32 || (a->head_dim != 64 && a->head_dim != 128) || rows == 0 ||
-      a->n_tokens == 0 || rows * a->num_kv_heads > INT32_MAX / 2 / a->batch)  // blocks of the join
+      a->n_tokens == 0)
     return AttnForm::kGeneral;
-  if (rows <= kSplitRows) return AttnForm::kSplit;
+  if (rows <= kSplitRows)  // its join has a block for each row of the batch's kv heads
+    return rows * a->num_kv_heads <= INT32_MAX / 2 / a->batch ? AttnForm::kSplit : AttnForm::kGeneral;
   // A half of 128 rows holds whole queries.
   return a->num_heads / a->num_kv_heads <= 128 ? AttnForm::kTiles : AttnForm::kGeneral;
 }

@@ -550,3 +550,21 @@ def test_scores_of_minus_infinity(dev, lens, dim, page, tensor_cores):
     tol_out, tol_lse = x.tolerance(ref, tensor_cores)
     assert bool(((out - ref[0]).abs() <= tol_out)[some].all())
     assert bool(((lse - ref[1]).abs() <= tol_lse)[some].all())
+
+
+@pytest.mark.parametrize("batch,max_q", [(255, 131072), (256, 131072), (2048, 16384), (64, 524288)])
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+def test_a_large_bound_on_chunks_changes_nothing(dev, batch, max_q, cache):
+    """max_q_len is only a bound: the kernel, its workspace and the results are those of a tight one."""
+    hs = _hs()
+    x = PagedInputs([(i % 50, 1 + (i % 40 == 3) * 30) for i in range(batch)], heads=32, kv_heads=8,
+                    dim=128, dtype="bf16", cache=cache, seed=23)
+    t = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    q, kc = x.q.to(dev), x.kc.to(dev)
+    need = [hs.paged_attention_workspace_bytes(q, kc, kc, t(x.table), t(x.req), t(x.cu), t(x.seq), q,
+                                               max_q_len=m, page_size=16) for m in (x.max_q, max_q)]
+    assert need[0] == need[1] > 0
+    tight = x.check(hs, dev, True)
+    wide = x.check(hs, dev, True, max_q=max_q)
+    for a, b in zip(tight, wide):
+        assert torch.equal(a, b)
