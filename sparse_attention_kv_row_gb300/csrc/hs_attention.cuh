@@ -53,9 +53,12 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b) {
   const int64_t state = p.flags & HS_REQ_STATE_I64
                             ? __ldg(static_cast<const long long*>(p.req_state) + b)
                             : __ldg(static_cast<const int32_t*>(p.req_state) + b);
-  const int64_t len = p.flags & HS_SEQ_LENS_I64
-                          ? __ldg(static_cast<const long long*>(p.seq_lens) + b)
-                          : __ldg(static_cast<const int32_t*>(p.seq_lens) + b);
+  const int64_t given = p.flags & HS_SEQ_LENS_I64
+                            ? __ldg(static_cast<const long long*>(p.seq_lens) + b)
+                            : __ldg(static_cast<const int32_t*>(p.seq_lens) + b);
+  // As 0 before it is compared: max_len is negative where the tiles of empty rows
+  // alone would pass 32 bits, and a row below it must not get by.
+  const int64_t len = given < 0 ? 0 : given;
   const int64_t q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
   if (state < 0) return r;
   if (state >= p.num_states || q0 < 0 || q1 < q0 || q1 > p.n_tokens || q1 - q0 > p.max_q ||
@@ -65,7 +68,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int b) {
   }
   r.q0 = static_cast<int32_t>(q0);
   r.n = static_cast<int32_t>(q1 - q0);
-  r.len = static_cast<int32_t>(len < 0 ? 0 : len);
+  r.len = static_cast<int32_t>(len);
   r.hi = r.len;
   if (p.window > 0) {
     const int64_t lo = static_cast<int64_t>(r.len) - r.n + 1 - p.window;

@@ -568,3 +568,30 @@ def test_a_large_bound_on_chunks_changes_nothing(dev, batch, max_q, cache):
     wide = x.check(hs, dev, True, max_q=max_q)
     for a, b in zip(tight, wide):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("length", [0, -1, -5000])
+def test_more_empty_rows_than_tiles_can_be_counted(dev, length):
+    """2^20 kv heads and 700 rows: one tile a unit is more than 32 bits count.  Every row is refused,
+    also where its length is negative (which counts as 0)."""
+    hs = _hs()
+    B, heads, dim = 700, 1 << 20, 64
+    q = torch.zeros(1, heads, dim, dtype=torch.bfloat16, device=dev).expand(B, heads, dim)
+    out = torch.full((1, heads, dim), -7.0, dtype=torch.bfloat16, device=dev)
+    kc = torch.zeros(1, 1, heads, dim, dtype=torch.bfloat16, device=dev)
+    i = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(dev)  # noqa: E731
+    status = i(np.full(B, -1))
+    hs.paged_attention(q, kc, kc, i(np.zeros((B, 1))), i(np.arange(B)), i(np.arange(B + 1)),
+                       i(np.full(B, length)), out.expand(B, heads, dim), max_q_len=17, page_size=1,
+                       status=status)
+    assert bool((status == 32).all()) and bool((out == -7).all())
+
+
+def test_negative_lengths_count_as_none(dev):
+    """Rows of a negative length see no key: zeros and -inf, in every kernel."""
+    for lens, dim, tensor_cores in ((DECODE, 64, True), (CHUNKS, 128, True), (CHUNKS, 40, False)):
+        for i64 in (True, False):
+            x = PagedInputs(lens, heads=4, kv_heads=2, dim=dim, dtype="bf16", seed=27, i64=i64)
+            x.seq[0], x.seq[3] = -1, -2 ** 31
+            _, lse, status = x.check(_hs(), dev, tensor_cores)
+            assert not bool(status.any()) and bool((lse[int(x.cu[3]): int(x.cu[4])] == -np.inf).all())
