@@ -691,19 +691,33 @@ def _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens
         table_stride, states, req_p, cu_p, seq_p, ks_p, vs_p, st_p)
 
 
-@functools.lru_cache(maxsize=4096)
-def _attention_workspace(dev, batch, heads, kv_heads, dim, dtype, code, max_q_len, tokens) -> int:
-    """Bytes of workspace for these sizes on this device (it depends on nothing else)."""
-    block = _capi.PagedAttentionArgs(
-        batch=batch, num_heads=heads, num_kv_heads=kv_heads, head_dim=dim, in_dtype=dtype,
-        cache_dtype=code, page_size=1, max_q_len=max_q_len, scale=1.0, n_tokens=tokens,
-        q_stride_head=dim, out_stride_head=dim, cache_stride_head=4 * dim, cache_stride_offset=1,
-        cache_stride_page=1)
+def _workspace_bytes(dev, block) -> int:
     with torch.cuda.device(dev):
-        n = int(_lib().hs_paged_attention_workspace_bytes(C.byref(block)))
+        n = int(_lib().hs_paged_attention_workspace_bytes(block))
     if n < 0:
         _capi.check(-n, "hs_paged_attention_workspace_bytes")
     return n
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(dev, group, dim, dtype, code, queries) -> int:
+    """Bytes of workspace for at most ``queries`` new tokens a request on this device.  It depends
+    on the kernel, which differs up to 16 query rows a kv head only, and not on how many requests,
+    tokens and kv heads there are: a server whose batches change asks once for each model."""
+    block = _capi.PagedAttentionArgs(
+        batch=1, num_heads=group, num_kv_heads=1, head_dim=dim, in_dtype=dtype, cache_dtype=code,
+        page_size=1, max_q_len=queries, scale=1.0, n_tokens=1, q_stride_head=dim,
+        out_stride_head=dim, cache_stride_head=4 * dim, cache_stride_offset=1, cache_stride_page=1)
+    return _workspace_bytes(dev, C.byref(block))
+
+
+def _attention_need(dev, fields) -> int:
+    """Bytes of workspace for the call of these fields; nothing where it has nothing to compute.
+    (Sizes that the call refuses get their message from the call.)"""
+    batch, heads, kv_heads, dim, dtype, code, _, _, queries = fields[:9]
+    if batch == 0 or fields[12] == 0 or queries < 1 or kv_heads < 1 or heads % kv_heads:
+        return 0
+    return _attention_workspace(dev, heads // kv_heads, dim, dtype, code, min(queries, 17))
 
 
 def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
@@ -711,7 +725,7 @@ def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, req_state,
     """Bytes of workspace that ``paged_attention`` needs for tensors of these shapes and types."""
     dev, f = _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out,
                               max_q_len, None, window, None, None, page_size, None, None)
-    return _attention_workspace(dev, *f[:6], max_q_len, f[12])
+    return _workspace_bytes(dev, _capi.PAGED_ATTENTION.pack(*f, 0, 0))
 
 
 def paged_attention(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, *, max_q_len,
@@ -751,7 +765,7 @@ def _attend(where, fn, q, k_cache, v_cache, block_table, req_state, cu_q, seq_le
         space_p = _vector(workspace, torch.uint8, n, "workspace")
         _device_of(q, workspace)
     else:
-        n = _attention_workspace(dev, *fields[:6], max_q_len, fields[12])
+        n = _attention_need(dev, fields)
         if n > 0:
             if stream is None or raw == _current_stream(dev):
                 workspace = torch.empty(n, dtype=torch.uint8, device=q.device)

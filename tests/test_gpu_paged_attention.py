@@ -595,3 +595,20 @@ def test_negative_lengths_count_as_none(dev):
             x.seq[0], x.seq[3] = -1, -2 ** 31
             _, lse, status = x.check(_hs(), dev, tensor_cores)
             assert not bool(status.any()) and bool((lse[int(x.cu[3]): int(x.cu[4])] == -np.inf).all())
+
+
+def test_workspace_sizes_are_asked_for_once(dev):
+    """The size follows from types, head size and the kernel: other token counts, bounds and batches
+    of a running server need no new look-up."""
+    hs = _hs()
+    g = torch.Generator(device=dev).manual_seed(1)
+    kv = torch.randn(2, 40, 16, 2, 64, generator=g, device=dev).to(torch.bfloat16)
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    table = torch.arange(36, dtype=torch.int32, device=dev).view(3, 12)
+    hs._attention_workspace.cache_clear()
+    for n in range(1, 60):
+        q = torch.randn(n + 2, 4, 64, generator=g, device=dev).to(torch.bfloat16)
+        for batch, cu in ((3, i(0, n, n + 1, n + 2)), (1, i(0, n))):
+            hs.paged_attention(q, kv[0], kv[1], table, i(0, 1, 2)[:batch], cu, i(n, 40, 50)[:batch],
+                               torch.empty_like(q), max_q_len=n)
+    assert hs._attention_workspace.cache_info().misses <= 20
