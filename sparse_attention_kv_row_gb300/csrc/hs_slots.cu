@@ -264,20 +264,32 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotPa
 }
 
 std::mutex g_slot_mu;
-bool g_slot_ok[64] = {false};
+int g_slot_cluster[64] = {0};  // 0: not asked yet
 
-// Shared memory and the 16-CTA cluster need an opt-in, once per device.
-hs_err slots_setup(const DeviceInfo& dev) {
+// Shared memory and the 16-CTA cluster need an opt-in, once per device.  A cluster
+// of more than 8 has to fit one part of the GPU, which a slice of it may not have:
+// *most is what the device can place.
+hs_err slots_setup(const DeviceInfo& dev, int* most) {
   std::lock_guard<std::mutex> lock(g_slot_mu);
-  if (g_slot_ok[dev.device]) return HS_OK;
-  cudaError_t e = cudaFuncSetAttribute(assign_slots_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSlotMaxBatch * (sizeof(SlotRow) + 4));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(assign_slots_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess)
-    return fail(HS_ERR_CUDA, "hs_assign_slots: %s", cudaGetErrorString(e));
-  g_slot_ok[dev.device] = true;
+  int& known = g_slot_cluster[dev.device];
+  if (known == 0) {
+    constexpr int kSmem = kSlotMaxBatch * (sizeof(SlotRow) + 4);
+    cudaError_t e = cudaFuncSetAttribute(assign_slots_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(assign_slots_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSlotMaxCluster, 1, 1);
+    cfg.blockDim = dim3(kSlotThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    int size = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxPotentialClusterSize(&size, assign_slots_kernel, &cfg);
+    if (e != cudaSuccess)
+      return fail(HS_ERR_CUDA, "hs_assign_slots: %s", cudaGetErrorString(e));
+    known = 1;
+    while (known < kSlotMaxCluster && known * 2 <= size) known *= 2;
+  }
+  *most = known;
   return HS_OK;
 }
 
@@ -312,7 +324,8 @@ extern "C" hs_err hs_assign_slots(const void* ctx_lens, const int32_t* new_lens,
   DeviceInfo dev;
   hs_err err = current_device(&dev);
   if (err != HS_OK) return err;
-  err = slots_setup(dev);
+  int most = 1;
+  err = slots_setup(dev, &most);
   if (err != HS_OK) return err;
 
   SlotParams p;
@@ -341,11 +354,11 @@ extern "C" hs_err hs_assign_slots(const void* ctx_lens, const int32_t* new_lens,
 
   // One small CTA for what its threads hold in one round, whose barriers are the
   // cheaper (34 rows: 4.8 us in a graph, 5.4 with 1024 threads); otherwise as many
-  // large ones as give every thread one token, up to the largest cluster (1024
-  // rows, 128,000 tokens: 27 us on 4 CTAs, 17 on 8, 12 on 16).
+  // large ones as give every thread one token, up to the largest cluster that the
+  // device can place (1024 rows, 128,000 tokens: 27 us on 4 CTAs, 17 on 8, 12 on 16).
   const int threads = batch <= kSlotSmall && max_tokens <= kSlotSmall ? kSlotSmall : kSlotThreads;
   int C = 1;
-  while (C < kSlotMaxCluster && static_cast<int64_t>(C) * kSlotThreads < max_tokens) C *= 2;
+  while (C < most && static_cast<int64_t>(C) * kSlotThreads < max_tokens) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);

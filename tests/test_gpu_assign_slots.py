@@ -217,3 +217,35 @@ def test_positions_of_refused_rows_past_32_bits(dev):
         assert ref["status"][1] == 32
         at = int(ref["cu_new"][1])
         assert ref["positions"][at: at + 4].tolist() == [ctx + i for i in range(4)]
+
+
+def test_first_call_of_a_process_captured(dev):
+    """The device's limits are asked for during the first call, which may be a captured one, of a
+    size that takes the largest cluster."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch, sparse_attention_kv_row_gb300 as hs
+dev = torch.device("cuda:0")
+z = lambda n, d=torch.int32: torch.zeros(n, dtype=d, device=dev)
+n, bs = 20000, 16
+new, table = z(2), torch.full((2, 1300), -1, dtype=torch.int32, device=dev)
+new[:] = 9000
+free, top = torch.arange(1300, dtype=torch.int32, device=dev), z(1)
+top[:] = 1300
+cu, seq, loc, ctx, req = z(3), z(2), z(n, torch.int64), z(2), torch.arange(2, device=dev)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    hs.assign_slots(ctx, new, req, table, free, top, block_size=bs, cu_new=cu, seq_lens=seq, cache_loc=loc)
+graph.replay()
+torch.cuda.synchronize()
+assert cu.tolist() == [0, 9000, 18000] and int(top) == 1300 - 2 * 563
+assert sorted(loc[:18000].tolist())[0] >= 0 and bool((loc[18000:] == -1).all())
+assert len(set(loc[:18000].tolist())) == 18000
+print("good")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "good" in r.stdout, r.stderr[-2000:]
