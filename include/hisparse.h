@@ -606,10 +606,12 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  * reports HS_ST_TIMEOUT and the outputs of the call are undefined; treat the
  * context as suspect.
  * Limits: head_dim <= 512, num_heads a multiple of num_kv_heads, batch <= 2048,
- * n_tokens and max_q_len * num_heads < 2^31 (else HS_ERR_UNSUPPORTED); L at most 2^30, and so short that 32-bit whole numbers
- * count the batch's tiles: batch * num_kv_heads * L < 2^36, and (n_tokens *
- * max(1, num_heads / num_kv_heads / 128) / 256 + batch) * num_kv_heads * L < 2^38
- * are enough (HS_ST_BAD_STATE for a longer row).
+ * n_tokens and max_q_len * num_heads < 2^31 (else HS_ERR_UNSUPPORTED); L at most
+ * 2^30, and so short that 32-bit whole numbers count the batch's tiles: with u =
+ * 2 * floor(128 * num_kv_heads / num_heads) tokens a unit (2 for more than 128 query
+ * heads to a kv head), batch * num_kv_heads * (L + 64) <= 2^36 - 32 and (n_tokens /
+ * u + batch) * num_kv_heads * (L + 1152) <= 2^38 - 128 are enough (HS_ST_BAD_STATE
+ * for a longer row).
  */
 typedef struct hs_paged_attention_args {
   int32_t batch, num_heads, num_kv_heads, head_dim;

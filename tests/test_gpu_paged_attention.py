@@ -612,3 +612,26 @@ def test_workspace_sizes_are_asked_for_once(dev):
             hs.paged_attention(q, kv[0], kv[1], table, i(0, 1, 2)[:batch], cu, i(n, 40, 50)[:batch],
                                torch.empty_like(q), max_q_len=n)
     assert hs._attention_workspace.cache_info().misses <= 20
+
+
+@pytest.mark.parametrize("over", [0, 1])
+def test_longest_row_of_a_large_call(dev, over):
+    """The bound on a row's length where units of whole tokens are counted, at its last length and
+    one past it: 2^20 tokens in units of 32, 8 kv heads."""
+    hs = _hs()
+    T, heads, kv_heads, dim, ps = 1 << 20, 64, 8, 64, 1 << 15
+    units = T // (2 * (128 // (heads // kv_heads))) + 1
+    most = ((2 ** 31 - 1) // (units * kv_heads) - 8) * 128
+    assert most == 1047424
+    g = torch.Generator(device=dev).manual_seed(1)
+    q = torch.randn(1, heads, dim, generator=g, device=dev).to(torch.bfloat16).expand(T, heads, dim)
+    out = torch.full((1, heads, dim), -7.0, dtype=torch.bfloat16, device=dev).expand(T, heads, dim)
+    kc = torch.zeros(1, ps, kv_heads, dim, dtype=torch.bfloat16, device=dev)
+    vc = torch.ones_like(kc)
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    status = i(-1)
+    hs.paged_attention(q, kc, vc, torch.zeros(1, 33, dtype=torch.int32, device=dev), i(0), i(0, 1),
+                       i(most + over), out, max_q_len=64, page_size=ps, status=status)
+    # equal weights, each of them 1: their sums are whole numbers, and their ratio is 1
+    assert status.tolist() == [32 if over else 0]
+    assert bool((out[0] == (-7.0 if over else 1.0)).all())
