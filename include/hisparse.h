@@ -599,8 +599,11 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  * head_dim 64 or 128 the products run on the tensor cores, with the softmax
  * weights rounded to in_dtype, or to fp16 for HS_DT_E4M3, whose values are
  * widened exactly; bf16 queries are then taken as fp16 after a power of two per
- * row, exact to 2^-22 of the row's largest.  Results do not depend on what else
- * is in the batch, except through the order of fp32 sums.
+ * row, exact to 2^-22 of the row's largest.  What other requests hold has no effect
+ * on a request's results.  How many they are and how long decides where the batch's
+ * work is cut: a request of more keys than a tile (32; 128 above 16 query rows a kv
+ * head) may then be joined from other parts, whose weights are rounded by their own
+ * running maxima and summed in another order, each time within the same bounds.
  * Time-out: the waits of the kernel for long chunks are bounded.  If one runs out
  * (the GPU did not complete a copy or a product within two seconds), every row
  * reports HS_ST_TIMEOUT and the outputs of the call are undefined; treat the

@@ -635,3 +635,68 @@ def test_longest_row_of_a_large_call(dev, over):
     # equal weights, each of them 1: their sums are whole numbers, and their ratio is 1
     assert status.tolist() == [32 if over else 0]
     assert bool((out[0] == (-7.0 if over else 1.0)).all())
+
+
+@pytest.mark.parametrize("lens", [DECODE, DRAFTS, CHUNKS], ids=["decode", "drafts", "chunks"])
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+def test_other_requests_values_have_no_effect(dev, lens, cache):
+    """Other queries, keys and values beside a request of the same lengths: its own bits stay."""
+    hs = _hs()
+    kw = dict(heads=8, kv_heads=2, dim=128, dtype="bf16", cache=cache, seed=24)
+    x = PagedInputs(lens, **kw)
+    first = x.call(hs, dev)
+    for b, (c, n) in enumerate(lens):
+        if c is None or n == 0:
+            continue
+        y = PagedInputs(lens, **kw)
+        kept = y.table[y.req[b]]
+        kept, rows = kept[kept >= 0], slice(int(y.cu[b]), int(y.cu[b + 1]))
+        q = torch.full_like(y.q, 1000.0)
+        q[rows] = y.q[rows]
+        y.q = q
+        others = torch.ones(len(y.kc), dtype=torch.bool)
+        others[torch.from_numpy(kept).long()] = False
+        for cache_, value in ((y.kc, 400.0), (y.vc, -400.0)):
+            bits = torch.uint8 if y.fp8 else torch.int16
+            cache_.view(bits)[others] = torch.tensor([value]).to(cache_.dtype).view(bits)
+        out, lse, _ = y.call(hs, dev)
+        assert torch.equal(out[rows], first[0][rows]) and torch.equal(lse[rows], first[1][rows])
+
+
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+def test_requests_alone_and_in_another_order(dev, long, cache):
+    """Requests of one tile of keys are never cut: the same bits alone, together and in any order.
+    Longer ones are cut elsewhere, so that their weights are rounded by another running maximum:
+    each within the bound, and so within twice the bound of each other."""
+    hs = _hs()
+    lens = DECODE + DRAFTS + (CHUNKS if long else [])
+    kw = dict(heads=4, kv_heads=2, dim=64, dtype="bf16", cache=cache)
+    x = PagedInputs(lens, seed=25, **kw)
+    top = x.max_q
+    together = x.call(hs, dev)
+    tol_out, tol_lse = x.tolerance(x.plain(), True)
+    one_tile = 128 if top * 2 > 16 else 32
+
+    def pick(order):
+        """The same data with the batch rows in `order`."""
+        y = PagedInputs(lens, seed=25, **kw)
+        rows = [np.arange(x.cu[b], x.cu[b + 1]) for b in order]
+        y.q = x.q[np.concatenate(rows)]
+        y.T = len(y.q)
+        y.cu = np.concatenate([[0], np.cumsum([len(r) for r in rows])]).astype(np.int32)
+        y.req, y.seq = x.req[order], x.seq[order]
+        out, lse, _ = y.call(hs, dev, max_q=top)
+        for i, b in enumerate(order):
+            mine, theirs = slice(int(y.cu[i]), int(y.cu[i + 1])), torch.from_numpy(rows[i])
+            for a, c, tol in ((out, together[0], tol_out), (lse, together[1], tol_lse)):
+                a, c = a[mine].cpu(), c.cpu()[theirs]
+                if x.seq[b] <= one_tile:
+                    assert torch.equal(a, c)
+                else:
+                    assert bool(((a.double() - c.double()).abs() <= 2 * tol[theirs]).all())
+
+    pick(list(range(len(lens)))[::-1])
+    for b, (c, n) in enumerate(lens):
+        if c is not None and n > 0:
+            pick([b])
