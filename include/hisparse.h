@@ -516,7 +516,9 @@ hs_err hs_assign_slots(const void* ctx_lens, const int32_t* new_lens, const void
  *  k_scale, v_scale  device fp32 [1] or NULL (HS_DT_E4M3 only)
  *  status      int32 [1] or NULL: HS_ST_BAD_INDEX is OR-ed in when a token's
  *              slot is outside [0, num_slots) (its K and V are skipped) or its
- *              position outside [0, max_pos) (its q and K are skipped)
+ *              position outside [0, max_pos) (its q and K are skipped).  A step
+ *              padded with slots of -1 (hs_assign_slots behind its last token)
+ *              sets it too: the status of hs_assign_slots tells its bad rows
  * A head whose x are all zero stays zero, with eps = 0 too.  The sum of squares is
  * held in fp32: a head with values past about 1e18 (whose sum overflows) becomes
  * zeros, and with eps = 0 so does one below 1e-23.  Limits: head_dim <= 1024,
@@ -580,12 +582,13 @@ hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* args, hs_stream_t strea
  *  scale       positive; k_scale, v_scale  device fp32 [1] or NULL (HS_DT_E4M3
  *              only), positive too
  *  max_q_len   a bound on every request's n (host value; it sizes the launch)
- *  status      int32 [batch] or NULL, overwritten
+ *  status      int32 [batch] or NULL, overwritten (the only sign of a time-out)
  *  workspace   device memory, 256-byte aligned, of at least
  *              hs_paged_attention_workspace_bytes(args) bytes (NULL if that is
  *              0).  Its contents need not be set and mean nothing afterwards;
  *              calls that may run at the same time (two streams, two graphs)
  *              need one each.
+ * out and lse overlap no other buffer (not checked).
  * Padding rows and rows whose queries lie outside [0, n_tokens) or number less
  * than 0 write nothing (status 0 / HS_ST_BAD_STATE); rows with r >= num_states,
  * n > max_q_len or L beyond table_blocks * page_size write nothing and report

@@ -2,7 +2,8 @@
 // sm_103a: the entry point, the general kernel and the status words.
 //
 // One pass over the keys with the running maximum m and sum l of the softmax
-// (scores in units of log2): for each new score s, with m' = max(m, s),
+// (Milakov and Gimelshein, 2018; scores in units of log2): for each new score s, with
+// m' = max(m, s),
 //   o <- o 2^(m - m') + 2^(s - m') v,   l <- l 2^(m - m') + 2^(s - m'),
 // and the result is o / l, with lse = ln 2 (m + log2 l).
 //

@@ -275,7 +275,9 @@ struct WideRows : SplitTypes<kIn, kFp8, D> {
         o[i][3] *= back[1];
       }
     }
-    // The weights are rounded to the products' type (half a step each).
+    // The weights are rounded to the type of V, as one product wants of its operands:
+    // half a step each, whose errors average out over the keys.  The sum above keeps
+    // them whole, for the log-sum.
     uint32_t w[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -467,7 +469,8 @@ struct NarrowRows : SplitTypes<kIn, kFp8, D> {
         o[i][3] *= back[1];
       }
     }
-    // The weights, rounded to the products' type, turned from (key, rows) to (row, keys).
+    // The weights, rounded to V's type as in the wide form, turned from (key, rows) to
+    // (row, keys).
     uint32_t w[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

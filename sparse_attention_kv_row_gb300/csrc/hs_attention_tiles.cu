@@ -13,12 +13,14 @@
 //
 // The running maximum m is only raised, and O rescaled, when a row's new
 // maximum is more than 2^8 above the old one: a larger weight is as good in the
-// products' type, and sums stay in fp32.
+// products' type, and sums stay in fp32.  (These roles and this rule are published
+// practice for attention on these tensor cores, written here from the formulas.)
 //
-// Measured (GB300, D = 128, bf16): about 1.6 us for a pair of tiles and 4 us for a
-// unit's beginning and end; two chunks of 2048 queries over 16 K keys 645 us, 1.7
-// PFLOP/s at the power limit with the tensor pipe 77 % busy; four 2048-token
-// prompts 116 us; a mixed batch over E4M3 196 us.
+// Measured (GB300, D = 128, bf16, replayed from a graph): about 1.6 us for a pair of
+// tiles and 4 us for a unit's beginning and end; two chunks of 2048 queries over 16 K
+// keys 650 us, 1.7 PFLOP/s at the power limit with the tensor pipe 77 % busy (730 us
+// a call, 1.5 PFLOP/s, where calls follow each other without a pause); four
+// 2048-token prompts 115 us; a mixed batch over E4M3 193 us.
 //
 // The flattened list of tiles of all units, each with one more for its fixed
 // cost, is cut into equal runs, one per SM.  A unit that a run covers alone is
@@ -53,9 +55,10 @@ constexpr float kRaise = 8.f;      // log2 of how far weights may exceed 1
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // A unit's fixed cost in tiles: its queries' way in and its outputs' way out
-// (about 4 us over a 16-bit cache and 6 over an FP8 one, to 1.6 and 1.8 a tile;
-// with 2 and 3 four 2048-token prompts took 117 and 119 us, a mixed FP8 batch 204
-// and 202).
+// (about 4 us over a 16-bit cache and 6 over an FP8 one, to 1.6 and 1.8 a tile of
+// D = 128).  With 1, 2, 3 and 4, in us: four 2048-token prompts over bf16 135, 116,
+// 119, 122 at D = 128 and 103, 98, 100, 104 at D = 64; over FP8 208, 171, 167, 171
+// and 138, 115, 115, 121; a mixed FP8 batch 212, 196, 194, 191 and 154, 140, 139, 138.
 constexpr int unit_cost(bool fp8) { return fp8 ? 3 : 2; }
 
 struct TilesParams : AttnParams {
@@ -591,7 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t x = fma2(two_words(s[q][2 * c], s[q][2 * c + 1]), sc2, ref2);
             const float a = fast_exp2(low_float(x)), b = fast_exp2(high_float(x));
             sum[c & 1] = add2(sum[c & 1], two_floats(a, b));
-            w16[c] = pack2t<kBf16>(a, b);  // half a step off each
+            // The weights take the type of V, as one product wants of its operands:
+            // half a step off each, whose errors average out over the keys.  The sum
+            // keeps them whole, for the log-sum.
+            w16[c] = pack2t<kBf16>(a, b);
           }
           tmem_st16(s_at + q * 16, w16);
           if (q == 1) {

@@ -603,8 +603,10 @@ extern "C" hs_err hs_qk_norm_rope_store(const hs_qk_norm_rope_args* a, hs_stream
   const uint32_t per_token = rows ? static_cast<uint32_t>(p.units_q + 2 * p.units_kv) : all;
   p.div_units = FastDiv{fastdiv_magic(per_token), per_token};
   // Heads that lie one behind the other are brought into L2 a wave of warps ahead
-  // where there are several waves (16384 tokens of 48 heads: 89 us without, 83
-  // with; 4097 tokens of 40 half-size heads, two waves: 12.5 and 13.1).
+  // where there are more than four waves.  Without and with it, inputs in HBM: 16384
+  // tokens of 48 heads of 128 (27 waves) 79.6 and 72.1 us, 4097 of 40 heads of 64 into
+  // FP8 (4.5 waves) 14.3 and 14.1, 4097 of 6 heads of 128 (3.4 waves) 9.8 and 9.6;
+  // inputs in L2: 10.9 and 10.8 for the second, but 7.5 and 7.9 for the third.
   const bool dense = a->q_stride_head == a->head_dim && a->k_stride_head == a->head_dim &&
                      a->v_stride_head == a->head_dim;
   const uint32_t wave = static_cast<uint32_t>(dev.sm_count) * 3 * kNormWarps;
