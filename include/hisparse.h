@@ -1,8 +1,9 @@
 /*
  * hisparse.h -- C ABI of libhisparse: the HiSparse decode-time KV-row swap-in,
- * the indexed KV-row movers and the operators around a paged KV cache (slot
- * assignment, query/key norm with rotation and cache write, attention), as
- * hand-written CUDA kernels for GB300 (sm_103a).
+ * the indexed KV-row movers, the operators around a paged KV cache (slot
+ * assignment, query/key norm with rotation and cache write, attention) and
+ * those of a latent-attention layer (residual norm, latent rows, attention over
+ * them), as hand-written CUDA kernels for GB300 (sm_103a).
  *
  * Conventions shared by every entry point
  *  - All calls are asynchronous and stream-ordered on `stream` (a CUDA runtime
@@ -19,7 +20,8 @@
  *    thread.  Empty work (batch == 0, top_k == 0, n == 0) returns HS_OK and
  *    launches nothing.
  *  - Rows are opaque bytes and no floating point is involved, except in
- *    hs_fp8_store_kv, hs_qk_norm_rope_store and hs_paged_attention.
+ *    hs_fp8_store_kv, hs_qk_norm_rope_store, hs_paged_attention,
+ *    hs_add_rms_norm, hs_latent_norm_rope_store and hs_latent_attention.
  */
 #ifndef HISPARSE_H
 #define HISPARSE_H
@@ -658,6 +660,192 @@ hs_err hs_paged_attention(const hs_paged_attention_args* args, hs_stream_t strea
 hs_err hs_paged_attention_timeout_selftest(const hs_paged_attention_args* args,
                                            hs_stream_t stream);
 
+/* hs_add_rms_norm_args.flags */
+#define HS_SCALE_POW2 1 /* scales of 8-bit values are rounded up to powers of two */
+
+/*
+ * hs_add_rms_norm -- the residual's addition and a root-mean-square norm, in the
+ * inputs' type, as E4M3 codes with scales, or both, in one pass.  For token t:
+ *   r[d] = round(x[d] + residual[d])     (r = x where residual is NULL), kept in
+ *          residual_out where that is given
+ *   y[d] = r[d] / sqrt(mean(r^2) + eps) * weight[d]      (weight NULL: times 1)
+ *   out[d] = round(y[d])
+ *   for every group g of `group` dims (the last may be shorter; 0: one group of
+ *   the whole token), with a = max |y| of the group:
+ *   s = a * fp32(1 / 448), rounded up to a power of two with HS_SCALE_POW2
+ *   codes[d] = e4m3(fp32(y[d] * fp32(1 / s)))  (0 where s is 0),  scales[t][g] = s
+ * The sum is rounded to the inputs' type first, so that y belongs to the residual
+ * stream that the next layers read; everything else is held in fp32 and rounded
+ * once.  A NaN in a token makes all its y NaN, an infinity its own (the others become
+ * zeros); a group that holds a NaN has NaN for scale and codes.  Defined by this library, beside hs_qk_norm_rope_store
+ * (the norm) and hs_fp8_store_kv (the codes).
+ *
+ *  x, residual, residual_out, out  dtype (HS_DT_F32 / F16 / BF16) [n_tokens, dim],
+ *              strides in elements, dims contiguous.  residual_out may be residual
+ *              or x, and out may be x or residual (each with that one's stride);
+ *              they may not be the same
+ *  weight      dtype [dim] or NULL
+ *  codes       E4M3 bytes [n_tokens, dim], stride in bytes, or NULL
+ *  scales      fp32, strides in elements for tokens and groups (either order);
+ *              NULL iff codes is
+ * out or codes must be given (or both); residual_out needs residual.  A token whose
+ * r are all zero gives zeros, with eps = 0 too.  The sum of squares is held in fp32,
+ * of scaled values where it would leave its range.  A scale below fp32's smallest
+ * normal number (a below 5e-36) is 0.  Limits: dim <= 65536 (else HS_ERR_UNSUPPORTED).
+ * Preconditions (not checked): no buffer overlaps another but in the ways above.
+ */
+typedef struct hs_add_rms_norm_args {
+  int64_t n_tokens;
+  int32_t dim, dtype, group, flags;
+  float eps;
+  int32_t reserved; /* 0 */
+  const void* x; int64_t x_stride;
+  const void* residual; int64_t residual_stride;
+  void* residual_out; int64_t residual_out_stride;
+  const void* weight;
+  void* out; int64_t out_stride;
+  uint8_t* codes; int64_t codes_stride;
+  float* scales; int64_t scales_stride_token; int64_t scales_stride_group;
+} hs_add_rms_norm_args;
+
+hs_err hs_add_rms_norm(const hs_add_rms_norm_args* args, hs_stream_t stream);
+
+/* How a latent row is kept: what hs_latent_norm_rope_store writes, hs_swap_in and
+ * the movers carry as bytes and hs_latent_attention reads.  A row has latent_dim
+ * latent values (keys and values of all query heads) and rope_dim rotary ones
+ * (keys only).
+ *  HS_ROW_SAME  latent_dim + rope_dim values of the operator's type
+ *  HS_ROW_E4M3  latent_dim E4M3 codes, an fp32 scale for each 128 of them (value =
+ *               code * scale), rope_dim values of the operator's 16-bit type: 656
+ *               bytes for 512 + 64 dims */
+#define HS_ROW_SAME 0
+#define HS_ROW_E4M3 1
+
+/*
+ * hs_latent_norm_rope_store -- a token's latent row from its projection: the norm of
+ * the latent, rotary positions of the rotary key, and the write of both to row
+ * loc[t]; and the same rotation of the rotary part of every query head.  With
+ * p = positions[t] and w = weight:
+ *   c[d] = latent[d] / sqrt(mean(latent^2) + eps) * w[d]      (c = latent, w NULL)
+ *   k = k_pe and, for each head, q = q_pe turned by the angles of p, as in
+ *   hs_qk_norm_rope_store with rot_dim = rope_dim (HS_ROPE_INTERLEAVED too)
+ *   HS_ROW_SAME: row = [round(c), round(k)]
+ *   HS_ROW_E4M3: codes and scales of c in groups of 128 as in hs_add_rms_norm
+ *   (HS_LATENT_SCALE_POW2 for powers of two), then round(k)
+ *   q_out = round(q)
+ * Everything is computed in fp32 and rounded once.  Defined by this library, beside
+ * hs_qk_norm_rope_store; the 656-byte row is the one of the swap-in benchmark.
+ *
+ *  latent [n_tokens, latent_dim], k_pe [n_tokens, rope_dim] of in_dtype, token strides
+ *              in elements, dims contiguous (views of one projection's output)
+ *  weight      in_dtype [latent_dim] or NULL (no norm)
+ *  cos_sin     fp32 [max_pos, rope_dim] contiguous, or NULL (no rotation; then
+ *              positions is NULL too)
+ *  positions   int64 [n_tokens]
+ *  q_pe, q_out in_dtype [n_tokens, num_heads, rope_dim], token and head strides in
+ *              elements; num_heads 0 and NULL: no queries.  q_out may be q_pe itself
+ *  rows        [num_rows] rows of row_format, row_stride bytes apart
+ *  loc         int64 [n_tokens]
+ *  status      int32 [1] or NULL: HS_ST_BAD_INDEX is OR-ed in when a token's loc is
+ *              outside [0, num_rows) (its row is skipped) or its position outside
+ *              [0, max_pos) (its row and queries are skipped)
+ * HS_ROW_E4M3 wants 16-bit inputs and latent_dim a multiple of 128.  A latent of
+ * zeros stays zero, with eps = 0 too; the sum of squares is held as there.
+ * Limits: latent_dim <= 1024, rope_dim even and <= 256, num_heads * rope_dim < 2^31
+ * (else HS_ERR_UNSUPPORTED).
+ * Preconditions (not checked): loc values in range are distinct; no buffer overlaps
+ * another, but for q_out = q_pe.
+ */
+#define HS_LATENT_SCALE_POW2 2 /* beside HS_ROPE_INTERLEAVED in flags */
+typedef struct hs_latent_rows_args {
+  int64_t n_tokens;
+  int32_t latent_dim, rope_dim, num_heads;
+  int32_t in_dtype, row_format, flags;
+  float eps;
+  int32_t reserved; /* 0 */
+  const void* latent; int64_t latent_stride;
+  const void* k_pe; int64_t k_pe_stride;
+  const void* weight;
+  const float* cos_sin; int64_t max_pos;
+  const int64_t* positions;
+  const void* q_pe; int64_t q_stride_token; int64_t q_stride_head;
+  void* q_out; int64_t out_stride_token; int64_t out_stride_head;
+  void* rows; int64_t row_stride; int64_t num_rows;
+  const int64_t* loc;
+  int32_t* status;
+} hs_latent_rows_args;
+
+hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t stream);
+
+/*
+ * hs_latent_attention -- attention whose keys and values are latent rows that all
+ * query heads share (the absorbed form: the queries have been multiplied by the key
+ * up-projection, the outputs are still to be by the value one).  With R = latent_dim
+ * and row_j the R + rope_dim values of row j, for token t and head h:
+ *   s_j = scale * (q[t][h] . row_j)
+ *   out[t][h] = sum_j exp(s_j - lse) * row_j[0..R),   lse[t][h] = log(sum_j exp(s_j))
+ * Which rows token t sees is given in one of two ways:
+ *  - flags & HS_LATENT_INDEX: the rows row_index[t][0..top_k), as hs_swap_in emits
+ *    them (out_rows).
+ *    A negative entry is no row.  One of num_rows or more is none either, and sets
+ *    HS_ST_BAD_INDEX in status[t].  An entry listed twice counts twice.
+ *  - otherwise by block tables, as in hs_paged_attention without a window: request
+ *    b's token t in [cu_q[b], cu_q[b+1]) has position p = seq_lens[b] - n + (t -
+ *    cu_q[b]) and sees the positions 0..p, position j in row block_table[r][j /
+ *    page_size] * page_size + j % page_size.  Padding rows, rows that cannot be
+ *    served and their status bits are those of hs_paged_attention; a block outside
+ *    [0, num_rows / page_size) that a query of the request sees stands for rows of
+ *    zeros and sets HS_ST_BAD_INDEX.
+ * A token that sees no row gives zeros and lse = -inf; with a NaN among its scores
+ * both are NaN.  Rows that a token does not see have no effect on it whatever they
+ * hold, but for a NaN or an infinity in a row that another token of its request sees.
+ * Defined by this library: the attention behind the swap-in, which resolves a
+ * selection to hot-buffer rows.
+ *
+ *  q           in_dtype [n_tokens, num_heads, R + rope_dim], out in_dtype [n_tokens,
+ *              num_heads, R]: token and head strides in elements, dims contiguous
+ *  lse         fp32 [n_tokens, num_heads] contiguous, or NULL
+ *  rows        [num_rows] rows of row_format, row_stride bytes apart
+ *  row_index   int32 [n_tokens, >=top_k], stride in elements (NULL if top_k is 0)
+ *  block_table, req_state, cu_q, seq_lens, max_q_len, page_size, batch, flags: as in
+ *              hs_paged_attention (all unused, and batch 0, with HS_LATENT_INDEX)
+ *  scale       positive
+ *  status      int32, overwritten, or NULL: [n_tokens] with HS_LATENT_INDEX, else [batch]
+ *  workspace   as in hs_paged_attention, hs_latent_attention_workspace_bytes of it
+ * out and lse overlap no other buffer (not checked).  Rows of q that belong to no
+ * request are left as they were in out and lse.
+ * Scores, sums and outputs are accumulated in fp32.
+ * Limits: R <= 512, rope_dim <= 256, batch <= 2048, num_rows, n_tokens, top_k and
+ * max_q_len * num_heads < 2^31, R a multiple of 128 for HS_ROW_E4M3, which wants
+ * 16-bit types (else HS_ERR_UNSUPPORTED); sequence lengths as in hs_paged_attention
+ * (2^30 at most, HS_ST_BAD_STATE beyond).
+ */
+#define HS_LATENT_INDEX 4 /* beside HS_SEQ_LENS_I64 and HS_REQ_STATE_I64 in flags */
+typedef struct hs_latent_attention_args {
+  int32_t batch, num_heads, latent_dim, rope_dim;
+  int32_t in_dtype, row_format;
+  int32_t flags, page_size;
+  int32_t max_q_len, top_k;
+  float scale;
+  int32_t table_blocks;
+  int64_t n_tokens;
+  const void* q; int64_t q_stride_token; int64_t q_stride_head;
+  void* out; int64_t out_stride_token; int64_t out_stride_head;
+  float* lse;
+  const void* rows; int64_t row_stride; int64_t num_rows;
+  const int32_t* row_index; int64_t row_index_stride;
+  const int32_t* block_table; int64_t block_table_stride; int64_t num_states;
+  const void* req_state; const int32_t* cu_q; const void* seq_lens;
+  int32_t* status;
+  void* workspace; int64_t workspace_bytes;
+} hs_latent_attention_args;
+
+/* Bytes of workspace that this call needs on the current device (0 for none,
+ * negative hs_err on bad arguments).  It depends on sizes and types only. */
+int64_t hs_latent_attention_workspace_bytes(const hs_latent_attention_args* args);
+
+hs_err hs_latent_attention(const hs_latent_attention_args* args, hs_stream_t stream);
+
 /*
  * hs_probe_read -- measurement utility, not part of the method: stream-read
  * `bytes` bytes (16-byte aligned pointer, bytes % 16 == 0) from device or
@@ -693,7 +881,7 @@ const char* hs_last_error(void);
  */
 hs_err hs_wait_selftest(int32_t max_polls, int32_t* status, hs_stream_t stream);
 
-#define HS_ABI_VERSION 9
+#define HS_ABI_VERSION 10
 int32_t hs_abi_version(void);
 
 #ifdef __cplusplus

@@ -15,6 +15,10 @@ Entry points (same names as the C ABI):
   assign_slots(...)        hs_assign_slots       -- block tables and slot maps from lengths
   qk_norm_rope_store(...)  hs_qk_norm_rope_store -- q/k norm, rotary positions, cache write
   paged_attention(...)     hs_paged_attention    -- new tokens' attention over the paged cache
+  add_rms_norm(...)            hs_add_rms_norm           -- residual addition, norm, 8-bit codes
+  latent_norm_rope_store(...)  hs_latent_norm_rope_store -- latent rows of new tokens
+  latent_attention(...)        hs_latent_attention       -- attention over indexed latent rows
+  paged_latent_attention(...)  hs_latent_attention       -- the same over block tables
 """
 from __future__ import annotations
 
@@ -34,7 +38,9 @@ __all__ = ["swap_in", "swap_in_args", "make_swap_in_args", "gather_misses", "fp8
            "store_kv", "transfer_kv",
            "transfer_kv_layers", "probe_read", "assign_slots", "qk_norm_rope_store",
            "paged_attention", "paged_attention_workspace_bytes",
-           "paged_attention_timeout_selftest", "swap_in_smem_bytes", "library_path",
+           "paged_attention_timeout_selftest", "add_rms_norm", "latent_norm_rope_store",
+           "latent_attention", "latent_attention_workspace_bytes", "paged_latent_attention",
+           "paged_latent_attention_workspace_bytes", "swap_in_smem_bytes", "library_path",
            "HisparseError", "SwapInArgs"]
 
 
@@ -753,6 +759,16 @@ def paged_attention_timeout_selftest(q, k_cache, v_cache, block_table, req_state
             k_scale, v_scale, page_size, None, status, None, stream)
 
 
+def _call_space(n, device, stream, raw, dev):
+    """n bytes of workspace for one call on the stream ``raw``."""
+    if stream is None or raw == _current_stream(dev):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    # Memory in that stream's order: what the current stream has given back may still be in
+    # use there, and what is given back here is reused only behind this call.
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _attend(where, fn, q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens, out, max_q_len,
             scale, window, k_scale, v_scale, page_size, lse, status, workspace, stream) -> None:
     dev, fields = _attention_block(q, k_cache, v_cache, block_table, req_state, cu_q, seq_lens,
@@ -767,13 +783,256 @@ def _attend(where, fn, q, k_cache, v_cache, block_table, req_state, cu_q, seq_le
     else:
         n = _attention_need(dev, fields)
         if n > 0:
-            if stream is None or raw == _current_stream(dev):
-                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-            else:
-                # Memory in that stream's order: what the current stream has given back may
-                # still be in use there, and what is given back here is reused only behind
-                # this call.
-                with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=q.device)):
-                    workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            workspace = _call_space(n, q.device, stream, raw, dev)
             space_p = workspace.data_ptr()
     _launch(dev, where, fn, _capi.PAGED_ATTENTION.pack(*fields, space_p, n), raw)
+
+
+def _token_rows(t, dtype, shape, name):
+    """Address and token stride of [tokens, dim] with contiguous dims."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    token, last = t.stride()
+    tokens, dim = shape
+    if dim > 1 and last != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return t.data_ptr(), token if tokens > 1 else dim
+
+
+def add_rms_norm(x, weight, out=None, *, residual=None, residual_out=None, eps=1e-6, codes=None,
+                 scales=None, group=0, pow2_scales=False, stream=None) -> None:
+    """Add ``residual`` [T, D] to ``x`` [T, D] in their type, keep the sum in ``residual_out``
+    (default ``residual`` itself), norm it (root mean square, times ``weight`` [D] or None) and
+    write the result to ``out`` in the inputs' type, to ``codes`` (float8_e4m3fn or uint8) with
+    fp32 ``scales`` [T, ceil(D / group)], or to both (see include/hisparse.h).  ``group`` 0 is one
+    scale a token; ``pow2_scales`` rounds scales up to powers of two.  ``out`` may be ``x``."""
+    dt = x.dtype
+    if dt not in _FP8_IN:
+        raise TypeError("x must be float32, float16 or bfloat16")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [tokens, dim], got {list(x.shape)}")
+    if group < 0:
+        raise ValueError("group must be >= 0")
+    shape = x.shape
+    T, D = shape
+    x_a = _token_rows(x, dt, shape, "x")
+    res_a = keep_a = out_a = codes_a = (0, 0)
+    scales_a = (0, 0, 0)
+    if residual is not None:
+        res_a = _token_rows(residual, dt, shape, "residual")
+        if residual_out is None:
+            residual_out = residual
+        keep_a = _token_rows(residual_out, dt, shape, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    w_p = 0 if weight is None else _vector(weight, dt, D, "weight")
+    if out is not None:
+        out_a = _token_rows(out, dt, shape, "out")
+    elif codes is None:
+        raise ValueError("need out, codes or both")
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+    if codes is not None:
+        if codes.dtype not in _FP8_CACHE:
+            raise TypeError("codes must be float8_e4m3fn or uint8 (E4M3 codes)")
+        codes_a = _token_rows(codes, codes.dtype, shape, "codes")
+        groups = -(-D // group) if group else 1
+        if scales.dtype is not torch.float32:
+            raise TypeError(f"scales must be torch.float32, got {scales.dtype}")
+        if scales.shape != (T, groups):
+            raise ValueError(f"scales must be {[T, groups]}, got {list(scales.shape)}")
+        scales_a = (scales.data_ptr(), *scales.stride())
+    dev = _device_of(x, weight, residual, residual_out, out, codes, scales)
+    block = _capi.ADD_RMS_NORM.pack(
+        T, D, _FP8_IN[dt], group, _capi.SCALE_POW2 if pow2_scales else 0, eps, 0, *x_a, *res_a,
+        *keep_a, w_p, *out_a, *codes_a, *scales_a)
+    _launch(dev, "hs_add_rms_norm", _lib().hs_add_rms_norm, block, _raw_stream(stream, dev))
+
+
+def _latent_rows(rows, dtype, latent, rope):
+    """(row format, address, row stride in bytes, rows) of latent rows: [rows, latent + rope] of
+    ``dtype``, or uint8 [rows, bytes of codes, scales and rotary values]."""
+    if rows.dim() != 2:
+        raise ValueError(f"rows must be 2-D, got shape {list(rows.shape)}")
+    n, cols = rows.shape
+    stride, last = rows.stride()
+    if rows.dtype is torch.uint8:
+        kind, size, want = _capi.ROW_E4M3, 1, latent + latent // 32 + 2 * rope
+    elif rows.dtype is dtype:
+        kind, size, want = _capi.ROW_SAME, 4 if dtype is torch.float32 else 2, latent + rope
+    else:
+        raise TypeError(f"rows must be {dtype}, or uint8 (codes, scales and rotary values)")
+    if cols != want:
+        raise ValueError(f"rows of {latent} + {rope} dims have {want} entries, got {cols}")
+    if last != 1:
+        raise ValueError("rows must be contiguous")
+    return kind, rows.data_ptr(), (stride if n > 1 else cols) * size, n
+
+
+def latent_norm_rope_store(latent, k_pe, weight, cos_sin, positions, rows, loc, *, q_pe=None,
+                           q_out=None, eps=1e-6, interleaved=False, pow2_scales=False, status=None,
+                           stream=None) -> None:
+    """Norm ``latent`` [T, R] (root mean square, times ``weight`` [R]; None = no norm), rotate
+    ``k_pe`` [T, P] by the angles ``cos_sin`` [max_pos, P] (fp32, cosines then sines; None = no
+    rotation) of ``positions`` [T], and write both to row loc[t] of ``rows``: [N, R + P] of the
+    inputs' type, or uint8 [N, R + R / 32 + 2 P] (E4M3 codes, a scale for each 128, rotary values:
+    656 bytes for 512 + 64).  ``q_pe`` [T, heads, P] is rotated too, to ``q_out`` (may be q_pe).
+    See include/hisparse.h."""
+    dt = latent.dtype
+    if dt not in _FP8_IN:
+        raise TypeError("latent must be float32, float16 or bfloat16")
+    if latent.dim() != 2 or k_pe.dim() != 2:
+        raise ValueError("latent and k_pe must be [tokens, dim]")
+    (T, R), P = latent.shape, k_pe.shape[1]
+    l_a = _token_rows(latent, dt, (T, R), "latent")
+    k_a = _token_rows(k_pe, dt, (T, P), "k_pe")
+    kind, rows_p, row_stride, n = _latent_rows(rows, dt, R, P)
+    w_p = 0 if weight is None else _vector(weight, dt, R, "weight")
+    max_pos = cs_p = pos_p = heads = 0
+    if cos_sin is None:
+        positions = None
+    else:
+        cs_p, cs_stride, max_pos, rot = _matrix(cos_sin, torch.float32, "cos_sin")
+        if rot != P or (cs_stride != rot and max_pos > 1):
+            raise ValueError(f"cos_sin must be a contiguous [max_pos, {P}]")
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+        pos_p = _vector(positions, torch.int64, T, "positions")
+    q_a = o_a = (0, 0, 0)
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out go together")
+    if q_pe is not None:
+        if q_pe.dim() != 3:
+            raise ValueError(f"q_pe must be [tokens, heads, {P}], got {list(q_pe.shape)}")
+        heads = q_pe.shape[1]
+        q_a = _heads(q_pe, dt, "q_pe", T, heads, P)
+        o_a = _heads(q_out, dt, "q_out", T, heads, P)
+        if o_a[0] == q_a[0] and o_a != q_a and T > 0:
+            raise ValueError("q_out may be q_pe itself, not another view of its memory")
+    loc_p = _vector(loc, torch.int64, T, "loc")
+    st_p = 0 if status is None else _vector(status, torch.int32, 1, "status")
+    dev = _device_of(latent, k_pe, weight, cos_sin, positions, rows, loc, q_pe, q_out, status)
+    flags = (_capi.ROPE_INTERLEAVED if interleaved else 0) | (
+        _capi.LATENT_SCALE_POW2 if pow2_scales else 0)
+    block = _capi.LATENT_ROWS.pack(T, R, P, heads, _FP8_IN[dt], kind, flags, eps, 0, *l_a, *k_a,
+                                   w_p, cs_p, max_pos, pos_p, *q_a, *o_a, rows_p, row_stride, n,
+                                   loc_p, st_p)
+    _launch(dev, "hs_latent_norm_rope_store", _lib().hs_latent_norm_rope_store, block,
+            _raw_stream(stream, dev))
+
+
+def _latent_block(q, rows, out, lse):
+    """What both forms of latent attention share: (tokens, heads, R, P, dtype code, row format)
+    and the fields from q to num_rows."""
+    dt = q.dtype
+    if dt not in _FP8_IN:
+        raise TypeError("q must be float32, float16 or bfloat16")
+    if q.dim() != 3 or out.dim() != 3:
+        raise ValueError("q must be [tokens, heads, R + P], out [tokens, heads, R]")
+    T, heads, dims = q.shape
+    R = out.shape[2]
+    if not 0 < R <= dims:
+        raise ValueError(f"out has {R} dims of q's {dims}")
+    kind, rows_p, row_stride, n = _latent_rows(rows, dt, R, dims - R)
+    q_a = _heads(q, dt, "q", T, heads, dims)
+    o_a = _heads(out, dt, "out", T, heads, R)
+    lse_p = 0
+    if lse is not None:
+        lse_p, lse_stride, lse_rows, lse_cols = _matrix(lse, torch.float32, "lse")
+        if (lse_rows, lse_cols) != (T, heads) or (lse_stride != heads and T > 1):
+            raise ValueError(f"lse must be a contiguous [{T}, {heads}]")
+    return (T, heads, R, dims - R, _FP8_IN[dt], kind), (*q_a, *o_a, lse_p, rows_p, row_stride, n)
+
+
+def _indexed_fields(q, rows, row_index, out, scale, lse, status):
+    (T, heads, R, P, dt, kind), body = _latent_block(q, rows, out, lse)
+    idx_p, idx_stride, idx_rows, top_k = _matrix(row_index, torch.int32, "row_index")
+    if idx_rows != T:
+        raise ValueError(f"row_index must be [{T}, top_k], got {list(row_index.shape)}")
+    st_p = 0 if status is None else _vector(status, torch.int32, T, "status")
+    dev = _device_of(q, rows, row_index, out, lse, status)
+    return dev, (0, heads, R, P, dt, kind, _capi.LATENT_INDEX, 1, 0, top_k, scale, 0, T, *body,
+                 idx_p, idx_stride, 0, 0, 0, 0, 0, 0, st_p)
+
+
+def _paged_latent_fields(q, rows, block_table, req_state, cu_q, seq_lens, out, max_q_len,
+                         page_size, scale, lse, status):
+    (T, heads, R, P, dt, kind), body = _latent_block(q, rows, out, lse)
+    batch = cu_q.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_q needs batch + 1 entries")
+    cu_p = _vector(cu_q, torch.int32, batch + 1, "cu_q")
+    seq_p, wide_len = _lens(seq_lens, batch, "seq_lens")
+    req_p, wide_req = _lens(req_state, batch, "req_state")
+    table_p, table_stride, states, blocks = _matrix(block_table, torch.int32, "block_table")
+    st_p = 0 if status is None else _vector(status, torch.int32, batch, "status")
+    dev = _device_of(q, rows, block_table, req_state, cu_q, seq_lens, out, lse, status)
+    flags = (_capi.SEQ_LENS_I64 if wide_len else 0) | (_capi.REQ_STATE_I64 if wide_req else 0)
+    return dev, (batch, heads, R, P, dt, kind, flags, page_size, max_q_len, 0, scale, blocks, T,
+                 *body, 0, 0, table_p, table_stride, states, req_p, cu_p, seq_p, st_p)
+
+
+def _latent_workspace_bytes(dev, fields) -> int:
+    with torch.cuda.device(dev):
+        n = int(_lib().hs_latent_attention_workspace_bytes(
+            _capi.LATENT_ATTENTION.pack(*fields, 0, 0)))
+    if n < 0:
+        _capi.check(-n, "hs_latent_attention_workspace_bytes")
+    return n
+
+
+def latent_attention_workspace_bytes(q, rows, row_index, out) -> int:
+    """Bytes of workspace that ``latent_attention`` needs for tensors of these shapes and types."""
+    return _latent_workspace_bytes(*_indexed_fields(q, rows, row_index, out, 1.0, None, None))
+
+
+def latent_attention(q, rows, row_index, out, *, scale, lse=None, status=None, workspace=None,
+                     stream=None) -> None:
+    """Attention of q [T, heads, R + P] over latent rows that all heads share (the absorbed form):
+    keys are whole rows, values their first R dims, ``out`` is [T, heads, R].  Token t sees the
+    rows row_index[t] (int32 [T, top_k], as ``swap_in`` emits ``out_rows``; negative = none) of
+    ``rows`` (layouts as in ``latent_norm_rope_store``; see include/hisparse.h).  ``lse`` [T, heads]
+    gets the softmax's log-sum-exp, ``status`` [T] the HS_ST_* bits.  ``workspace`` (uint8, 256-byte
+    aligned, ``latent_attention_workspace_bytes`` of it) may be passed to keep one for a captured
+    graph; otherwise one is allocated for the call."""
+    dev, fields = _indexed_fields(q, rows, row_index, out, scale, lse, status)
+    _latent_attend(q, dev, fields, workspace, stream)
+
+
+def paged_latent_attention_workspace_bytes(q, rows, block_table, req_state, cu_q, seq_lens, out, *,
+                                           max_q_len, page_size) -> int:
+    """Bytes of workspace that ``paged_latent_attention`` needs for tensors of these shapes and
+    types."""
+    return _latent_workspace_bytes(*_paged_latent_fields(
+        q, rows, block_table, req_state, cu_q, seq_lens, out, max_q_len, page_size, 1.0, None, None))
+
+
+def paged_latent_attention(q, rows, block_table, req_state, cu_q, seq_lens, out, *, max_q_len,
+                           page_size, scale, lse=None, status=None, workspace=None,
+                           stream=None) -> None:
+    """Causal attention of the new tokens q [T, heads, R + P] over each request's latent rows,
+    found by block tables as in ``paged_attention``: request b has the queries cu_q[b] to
+    cu_q[b + 1] (at most ``max_q_len``), the last of its seq_lens[b] tokens; its position j is row
+    block_table[req_state[b]][j // page_size] * page_size + j % page_size of ``rows``.  The rest
+    as in ``latent_attention``; ``status`` is [batch]."""
+    dev, fields = _paged_latent_fields(q, rows, block_table, req_state, cu_q, seq_lens, out,
+                                       max_q_len, page_size, scale, lse, status)
+    _latent_attend(q, dev, fields, workspace, stream)
+
+
+def _latent_attend(q, dev, fields, workspace, stream) -> None:
+    raw = _raw_stream(stream, dev)
+    space_p = n = 0
+    if workspace is not None:
+        n = workspace.numel()
+        space_p = _vector(workspace, torch.uint8, n, "workspace")
+        _device_of(q, workspace)
+    else:
+        n = _latent_workspace_bytes(dev, fields)
+        if n > 0:
+            workspace = _call_space(n, q.device, stream, raw, dev)
+            space_p = workspace.data_ptr()
+    _launch(dev, "hs_latent_attention", _lib().hs_latent_attention,
+            _capi.LATENT_ATTENTION.pack(*fields, space_p, n), raw)

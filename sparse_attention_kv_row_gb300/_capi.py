@@ -28,7 +28,10 @@ OVERLAP_PREV = 4
 DT_F32, DT_F16, DT_BF16, DT_E4M3 = 0, 1, 2, 3
 ROPE_INTERLEAVED = 1
 XFER_HAS_V, XFER_DEVICE_SOURCES = 1, 2
-ABI_VERSION = 9
+ROW_SAME, ROW_E4M3 = 0, 1
+LATENT_INDEX = 4
+SCALE_POW2, LATENT_SCALE_POW2 = 1, 2
+ABI_VERSION = 10
 
 # Every symbol include/hisparse.h declares.
 EXPORTS = ("hs_swap_in", "hs_swap_in_smem_bytes", "hs_store_kv", "hs_transfer_kv",
@@ -36,7 +39,8 @@ EXPORTS = ("hs_swap_in", "hs_swap_in_smem_bytes", "hs_store_kv", "hs_transfer_kv
            "hs_abi_version", "hs_wait_selftest", "hs_swap_in_timeout_selftest",
            "hs_swap_in_layers", "hs_swap_in_layers_timeout_selftest", "hs_assign_slots",
            "hs_qk_norm_rope_store", "hs_paged_attention", "hs_paged_attention_workspace_bytes",
-           "hs_paged_attention_timeout_selftest")
+           "hs_paged_attention_timeout_selftest", "hs_add_rms_norm", "hs_latent_norm_rope_store",
+           "hs_latent_attention", "hs_latent_attention_workspace_bytes")
 
 
 class SwapInArgs(C.Structure):
@@ -109,6 +113,60 @@ class PagedAttentionArgs(C.Structure):
     ]
 
 
+class AddRmsNormArgs(C.Structure):
+    """Mirror of ``hs_add_rms_norm_args``."""
+    _fields_ = [
+        ("n_tokens", C.c_int64),
+        ("dim", C.c_int32), ("dtype", C.c_int32), ("group", C.c_int32), ("flags", C.c_int32),
+        ("eps", C.c_float), ("reserved", C.c_int32),
+        ("x", C.c_void_p), ("x_stride", C.c_int64),
+        ("residual", C.c_void_p), ("residual_stride", C.c_int64),
+        ("residual_out", C.c_void_p), ("residual_out_stride", C.c_int64),
+        ("weight", C.c_void_p),
+        ("out", C.c_void_p), ("out_stride", C.c_int64),
+        ("codes", C.c_void_p), ("codes_stride", C.c_int64),
+        ("scales", C.c_void_p), ("scales_stride_token", C.c_int64),
+        ("scales_stride_group", C.c_int64),
+    ]
+
+
+class LatentRowsArgs(C.Structure):
+    """Mirror of ``hs_latent_rows_args``."""
+    _fields_ = [
+        ("n_tokens", C.c_int64),
+        ("latent_dim", C.c_int32), ("rope_dim", C.c_int32), ("num_heads", C.c_int32),
+        ("in_dtype", C.c_int32), ("row_format", C.c_int32), ("flags", C.c_int32),
+        ("eps", C.c_float), ("reserved", C.c_int32),
+        ("latent", C.c_void_p), ("latent_stride", C.c_int64),
+        ("k_pe", C.c_void_p), ("k_pe_stride", C.c_int64),
+        ("weight", C.c_void_p),
+        ("cos_sin", C.c_void_p), ("max_pos", C.c_int64), ("positions", C.c_void_p),
+        ("q_pe", C.c_void_p), ("q_stride_token", C.c_int64), ("q_stride_head", C.c_int64),
+        ("q_out", C.c_void_p), ("out_stride_token", C.c_int64), ("out_stride_head", C.c_int64),
+        ("rows", C.c_void_p), ("row_stride", C.c_int64), ("num_rows", C.c_int64),
+        ("loc", C.c_void_p), ("status", C.c_void_p),
+    ]
+
+
+class LatentAttentionArgs(C.Structure):
+    """Mirror of ``hs_latent_attention_args``."""
+    _fields_ = [
+        ("batch", C.c_int32), ("num_heads", C.c_int32), ("latent_dim", C.c_int32),
+        ("rope_dim", C.c_int32), ("in_dtype", C.c_int32), ("row_format", C.c_int32),
+        ("flags", C.c_int32), ("page_size", C.c_int32), ("max_q_len", C.c_int32),
+        ("top_k", C.c_int32), ("scale", C.c_float), ("table_blocks", C.c_int32),
+        ("n_tokens", C.c_int64),
+        ("q", C.c_void_p), ("q_stride_token", C.c_int64), ("q_stride_head", C.c_int64),
+        ("out", C.c_void_p), ("out_stride_token", C.c_int64), ("out_stride_head", C.c_int64),
+        ("lse", C.c_void_p),
+        ("rows", C.c_void_p), ("row_stride", C.c_int64), ("num_rows", C.c_int64),
+        ("row_index", C.c_void_p), ("row_index_stride", C.c_int64),
+        ("block_table", C.c_void_p), ("block_table_stride", C.c_int64), ("num_states", C.c_int64),
+        ("req_state", C.c_void_p), ("cu_q", C.c_void_p), ("seq_lens", C.c_void_p),
+        ("status", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64),
+    ]
+
+
 def _packer(block) -> struct.Struct:
     """The layout of an argument block, for filling one in a single call."""
     code = {C.c_int32: "i", C.c_int64: "q", C.c_float: "f", C.c_void_p: "P"}
@@ -119,6 +177,9 @@ def _packer(block) -> struct.Struct:
 
 QK_NORM_ROPE = _packer(QkNormRopeArgs)
 PAGED_ATTENTION = _packer(PagedAttentionArgs)
+ADD_RMS_NORM = _packer(AddRmsNormArgs)
+LATENT_ROWS = _packer(LatentRowsArgs)
+LATENT_ATTENTION = _packer(LatentAttentionArgs)
 
 
 class HisparseError(RuntimeError):
@@ -185,6 +246,11 @@ def load() -> C.CDLL:
         lib.hs_paged_attention_timeout_selftest.restype = C.c_int
         lib.hs_paged_attention_workspace_bytes.argtypes = [vp]
         lib.hs_paged_attention_workspace_bytes.restype = i64
+        for name in ("hs_add_rms_norm", "hs_latent_norm_rope_store", "hs_latent_attention"):
+            getattr(lib, name).argtypes = [vp, vp]
+            getattr(lib, name).restype = C.c_int
+        lib.hs_latent_attention_workspace_bytes.argtypes = [vp]
+        lib.hs_latent_attention_workspace_bytes.restype = i64
         lib.hs_err_string.argtypes = [i32]
         lib.hs_err_string.restype = C.c_char_p
         lib.hs_status_string.argtypes = [i32]

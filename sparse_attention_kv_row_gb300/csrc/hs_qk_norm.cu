@@ -18,14 +18,13 @@
 // of a copy's rate; 89 us with the kinds mixed in a warp, 136 in the first form.
 // norm_rope_general: any strides, alignment, head and rotation size; a warp per
 // head with the head staged in shared memory.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "hs_device.cuh"
 #include "hs_host.h"
+#include "hs_values.cuh"
 
 namespace hs {
 namespace {
@@ -62,77 +61,6 @@ struct NormParams {
   uint32_t rows;                             // heads (general) or units (rows) of this launch
 };
 
-template <int kDtype>
-struct Elem;
-template <>
-struct Elem<HS_DT_F32> {
-  static constexpr int kBytes = 4, kChunk = 4;
-  __device__ static float load(const unsigned char* p) { return *reinterpret_cast<const float*>(p); }
-  __device__ static void store(unsigned char* p, float x) { *reinterpret_cast<float*>(p) = x; }
-};
-template <>
-struct Elem<HS_DT_F16> {
-  static constexpr int kBytes = 2, kChunk = 8;
-  __device__ static float load(const unsigned char* p) {
-    return __half2float(*reinterpret_cast<const __half*>(p));
-  }
-  __device__ static void store(unsigned char* p, float x) {
-    *reinterpret_cast<__half*>(p) = __float2half_rn(x);
-  }
-};
-template <>
-struct Elem<HS_DT_BF16> {
-  static constexpr int kBytes = 2, kChunk = 8;
-  __device__ static float load(const unsigned char* p) {
-    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
-  }
-  __device__ static void store(unsigned char* p, float x) {
-    *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(x);
-  }
-};
-
-// Round to nearest even; finite overflow and infinities go to +-448, NaN stays.
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
-template <int kDtype>
-__device__ __forceinline__ void unpack(uint4 raw, float* x) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kDtype == HS_DT_F32) {
-      x[i] = __uint_as_float(w[i]);
-    } else if constexpr (kDtype == HS_DT_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    } else {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
-template <int kDtype>
-__device__ __forceinline__ uint4 pack(const float* x) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kDtype == HS_DT_F32) {
-      w[i] = __float_as_uint(x[i]);
-    } else if constexpr (kDtype == HS_DT_F16) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Which head a flattened row is: kind 0 = q, 1 = k, 2 = v.
 struct HeadAt {
   int64_t token;
@@ -161,32 +89,6 @@ __device__ __forceinline__ float inverse_norm(float sum_sq, const NormParams& p)
   return ms == 0.f ? 0.f : rsqrtf(ms);
 }
 
-// Pairs of fp32 values and the paired operations on them.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 template <int kDtype, int kN>
 __device__ __forceinline__ void unpack2(uint4 raw, uint64_t (&x)[kN]) {
   float f[2 * kN];

@@ -1,0 +1,50 @@
+"""latent_attention and paged_latent_attention against their statement in 64 bits."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from latent_cases import LatentInputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def hs(dev):
+    import sparse_attention_kv_row_gb300
+
+    return sparse_attention_kv_row_gb300
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    return torch.device("cuda:0")
+
+
+# ------------------------------------------------------------------ the general kernel
+@pytest.mark.parametrize("latent,rope,dtype,fmt", [
+    (512, 64, "f32", "same"), (128, 64, "bf16", "fp8"), (256, 64, "f16", "fp8"), (64, 32, "bf16", "same"),
+    (100, 0, "f32", "same"), (1, 1, "f16", "same"), (512, 256, "bf16", "same")])
+def test_general(hs, dev, latent, rope, dtype, fmt):
+    a = LatentInputs(heads=3, dtype=dtype, fmt=fmt, latent=latent, rope=rope)
+    a.indexed(5, 70, 200, empty=[2], bad=[1]).check(hs, dev, "general")
+    a = LatentInputs(heads=3, dtype=dtype, fmt=fmt, latent=latent, rope=rope)
+    a.paged([(40, 1), (0, 3), (None, 0), (17, 2), (0, 0)], 16, gap=2).check(hs, dev, "general")
+
+
+def test_general_unaligned(hs, dev):
+    """Rows and queries that allow no 16-byte accesses."""
+    a = LatentInputs(heads=2, dtype="bf16", fmt="fp8").indexed(4, 40, 100)
+    rows = torch.zeros(100, 660, dtype=torch.uint8, device=dev)[:, :656]
+    rows.copy_(a.rows)
+    a.check(hs, dev, "general", rows=rows)
+    a = LatentInputs(heads=2, dtype="f16", fmt="same").paged([(30, 2), (5, 1)], 8)
+    q = torch.zeros(a.T, 2, 577, dtype=torch.float16, device=dev)[..., 1:]
+    q.copy_(a.q)
+    a.check(hs, dev, "general", q=q)
