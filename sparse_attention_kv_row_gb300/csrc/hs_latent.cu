@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "hs_latent.cuh"
+#include "hs_latent_split.cuh"
 
 namespace hs {
 namespace {
@@ -196,9 +197,36 @@ LatentParams make_params(const hs_latent_attention_args* a) {
   p.max_q = indexed ? a->top_k : a->max_q_len;
   p.window = 0;
   p.n_tokens = a->n_tokens;
+  // Whole numbers of 32 bits count the batch's tiles: of 32 positions for every block
+  // of 16 query rows.
   p.max_len = 1ll << 30;
+  if (!indexed) {
+    const int64_t blocks = (static_cast<int64_t>(a->max_q_len) * a->num_heads + 15) / 16;
+    const int64_t units = (a->batch > 0 ? a->batch : 1) * (blocks > 0 ? blocks : 1);
+    const int64_t len = ((1ll << 31) - 1) / units * 32 - 32;
+    if (len < p.max_len) p.max_len = len;
+  }
   p.softmax_scale = a->scale;
   return p;
+}
+
+// Which kernels a call takes, by sizes and types only (the workspace depends on it).
+enum class LatentForm { kGeneral, kSplit };
+LatentForm latent_form(const hs_latent_attention_args* a) {
+  if (a->in_dtype == HS_DT_F32 || a->latent_dim != 512 || a->rope_dim != 64 || a->n_tokens == 0 ||
+      (!(a->flags & HS_LATENT_INDEX) && (a->max_q_len == 0 || a->batch == 0)))
+    return LatentForm::kGeneral;
+  return latent_split_fits(make_params(a)) ? LatentForm::kSplit : LatentForm::kGeneral;
+}
+
+// Whether every address that the tensor-core kernels form allows 16-byte accesses.
+bool latent_aligned(const LatentParams& p) {
+  const uintptr_t all =
+      reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.out) |
+      reinterpret_cast<uintptr_t>(p.rows) | static_cast<uintptr_t>(p.q_token) |
+      static_cast<uintptr_t>(p.q_head) | static_cast<uintptr_t>(p.out_token) |
+      static_cast<uintptr_t>(p.out_head) | static_cast<uintptr_t>(p.row_stride);
+  return all % 16 == 0;
 }
 
 }  // namespace
@@ -209,7 +237,10 @@ extern "C" int64_t hs_latent_attention_workspace_bytes(const hs_latent_attention
   clear_error();
   const hs_err err = check_args(a);
   if (err != HS_OK) return -static_cast<int64_t>(err);
-  return 0;
+  if (latent_form(a) == LatentForm::kGeneral) return 0;
+  DeviceInfo dev;
+  if (current_device(&dev) != HS_OK) return -static_cast<int64_t>(HS_ERR_CUDA);
+  return latent_split_workspace(a->in_dtype, a->row_format == HS_ROW_E4M3, dev);
 }
 
 extern "C" hs_err hs_latent_attention(const hs_latent_attention_args* a, hs_stream_t stream) {
@@ -230,11 +261,19 @@ extern "C" hs_err hs_latent_attention(const hs_latent_attention_args* a, hs_stre
   if ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out)) % esz != 0 ||
       (reinterpret_cast<uintptr_t>(a->rows) | static_cast<uintptr_t>(a->row_stride)) % (codes ? 4 : esz) != 0)
     return fail(HS_ERR_ARG, "%s: a pointer or row_stride is not a multiple of its element size", who);
+  const int64_t need = hs_latent_attention_workspace_bytes(a);
+  if (need < 0) return static_cast<hs_err>(-need);
+  if (need > 0 && (a->workspace == nullptr || a->workspace_bytes < need ||
+                   reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0))
+    return fail(HS_ERR_ARG, "%s: needs %lld bytes of 256-byte aligned workspace", who,
+                static_cast<long long>(need));
   DeviceInfo dev;
   err = current_device(&dev);
   if (err != HS_OK) return err;
   const LatentParams p = make_params(a);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (latent_form(a) == LatentForm::kSplit && latent_aligned(p))
+    return latent_split_launch(p, a->in_dtype, codes, a->workspace, dev, st);
   if (a->n_tokens > 0 && (indexed || a->max_q_len > 0)) {
     const GenFn fn =
         a->in_dtype == HS_DT_F32

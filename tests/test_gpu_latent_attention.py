@@ -48,3 +48,26 @@ def test_general_unaligned(hs, dev):
     q = torch.zeros(a.T, 2, 577, dtype=torch.float16, device=dev)[..., 1:]
     q.copy_(a.q)
     a.check(hs, dev, "general", q=q)
+
+
+# ------------------------------------------------------------------ the tensor-core kernels
+TYPES = [("bf16", "fp8"), ("f16", "fp8"), ("bf16", "same"), ("f16", "same")]
+
+
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+@pytest.mark.parametrize("heads", [1, 5, 16])
+@pytest.mark.parametrize("T,top_k", [(1, 1), (3, 31), (2, 33), (5, 300), (40, 64), (500, 20), (2, 2048)])
+def test_indexed(hs, dev, dtype, fmt, heads, T, top_k):
+    a = LatentInputs(heads=heads, dtype=dtype, fmt=fmt, seed=T)
+    a.indexed(T, top_k, 2 * top_k + 5, empty=[T // 2] if T > 2 else [], bad=[T - 1] if T > 1 else [])
+    a.check(hs, dev, "split")
+
+
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+@pytest.mark.parametrize("heads,page", [(16, 64), (3, 1), (8, 48), (16, 7)])
+@pytest.mark.parametrize("lens", [
+    [(0, 1)], [(31, 1), (32, 1), (63, 1)], [(700, 1), (None, 0), (3, 2), (0, 0), (40, 3)], [(0, 5), (129, 4)],
+    [(i * 7 % 50, 1 + i % 2) for i in range(40)]])
+def test_paged(hs, dev, dtype, fmt, heads, page, lens):
+    a = LatentInputs(heads=heads, dtype=dtype, fmt=fmt, seed=page)
+    a.paged(lens, page, gap=3).check(hs, dev, "split")
