@@ -814,11 +814,22 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  *  workspace   as in hs_paged_attention, hs_latent_attention_workspace_bytes of it
  * out and lse overlap no other buffer (not checked).  Rows of q that belong to no
  * request are left as they were in out and lse.
- * Scores, sums and outputs are accumulated in fp32.
+ * Scores, sums and outputs are accumulated in fp32.  16-bit calls with R = 512 and
+ * rope_dim = 64 run on the tensor cores, where the addresses and strides in bytes of
+ * q, out and rows are multiples of 16.  There the weights are rounded to the type of the
+ * values before their product with them (the sums that they are divided by are not).
+ * Over codes that type is fp16: a value becomes code * scale / 2^e, with 2^e the power of
+ * two not below the row's largest scale (within 2^-100 .. 2^125), half a step of fp16 off
+ * or 2^-25, and so counts in scores and outputs alike; a bf16 query's latent dims are
+ * taken as fp16 over a power of two of the query row, exact within 2^-22 of its largest
+ * value.  Other calls hold everything in fp32.
+ * A bounded wait inside a kernel that runs out (it cannot, short of a fault) ends the call
+ * and sets HS_ST_TIMEOUT in every status word; out and lse are then not to be used.
  * Limits: R <= 512, rope_dim <= 256, batch <= 2048, num_rows, n_tokens, top_k and
  * max_q_len * num_heads < 2^31, R a multiple of 128 for HS_ROW_E4M3, which wants
- * 16-bit types (else HS_ERR_UNSUPPORTED); sequence lengths as in hs_paged_attention
- * (2^30 at most, HS_ST_BAD_STATE beyond).
+ * 16-bit types (else HS_ERR_UNSUPPORTED).  Sequence lengths: up to 2^30, and as long as
+ * the tiles of 128 rows that all query heads and tokens might see, 64 query rows a unit,
+ * are fewer than 2^31 (HS_ST_BAD_STATE beyond).
  */
 #define HS_LATENT_INDEX 4 /* beside HS_SEQ_LENS_I64 and HS_REQ_STATE_I64 in flags */
 typedef struct hs_latent_attention_args {
@@ -845,6 +856,16 @@ typedef struct hs_latent_attention_args {
 int64_t hs_latent_attention_workspace_bytes(const hs_latent_attention_args* args);
 
 hs_err hs_latent_attention(const hs_latent_attention_args* args, hs_stream_t stream);
+
+/*
+ * hs_latent_attention_timeout_selftest -- hs_latent_attention with every bounded wait
+ * that is not over at once made to run out, as hs_paged_attention_timeout_selftest:
+ * every status word must report HS_ST_TIMEOUT beside its other bits, and the next call
+ * must be right.  Errors: those of hs_latent_attention, and HS_ERR_ARG for a call
+ * whose kernel has no such wait (not for the tensor cores).
+ */
+hs_err hs_latent_attention_timeout_selftest(const hs_latent_attention_args* args,
+                                            hs_stream_t stream);
 
 /*
  * hs_probe_read -- measurement utility, not part of the method: stream-read

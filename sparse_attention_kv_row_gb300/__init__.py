@@ -40,8 +40,8 @@ __all__ = ["swap_in", "swap_in_args", "make_swap_in_args", "gather_misses", "fp8
            "paged_attention", "paged_attention_workspace_bytes",
            "paged_attention_timeout_selftest", "add_rms_norm", "latent_norm_rope_store",
            "latent_attention", "latent_attention_workspace_bytes", "paged_latent_attention",
-           "paged_latent_attention_workspace_bytes", "swap_in_smem_bytes", "library_path",
-           "HisparseError", "SwapInArgs"]
+           "paged_latent_attention_workspace_bytes", "latent_attention_timeout_selftest",
+           "swap_in_smem_bytes", "library_path", "HisparseError", "SwapInArgs"]
 
 
 def library_path() -> str:
@@ -983,6 +983,25 @@ def _latent_workspace_bytes(dev, fields) -> int:
     return n
 
 
+@functools.lru_cache(maxsize=1024)
+def _latent_workspace(dev, latent, rope, dtype, kind, rows) -> int:
+    """Bytes of workspace for calls of ``rows`` query rows a token (or, by block tables, a request)
+    on this device: it depends on the kernel and on these up to 64, not on how much there is."""
+    stride = latent + rope
+    return _latent_workspace_bytes(dev, (
+        0, rows, latent, rope, dtype, kind, _capi.LATENT_INDEX, 1, 0, 1, 1.0, 0, 1, 0, rows * stride,
+        stride, 0, rows * latent, latent, 0, 0, 4 * stride, 1, 0, 1, 0, 0, 0, 0, 0, 0, 0))
+
+
+def _latent_need(dev, fields) -> int:
+    """Bytes of workspace for the call of these fields; nothing where it has nothing to compute.
+    (Sizes that the call refuses get their message from the call.)"""
+    heads, tokens = fields[1], 1 if fields[6] & _capi.LATENT_INDEX else fields[8]
+    if fields[12] == 0 or heads < 1 or tokens < 1:
+        return 0
+    return _latent_workspace(dev, *fields[2:6], min(heads * tokens, 64))
+
+
 def latent_attention_workspace_bytes(q, rows, row_index, out) -> int:
     """Bytes of workspace that ``latent_attention`` needs for tensors of these shapes and types."""
     return _latent_workspace_bytes(*_indexed_fields(q, rows, row_index, out, 1.0, None, None))
@@ -998,7 +1017,17 @@ def latent_attention(q, rows, row_index, out, *, scale, lse=None, status=None, w
     aligned, ``latent_attention_workspace_bytes`` of it) may be passed to keep one for a captured
     graph; otherwise one is allocated for the call."""
     dev, fields = _indexed_fields(q, rows, row_index, out, scale, lse, status)
-    _latent_attend(q, dev, fields, workspace, stream)
+    _latent_attend("hs_latent_attention", _lib().hs_latent_attention, q, dev, fields, workspace,
+                   stream)
+
+
+def latent_attention_timeout_selftest(q, rows, row_index, out, *, scale, status=None,
+                                      stream=None) -> None:
+    """hs_latent_attention with every bounded wait made to run out at once: every token must
+    report HS_ST_TIMEOUT, and later calls be right."""
+    dev, fields = _indexed_fields(q, rows, row_index, out, scale, None, status)
+    _latent_attend("hs_latent_attention_timeout_selftest",
+                   _lib().hs_latent_attention_timeout_selftest, q, dev, fields, None, stream)
 
 
 def paged_latent_attention_workspace_bytes(q, rows, block_table, req_state, cu_q, seq_lens, out, *,
@@ -1019,10 +1048,11 @@ def paged_latent_attention(q, rows, block_table, req_state, cu_q, seq_lens, out,
     as in ``latent_attention``; ``status`` is [batch]."""
     dev, fields = _paged_latent_fields(q, rows, block_table, req_state, cu_q, seq_lens, out,
                                        max_q_len, page_size, scale, lse, status)
-    _latent_attend(q, dev, fields, workspace, stream)
+    _latent_attend("hs_latent_attention", _lib().hs_latent_attention, q, dev, fields, workspace,
+                   stream)
 
 
-def _latent_attend(q, dev, fields, workspace, stream) -> None:
+def _latent_attend(where, fn, q, dev, fields, workspace, stream) -> None:
     raw = _raw_stream(stream, dev)
     space_p = n = 0
     if workspace is not None:
@@ -1030,9 +1060,8 @@ def _latent_attend(q, dev, fields, workspace, stream) -> None:
         space_p = _vector(workspace, torch.uint8, n, "workspace")
         _device_of(q, workspace)
     else:
-        n = _latent_workspace_bytes(dev, fields)
+        n = _latent_need(dev, fields)
         if n > 0:
             workspace = _call_space(n, q.device, stream, raw, dev)
             space_p = workspace.data_ptr()
-    _launch(dev, "hs_latent_attention", _lib().hs_latent_attention,
-            _capi.LATENT_ATTENTION.pack(*fields, space_p, n), raw)
+    _launch(dev, where, fn, _capi.LATENT_ATTENTION.pack(*fields, space_p, n), raw)

@@ -40,7 +40,8 @@ EXPORTS = ("hs_swap_in", "hs_swap_in_smem_bytes", "hs_store_kv", "hs_transfer_kv
            "hs_swap_in_layers", "hs_swap_in_layers_timeout_selftest", "hs_assign_slots",
            "hs_qk_norm_rope_store", "hs_paged_attention", "hs_paged_attention_workspace_bytes",
            "hs_paged_attention_timeout_selftest", "hs_add_rms_norm", "hs_latent_norm_rope_store",
-           "hs_latent_attention", "hs_latent_attention_workspace_bytes")
+           "hs_latent_attention", "hs_latent_attention_workspace_bytes",
+           "hs_latent_attention_timeout_selftest")
 
 
 class SwapInArgs(C.Structure):
@@ -246,7 +247,8 @@ def load() -> C.CDLL:
         lib.hs_paged_attention_timeout_selftest.restype = C.c_int
         lib.hs_paged_attention_workspace_bytes.argtypes = [vp]
         lib.hs_paged_attention_workspace_bytes.restype = i64
-        for name in ("hs_add_rms_norm", "hs_latent_norm_rope_store", "hs_latent_attention"):
+        for name in ("hs_add_rms_norm", "hs_latent_norm_rope_store", "hs_latent_attention",
+                     "hs_latent_attention_timeout_selftest"):
             getattr(lib, name).argtypes = [vp, vp]
             getattr(lib, name).restype = C.c_int
         lib.hs_latent_attention_workspace_bytes.argtypes = [vp]

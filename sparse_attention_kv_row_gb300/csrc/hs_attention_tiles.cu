@@ -52,7 +52,6 @@ constexpr int kLoaders = 128;
 constexpr uint32_t kSoftmaxRegs = 168, kLoaderRegs = 112, kMmaRegs = 64;
 static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 512, "65536 registers per SM");
 constexpr float kRaise = 8.f;      // log2 of how far weights may exceed 1
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 // A unit's fixed cost in tiles: its queries' way in and its outputs' way out
 // (about 4 us over a 16-bit cache and 6 over an FP8 one, to 1.6 and 1.8 a tile of
@@ -197,68 +196,6 @@ struct Shared {
   int64_t offs[2][kKeys];
 };
 
-// Waits for phase `parity`, unless the block has given up; gives up itself
-// after kWaitNs.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  uint64_t t0 = 0;
-  for (uint32_t n = 0;; ++n) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((n & 15) == 15) {
-      if (*dead) return false;
-      const uint64_t now = global_ns();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > kWaitNs) {
-        *dead = 1;
-        return false;
-      }
-    }
-  }
-}
-
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack2t(float lo, float hi) {
-  uint32_t r;
-  if constexpr (kBf16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Pairs of floats in 64-bit registers and the paired fp32 operations on them.
-__device__ __forceinline__ uint64_t two_words(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t two_floats(float lo, float hi) {
-  return two_words(__float_as_uint(lo), __float_as_uint(hi));
-}
-__device__ __forceinline__ float low_float(uint64_t x) {
-  return __uint_as_float(static_cast<uint32_t>(x));
-}
-__device__ __forceinline__ float high_float(uint64_t x) {
-  return __uint_as_float(static_cast<uint32_t>(x >> 32));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -277,23 +214,6 @@ struct RingAt {
   }
 };
 
-// 16-byte chunk c (of 64 elements' eight) of row r of a panel.
-__device__ __forceinline__ uint32_t in_panel(int r, int c) {
-  return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
-}
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // The same, and whether `ok` holds for every loader: they give up together.
 __device__ __forceinline__ bool loaders_all(bool ok) {

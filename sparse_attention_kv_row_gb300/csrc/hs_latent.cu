@@ -13,7 +13,6 @@
 #include <cstdint>
 
 #include "hs_latent.cuh"
-#include "hs_latent_split.cuh"
 
 namespace hs {
 namespace {
@@ -197,26 +196,18 @@ LatentParams make_params(const hs_latent_attention_args* a) {
   p.max_q = indexed ? a->top_k : a->max_q_len;
   p.window = 0;
   p.n_tokens = a->n_tokens;
-  // Whole numbers of 32 bits count the batch's tiles: of 32 positions for every block
-  // of 16 query rows.
+  // Whole numbers of 32 bits count the batch's tiles.
   p.max_len = 1ll << 30;
-  if (!indexed) {
-    const int64_t blocks = (static_cast<int64_t>(a->max_q_len) * a->num_heads + 15) / 16;
-    const int64_t units = (a->batch > 0 ? a->batch : 1) * (blocks > 0 ? blocks : 1);
-    const int64_t len = ((1ll << 31) - 1) / units * 32 - 32;
-    if (len < p.max_len) p.max_len = len;
-  }
+  if (!indexed && latent_tiles_max_len(p) < p.max_len) p.max_len = latent_tiles_max_len(p);
   p.softmax_scale = a->scale;
   return p;
 }
 
-// Which kernels a call takes, by sizes and types only (the workspace depends on it).
-enum class LatentForm { kGeneral, kSplit };
-LatentForm latent_form(const hs_latent_attention_args* a) {
-  if (a->in_dtype == HS_DT_F32 || a->latent_dim != 512 || a->rope_dim != 64 || a->n_tokens == 0 ||
-      (!(a->flags & HS_LATENT_INDEX) && (a->max_q_len == 0 || a->batch == 0)))
-    return LatentForm::kGeneral;
-  return latent_split_fits(make_params(a)) ? LatentForm::kSplit : LatentForm::kGeneral;
+// Whether a call is for the tensor-core kernel, by sizes and types only (the workspace
+// depends on it).
+bool latent_tiled(const LatentParams& p, const hs_latent_attention_args* a) {
+  return a->in_dtype != HS_DT_F32 && a->latent_dim == 512 && a->rope_dim == 64 && a->n_tokens > 0 &&
+         (p.indexed || (a->max_q_len > 0 && a->batch > 0)) && latent_tiles_fits(p);
 }
 
 // Whether every address that the tensor-core kernels form allows 16-byte accesses.
@@ -226,7 +217,7 @@ bool latent_aligned(const LatentParams& p) {
       reinterpret_cast<uintptr_t>(p.rows) | static_cast<uintptr_t>(p.q_token) |
       static_cast<uintptr_t>(p.q_head) | static_cast<uintptr_t>(p.out_token) |
       static_cast<uintptr_t>(p.out_head) | static_cast<uintptr_t>(p.row_stride);
-  return all % 16 == 0;
+  return all % 16 == 0 && p.num_rows > 0;
 }
 
 }  // namespace
@@ -237,15 +228,16 @@ extern "C" int64_t hs_latent_attention_workspace_bytes(const hs_latent_attention
   clear_error();
   const hs_err err = check_args(a);
   if (err != HS_OK) return -static_cast<int64_t>(err);
-  if (latent_form(a) == LatentForm::kGeneral) return 0;
+  const LatentParams p = make_params(a);
+  if (!latent_tiled(p, a)) return 0;
   DeviceInfo dev;
   if (current_device(&dev) != HS_OK) return -static_cast<int64_t>(HS_ERR_CUDA);
-  return latent_split_workspace(a->in_dtype, a->row_format == HS_ROW_E4M3, dev);
+  return latent_tiles_workspace(p, dev);
 }
 
-extern "C" hs_err hs_latent_attention(const hs_latent_attention_args* a, hs_stream_t stream) {
-  hs::CallRange range("hs_latent_attention");
-  using namespace hs;
+namespace hs {
+namespace {
+hs_err attend(const hs_latent_attention_args* a, bool give_up, hs_stream_t stream) {
   clear_error();
   hs_err err = check_args(a);
   if (err != HS_OK) return err;
@@ -272,8 +264,10 @@ extern "C" hs_err hs_latent_attention(const hs_latent_attention_args* a, hs_stre
   if (err != HS_OK) return err;
   const LatentParams p = make_params(a);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (latent_form(a) == LatentForm::kSplit && latent_aligned(p))
-    return latent_split_launch(p, a->in_dtype, codes, a->workspace, dev, st);
+  if (latent_tiled(p, a) && latent_aligned(p))
+    return latent_tiles_launch(p, a->in_dtype, codes, a->workspace, give_up, dev, st);
+  if (give_up)
+    return fail(HS_ERR_ARG, "hs_latent_attention_timeout_selftest: this call has no bounded waits");
   if (a->n_tokens > 0 && (indexed || a->max_q_len > 0)) {
     const GenFn fn =
         a->in_dtype == HS_DT_F32
@@ -291,4 +285,18 @@ extern "C" hs_err hs_latent_attention(const hs_latent_attention_args* a, hs_stre
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
   return HS_OK;
+}
+
+}  // namespace
+}  // namespace hs
+
+extern "C" hs_err hs_latent_attention(const hs_latent_attention_args* a, hs_stream_t stream) {
+  hs::CallRange range("hs_latent_attention");
+  return hs::attend(a, false, stream);
+}
+
+extern "C" hs_err hs_latent_attention_timeout_selftest(const hs_latent_attention_args* a,
+                                                       hs_stream_t stream) {
+  hs::CallRange range("hs_latent_attention_timeout_selftest");
+  return hs::attend(a, true, stream);
 }

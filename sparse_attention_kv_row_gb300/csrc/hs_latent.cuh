@@ -56,4 +56,11 @@ __device__ __forceinline__ void latent_write_status(const LatentParams& p, int b
   if (threadIdx.x == 0) p.status[b] = (bad ? HS_ST_BAD_INDEX : 0) | also;
 }
 
+// hs_latent_tiles.cu: 16-bit types with 512 + 64 dims, on the tensor cores.
+int64_t latent_tiles_workspace(const LatentParams& p, const DeviceInfo& dev);
+bool latent_tiles_fits(const LatentParams& p);
+int64_t latent_tiles_max_len(const LatentParams& p);
+hs_err latent_tiles_launch(const LatentParams& p, int in_dtype, bool codes, void* workspace, bool give_up,
+                           const DeviceInfo& dev, cudaStream_t stream);
+
 }  // namespace hs

@@ -1,0 +1,1053 @@
+// hs_latent_tiles.cu -- attention over latent rows on the fifth-generation tensor cores,
+// for sm_103a.
+//
+// A unit is up to N query rows (query heads of a token, or of a few tokens of a request)
+// against the latent rows they see, in tiles of 128 rows.  The products are transposed,
+// so that the long sides are the 128 rows and the 512 latent dims, and the query rows
+// are the short one that a unit has few or many of:
+//   S^T = K Q^T        (128 x N x 576),     P = 2^(S c - m),
+//   O_g^T += V_g^T P^T (128 x N x 128) for the four quarters g of the latent dims.
+// A tile lies in shared memory once, as 9 panels of 64 dims (128 bytes a row, swizzled):
+// read along the dims as keys, across the rows as values, so that every latent row is
+// read, and widened where it is codes, once for all N query rows.  S and O stay in
+// tensor memory (6 N columns).  The weights take the place of the rotary panel, which is
+// done with by then.
+//
+// Codes become fp16 times the row's scales, each divided by a power of two 2^e of the
+// row (at least its largest scale): half a step of fp16 of every value.  2^e goes to the
+// row's scores (a thread has one row, all query rows) and, over a running power of two
+// of the unit, to its weights.  The rotary dims have a product of their own then, in
+// their own type.  The running maximum is only raised, and O rescaled, when a score is
+// more than 2^8 above what it was; sums are in fp32, of unrounded weights.
+//
+// Roles: a warpgroup for the softmax and the outputs (a thread a row, then a thread a
+// dim; it also brings in the next unit's queries), a warp that issues the products, and
+// those that bring in rows: 16 warps that copy codes into a panel and turn them into fp16
+// in place, or three that issue tensor-map loads of 16-bit rows.  A quarter of a tile is
+// handed over as soon as it is there, and filled again as soon as its values are used;
+// the rows of the tile behind it are brought into L2 meanwhile.
+//
+// The flattened list of tiles of all units, each with some more for its fixed cost, is
+// cut into equal runs, one per SM.  A unit that a run covers alone is written at once;
+// the others leave their parts in the workspace, and a second kernel joins them.
+//
+// What bounds it: the chain of a tile (its rows come in, four times the keys' product with
+// what has come, softmax, four times the values' product, and only then room for the next
+// rows), behind a start of some 8 us.  One unit an SM over codes takes, for 1, 2, 4, 8 and
+// 16 tiles, 12.6, 16.8, 25.2, 45.9 and 84.5 us with 16 query rows and 26, 34, 48, 84 and
+// 147 us with 64: 4.8 and 7.9 us a tile, 2.4 TB/s of rows and 0.29 PFLOP/s at 16 tiles.
+// Measured against it, at 16 tiles: 16 query rows by 32 latent rows on mma.sync, eight warps
+// on their own (94 us, and 330 for 64 query rows, which it does 16 at a time); codes landing
+// in a buffer of their own ahead of their panels (83 to 92 us and 150 to 197: the room is
+// three quarters of a tile's codes at most, and the copies' and the conversion's accesses to
+// shared memory then meet); rows of codes by bulk copies (one row an instruction, 90 to 145
+// clocks each in its warp).
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cstddef>
+#include <mutex>
+
+#include "hs_latent.cuh"
+#include "hs_tcgen05.cuh"
+
+namespace hs {
+namespace {
+
+constexpr int kKeys = 128;                // rows of a tile
+constexpr int kPanel = kKeys * 128;       // bytes: 64 dims
+constexpr int kLatent = 512, kRope = 64;
+constexpr int kQuarters = 4;              // of the latent dims, two panels each
+constexpr int kRopePanel = 8;
+constexpr int kTileBytes = 9 * kPanel;
+constexpr int kChunkRows = 16, kChunks = kKeys / kChunkRows;  // 16-bit rows that may come in together
+constexpr int kRowWarps = 3;                      // that bring in 16-bit rows
+// Warps: 4 of softmax, over codes 16 that bring in and convert, the one of the products,
+// those of 16-bit rows (over codes, as many without work).
+constexpr int product_warp(bool codes) { return codes ? 20 : 4; }
+constexpr int block_threads(bool codes) { return (product_warp(codes) + 4) * kWarp; }
+// Registers over codes: of the launch, and of the warpgroups after they have shared them
+// out (softmax, four that convert, one of the products).
+constexpr uint32_t kLaunchRegs = 80;
+constexpr uint32_t softmax_regs(int n) { return n == 64 ? 184 : 128; }
+constexpr uint32_t convert_regs(int n) { return n == 64 ? 64 : 72; }
+constexpr uint32_t product_regs(int n) { return n == 64 ? 40 : 64; }
+static_assert(softmax_regs(64) + 4 * convert_regs(64) + product_regs(64) <= 6 * kLaunchRegs &&
+                  softmax_regs(32) + 4 * convert_regs(32) + product_regs(32) <= 6 * kLaunchRegs,
+              "what the block was launched with");
+constexpr float kNoScale = 0x1p-100f;      // 2^e of a row of zeros
+constexpr float kRaise = 8.f;             // log2 of how far weights may exceed their reference
+constexpr int kUnitCost = 2;              // a unit's fixed cost in tiles
+
+struct LatentTilesParams : LatentParams {
+  int tokens;      // of a unit, at most
+  int chunks;      // of the query heads: units of a token group
+  int give_up;     // (self-test) every wait that is not over at once runs out
+};
+
+struct TilesSpace {
+  int4* joins;       // [workers]: the split unit that a worker's boundary is the first to cut
+  int32_t* failed;   // [workers]: a bounded wait gave up
+  float* slots;      // two per worker: o [N][512], then log2-sum-exp [N]
+  uint32_t workers;
+};
+constexpr int slot_floats(int n) { return n * (kLatent + 1); }
+constexpr int64_t kTilesHead = 64 * 1024;  // joins and failure words, up to 2048 workers
+
+// A unit: `tokens` tokens from the i0-th on of a batch row, `heads` query heads from
+// head0 on; the latent rows [0, end), in tiles.
+struct Unit {
+  int i0, tokens, head0, heads, end, tiles;
+};
+__device__ __forceinline__ int row_units(const LatentTilesParams& p, const AttnRow& r) {
+  return (r.n + p.tokens - 1) / p.tokens * p.chunks;
+}
+template <int N>
+__device__ __forceinline__ Unit unit_at(const LatentTilesParams& p, const AttnRow& r, int x) {
+  Unit u;
+  const int group = x / p.chunks;
+  u.i0 = group * p.tokens;
+  u.tokens = min(p.tokens, r.n - u.i0);
+  u.head0 = (x - group * p.chunks) * N;
+  u.heads = min(N, p.heads - u.head0);
+  u.end = latent_end(p, r, u.i0 + u.tokens - 1);
+  u.tiles = max(1, (u.end + kKeys - 1) / kKeys);
+  return u;
+}
+template <int N>
+__device__ __forceinline__ uint32_t row_cost(const LatentTilesParams& p, const AttnRow& r) {
+  if (p.indexed) return static_cast<uint32_t>(p.chunks) * (unit_at<N>(p, r, 0).tiles + kUnitCost);
+  uint32_t n = 0;
+  for (int x = 0; x < row_units(p, r); x += p.chunks) n += unit_at<N>(p, r, x).tiles + kUnitCost;
+  return n * p.chunks;
+}
+
+// Walks the units of a worker's run; all roles walk the same way.
+template <int N>
+struct Walk {
+  uint32_t c1;    // end of the run
+  uint32_t u0;    // cost index of the current unit
+  int b, x;
+  AttnRow row;
+  Unit unit;
+  int k0, k1;     // this run's tiles of the unit
+
+  __device__ __forceinline__ void clip(uint32_t c0) {
+    const int64_t a = static_cast<int64_t>(c0) - u0 - kUnitCost, e = static_cast<int64_t>(c1) - u0 - kUnitCost;
+    k0 = a > 0 ? static_cast<int>(a) : 0;
+    k1 = e < unit.tiles ? static_cast<int>(e) : unit.tiles;
+  }
+  __device__ __forceinline__ bool seek(uint32_t c0, uint32_t end, const uint32_t* prefix,
+                                       const LatentTilesParams& p) {
+    c1 = end;
+    if (c0 >= c1) return false;
+    x = 0;
+    if (p.indexed) {
+      row = latent_row(p, 0);
+      const uint32_t per = row_cost<N>(p, row);
+      b = c0 / per;
+      u0 = b * per;
+    } else {
+      int a = 0, n = p.batch;  // the largest b with prefix[b] <= c0
+      while (n - a > 1) {
+        const int mid = (a + n) >> 1;
+        if (prefix[mid] <= c0)
+          a = mid;
+        else
+          n = mid;
+      }
+      b = a;
+      u0 = prefix[b];
+    }
+    row = latent_row(p, b);
+    unit = unit_at<N>(p, row, 0);
+    while (c0 - u0 >= static_cast<uint32_t>(unit.tiles + kUnitCost)) {
+      u0 += unit.tiles + kUnitCost;
+      unit = unit_at<N>(p, row, ++x);
+    }
+    clip(c0);
+    return k1 > k0 || next(prefix, p);
+  }
+  // The next unit with tiles in the run.
+  __device__ __forceinline__ bool next(const uint32_t* prefix, const LatentTilesParams& p) {
+    u0 += unit.tiles + kUnitCost;
+    if (u0 + kUnitCost >= c1) return false;
+    if (++x == row_units(p, row)) {
+      x = 0;
+      ++b;
+      if (!p.indexed)
+        while (prefix[b + 1] == prefix[b]) ++b;
+      row = latent_row(p, b);
+    }
+    unit = unit_at<N>(p, row, x);
+    clip(u0);
+    return true;
+  }
+};
+
+template <int N>
+struct alignas(16) Shared {
+  // read four at a time
+  alignas(16) float undo[2][N];  // what undoes the factors of the queries
+  alignas(16) float ref[N];      // what scores are taken relative to, negated
+  float factor[N];               // what rescales O; then what outputs are multiplied by
+  float most[4][N];              // per warp: largest scores, then sums
+  float row_scale[kKeys];        // 2^e, or -1 for a row that nobody sees
+  int64_t to[N];                 // a query row's output's byte, -1: none
+  uint64_t q_full, full[5], empty[5], s_full, p_full, o_done, drain;
+  uint32_t scale_most[4];
+  int vis[N];                    // rows [0, vis) that a query row sees; 0: no query row
+  bool started[N];               // a query row has met a row that it sees
+  uint32_t tmem;
+  volatile int dead;
+};
+static_assert(offsetof(Shared<16>, ref) % 16 == 0 && offsetof(Shared<32>, undo[1]) % 16 == 0 &&
+                  offsetof(Shared<64>, to) % 8 == 0, "alignment of vector reads");
+
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool group_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+// Pairs of fp16: c times a factor that is given as fp16 and what its rounding left; the
+// rounding of the small product is 2^-11 of that.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t c, uint32_t hi, uint32_t lo) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tmul.rn.f16x2 t, %1, %3;\n\tfma.rn.f16x2 %0, %1, %2, t;\n\t}"
+      : "=r"(r)
+      : "r"(c), "r"(hi), "r"(lo));
+  return r;
+}
+// Floats as whole numbers of the same order (NaN aside), and back.
+__device__ __forceinline__ int ordered(float x) {
+  const int b = __float_as_int(x);
+  return b ^ (b >> 31 & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b ^ (b >> 31 & 0x7FFFFFFF)); }
+
+// N columns of a warp's 32 lanes of tensor memory.
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t (&r)[N], uint32_t addr) {
+  if constexpr (N == 16) {
+    tmem_ld16(r, addr);
+  } else {
+    static_assert(N == 32, "16 or 32 columns");
+    tmem_ld32(r, addr);
+  }
+}
+
+template <int kIn, bool kCodes, int N>
+__global__ void __launch_bounds__(block_threads(kCodes), 1)
+    latent_tiles_kernel(const LatentTilesParams p, const TilesSpace ws,
+                        const __grid_constant__ CUtensorMap row_map,
+                        const __grid_constant__ CUtensorMap box_map) {
+  constexpr bool kBf16 = kIn == HS_DT_BF16 && !kCodes;  // type of the latent products
+  constexpr bool kRopeBf16 = kIn == HS_DT_BF16;
+  constexpr bool kHalve = kIn == HS_DT_BF16 && kCodes;  // the queries' latent dims become fp16
+  constexpr int kQPanel = N * 128;
+  // Keys that codes stand for go to tensor memory where there is room: the first product
+  // then takes 12 clocks for 16 query rows and 18 for 32, 42 and 43 with keys in shared
+  // memory, which is read and written by everything else.
+  constexpr bool kKeysApart = kCodes && N <= 32;
+  // Columns of tensor memory: the scores (the rotary dims' behind them), the outputs, and
+  // those keys.
+  constexpr int kO = 2 * N, kK = 6 * N;
+  constexpr uint32_t kCols = kKeysApart || N == 64 ? 512 : (N == 16 ? 128 : 256);
+  static_assert(kK + (kKeysApart ? kLatent / 2 : 0) <= kCols, "tensor memory");
+  // fp16 weights reach 2^(6 + 8) and keep what is 2^-30 of the reference.
+  constexpr float kBias = kBf16 ? 0.f : 6.f;
+  constexpr int kStep = N < 32 ? N : 32;  // columns read at once
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + kTileBytes + 9 * kQPanel);
+  __shared__ Shared<N> sh;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
+  const uint32_t tile = smem_addr(smem), q_at = tile + kTileBytes;
+
+  if (tid == 0) {
+    mbar_init(&sh.q_full, 4);
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(&sh.full[i], kCodes ? (i < kQuarters ? 4 : 16) : kRowWarps);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.s_full, 1);
+    mbar_init(&sh.p_full, kKeys);
+    mbar_init(&sh.o_done, 1);
+    mbar_init(&sh.drain, 1);
+    fence_mbar_init();
+    sh.dead = p.give_up;
+  }
+  constexpr int kProduct = product_warp(kCodes);
+  if (warp == kProduct) tmem_alloc(&sh.tmem, kCols);
+  uint32_t total;
+  if (p.indexed)
+    total = static_cast<uint32_t>(p.batch) * row_cost<N>(p, latent_row(p, 0));
+  else
+    total = attn_prefix(p, prefix, [&](const AttnRow& r) { return row_cost<N>(p, r); });
+  grid_dep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(kFullMask, sh.tmem, 0);
+  const uint32_t workers = min(ws.workers, total), me = blockIdx.x;
+  const uint32_t c0 = me < workers ? split_begin(me, total, workers) : 0;
+  const uint32_t c1 = me < workers ? split_begin(me + 1, total, workers) : 0;
+  volatile int* dead = &sh.dead;
+  Walk<N> w;
+
+  if (warp < 4) {
+    // ---------------------------------------------------------------- softmax, outputs
+    if constexpr (kCodes) regs_grow<softmax_regs(N)>();
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const float s2 = p.softmax_scale * kLog2e;
+    uint32_t n = 0, u_n = 0;  // tiles and units so far
+    bool ok = true, more = w.seek(c0, c1, prefix, p);
+    // The queries of a unit, zeros past the last, a row a warp at a time: on their way,
+    // and then ready.
+    auto send_queries = [&](const Walk<N>& nx) {
+#pragma unroll 1
+      for (int m = warp; m < N; m += 4) {
+        const int in = m / nx.unit.heads, h = m - in * nx.unit.heads;
+        const bool live = in < nx.unit.tokens;
+        const unsigned char* src = p.q + (static_cast<int64_t>(nx.row.q0) + (live ? nx.unit.i0 + in : 0)) * p.q_token +
+                                   static_cast<int64_t>(live ? nx.unit.head0 + h : 0) * p.q_head;
+#pragma unroll
+        for (int c = lane; c < (kLatent + kRope) / 8; c += kWarp)
+          cp_async_16_zfill(q_at + (c / 8) * kQPanel + in_panel(m, c % 8), src + c * 16, live);
+      }
+      cp_async_commit();
+    };
+    auto finish_queries = [&](uint32_t u_at) {
+      cp_async_wait_group<0>();
+      if constexpr (kHalve) {
+        // In place, a chunk in the lane that brought it: latent dims to fp16, times a
+        // power of two of the row.
+#pragma unroll 2
+        for (int m = warp; m < N; m += 4) {
+          uint32_t at[2], top = 0;
+          uint4 v[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = i * kWarp + lane;
+            at[i] = q_at + (c / 8) * kQPanel + in_panel(m, c % 8);
+            v[i] = ld_shared_v4(at[i]);
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+          }
+          top = __reduce_max_sync(kFullMask, top);
+          const float up = f16_factor(top);
+          if (lane == 0) sh.undo[u_at & 1][m] = 1.0f / up;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = pack2<false>(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
+            st_shared_v4(at[i], make_uint4(x[0], x[1], x[2], x[3]));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+    };
+    if (more) {
+      send_queries(w);
+      finish_queries(0);
+    }
+    for (; more && ok; ++u_n) {
+      const bool whole = w.k0 == 0 && w.k1 == w.unit.tiles;
+      if (tid < N) {
+        // Query row tid of the unit.
+        const int in = tid / w.unit.heads, h = tid - in * w.unit.heads;
+        const bool live = in < w.unit.tokens;
+        sh.vis[tid] = live ? latent_end(p, w.row, w.unit.i0 + in) : 0;
+        sh.to[tid] = live ? (static_cast<int64_t>(w.row.q0) + w.unit.i0 + in) * p.out_token +
+                                static_cast<int64_t>(w.unit.head0 + h) * p.out_head
+                          : -1;
+        sh.ref[tid] = kBias;
+        sh.started[tid] = sh.vis[tid] == 0;
+      }
+      const int all_end = latent_end(p, w.row, w.unit.i0);  // rows that every query row sees
+      float l[N];
+#pragma unroll
+      for (int h = 0; h < N; ++h) l[h] = 0.f;
+      float norm = 0.f;   // a power of two that no row's 2^e so far exceeds
+      bool fresh = true;  // some query row has not met a row that it sees
+      group_sync();
+      for (int k = w.k0; k < w.k1; ++k, ++n) {
+        ok = __all_sync(kFullMask, wait_for(&sh.s_full, n & 1, dead));
+        if (group_any(!ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float mine = sh.row_scale[tid];
+        const float c = kCodes ? s2 * mine : s2;
+        const int j = k * kKeys + tid;
+        // Scores over their reference points, two query rows at a time.
+        uint64_t z2[N / 2];
+        const uint64_t c2 = two_floats(c, c), s22 = two_floats(s2, s2);
+#pragma unroll
+        for (int q = 0; q < N; q += kStep) {
+          uint32_t a[kStep];
+          tmem_ld_n(a, tmem + lanes + q);
+          uint32_t r[kCodes ? kStep : 16];
+          if constexpr (kCodes) tmem_ld_n(r, tmem + lanes + N + q);
+          tmem_wait_ld();
+          tmem_pin(a);
+          if constexpr (kCodes) tmem_pin(r);
+#pragma unroll
+          for (int i = 0; i < kStep; i += 4) {
+            const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(&sh.ref[q + i]);  // (negated)
+            ulonglong2 un = make_ulonglong2(0, 0);
+            if constexpr (kHalve) un = *reinterpret_cast<const ulonglong2*>(&sh.undo[u_n & 1][q + i]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint64_t s = two_words(a[i + 2 * x], a[i + 2 * x + 1]);
+              uint64_t add = x ? ref.y : ref.x;
+              if constexpr (kHalve) s = mul2(s, x ? un.y : un.x);
+              if constexpr (kCodes) add = fma2(two_words(r[i + 2 * x], r[i + 2 * x + 1]), s22, add);
+              z2[(q + i) / 2 + x] = fma2(s, c2, add);
+            }
+          }
+        }
+        float z[N];
+#pragma unroll
+        for (int h = 0; h < N; h += 2) {
+          z[h] = low_float(z2[h / 2]);
+          z[h + 1] = high_float(z2[h / 2]);
+        }
+        if (k * kKeys + kKeys > all_end || __any_sync(kFullMask, mine < 0.f)) {
+#pragma unroll
+          for (int h = 0; h < N; ++h)
+            if (mine < 0.f || j >= sh.vis[h]) z[h] = -INFINITY;
+        }
+        float top = z[0];
+#pragma unroll
+        for (int h = 1; h + 1 < N; h += 2) top = fmaxf(top, fmaxf(z[h], z[h + 1]));
+        top = fmaxf(top, z[N - 1]);
+        bool over = top > kRaise + kBias;
+        if (kCodes) over |= mine > norm;
+        if (group_any(over) || fresh) {
+          // ---- new reference points: where they are exceeded, and where there are none yet
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            const int most = __reduce_max_sync(kFullMask, ordered(z[h]));
+            if (lane == (h & 31)) sh.most[warp][h] = from_ordered(most);
+          }
+          const uint32_t sm = __reduce_max_sync(kFullMask, mine > 0.f ? __float_as_uint(mine) : 0u);
+          if (lane == 0) sh.scale_most[warp] = sm;
+          group_sync();
+          float back = 1.f;
+          if constexpr (kCodes) {
+            const float to = __uint_as_float(max(max(max(sh.scale_most[0], sh.scale_most[1]),
+                                                     max(sh.scale_most[2], sh.scale_most[3])), 0x0D800000u));
+            if (to > norm) {
+              back = norm / to;
+              norm = to;
+            }
+          }
+          bool waits = false;
+          if (tid < N) {
+            const float most = fmaxf(fmaxf(sh.most[0][tid], sh.most[1][tid]), fmaxf(sh.most[2][tid], sh.most[3][tid]));
+            float up = 0.f, f = 1.f;
+            if (most > kRaise + kBias || (!sh.started[tid] && most > -INFINITY)) {
+              up = most - kBias;
+              f = sh.started[tid] ? fast_exp2(-up) : 0.f;
+              sh.started[tid] = true;
+            }
+            sh.most[0][tid] = up;
+            sh.factor[tid] = f;
+            waits = !sh.started[tid];
+          }
+          fresh = group_any(waits);
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            z[h] -= sh.most[0][h];
+            l[h] *= sh.factor[h];
+          }
+          if (k > w.k0) {
+            // O is whole once the last tile's products are.
+            ok = __all_sync(kFullMask, wait_for(&sh.o_done, (n - 1) & 1, dead));
+            if (group_any(!ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 4 * N; q += 16) {
+              uint32_t o[16];
+              tmem_ld16(o, tmem + lanes + kO + q);
+              tmem_wait_ld();
+              tmem_pin(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * (sh.factor[(q + i) % N] * back));
+              tmem_st16(tmem + lanes + kO + q, o);
+            }
+            tmem_wait_st();
+          }
+          group_sync();
+          if (tid < N) sh.ref[tid] -= sh.most[0][tid];
+          group_sync();
+        }
+        // ---- weights, into the rotary panel: a row of up to 64 query rows
+        const float kn = kCodes ? (mine > 0.f ? mine * (1.0f / norm) : 0.f) : 1.f;
+        const uint32_t to = tile + kRopePanel * kPanel;
+#pragma unroll
+        for (int q = 0; q < N; q += 8) {
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e0 = fast_exp2(z[q + 2 * i]), e1 = fast_exp2(z[q + 2 * i + 1]);
+            l[q + 2 * i] += e0;
+            l[q + 2 * i + 1] += e1;
+            // The weights take the type of the values, as one product wants of its
+            // operands: half a step off each, whose errors average out over the rows.
+            v[i] = kCodes ? pack2<false>(e0 * kn, e1 * kn) : pack2<kBf16>(e0, e1);
+          }
+          st_shared_v4(to + in_panel(tid, q / 8), make_uint4(v[0], v[1], v[2], v[3]));
+        }
+        fence_proxy_async_smem();  // the MMA reads through the async proxy
+        tc_fence_before();
+        mbar_arrive(&sh.p_full);
+      }
+      if (!ok) break;
+      // ---- the next unit's queries, whose place the last tile's scores have left free
+      const Unit unit = w.unit;
+      const int32_t q0 = w.row.q0;
+      const bool from_start = w.k0 == 0;
+      more = w.next(prefix, p);
+      if (more) send_queries(w);
+      // ---- sums over the rows, 32 lanes and 4 warps
+#pragma unroll
+      for (int h = 0; h < N; ++h) {
+#pragma unroll
+        for (int d = kWarp / 2; d > 0; d >>= 1) l[h] += __shfl_xor_sync(kFullMask, l[h], d);
+        if (lane == (h & 31)) sh.most[warp][h] = l[h];
+      }
+      group_sync();
+      float* part = ws.slots + static_cast<int64_t>(2 * me + (from_start ? 1 : 0)) * slot_floats(N);
+      if (tid < N) {
+        const float sum = (sh.most[0][tid] + sh.most[1][tid]) + (sh.most[2][tid] + sh.most[3][tid]);
+        // A sum of 0 is that of a token without rows: zeros, and -inf.
+        sh.factor[tid] = sum == 0.f ? 0.f : (kCodes ? norm : 1.f) / sum;
+        const float lse = log2f(sum) - sh.ref[tid];
+        if (!whole) {
+          part[N * kLatent + tid] = lse;
+        } else if (sh.to[tid] >= 0 && p.lse != nullptr) {
+          const int in = tid / unit.heads;
+          p.lse[(static_cast<int64_t>(q0) + unit.i0 + in) * p.heads + unit.head0 + tid - in * unit.heads] = lse * kLn2;
+        }
+      }
+      if (more) finish_queries(u_n + 1);
+      ok = __all_sync(kFullMask, wait_for(&sh.o_done, (n - 1) & 1, dead));
+      if (group_any(!ok)) break;
+      tc_fence_after();
+      // A thread has a latent dim of each quarter; 16 query rows at a time.
+#pragma unroll 1
+      for (int q = 0; q < N; q += 16) {
+        uint32_t o[kQuarters][16];
+#pragma unroll
+        for (int g = 0; g < kQuarters; ++g) tmem_ld16(o[g], tmem + lanes + kO + g * N + q);
+        tmem_wait_ld();
+#pragma unroll
+        for (int g = 0; g < kQuarters; ++g) tmem_pin(o[g]);
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int64_t to = sh.to[q + i];
+            const float f = sh.factor[q + i];
+            if (to >= 0) {
+              unsigned char* const out = p.out + to + tid * 2;
+#pragma unroll
+              for (int g = 0; g < kQuarters; ++g) attn_store<kIn>(out + g * 256, __uint_as_float(o[g][i]) * f);
+            }
+          }
+        } else {
+          float* const mine = part + q * kLatent + tid;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float f = sh.factor[q + i];
+#pragma unroll
+            for (int g = 0; g < kQuarters; ++g) mine[i * kLatent + g * 128] = __uint_as_float(o[g][i]) * f;
+          }
+        }
+      }
+      tc_fence_before();  // O is read before the next unit's first product, which waits for P
+      group_sync();
+    }
+  } else if (warp < kProduct) {
+    // ---------------------------------------------------------------- codes to fp16
+    if constexpr (kCodes) {
+      regs_shrink<convert_regs(N)>();
+      // A warp has 32 rows of every tile, a row a lane, and a quarter of their dims.
+      constexpr int kRowBytes = kLatent + 16 + 2 * kRope;
+      const int rows = (warp & 3) * kWarp, g = (warp - 4) >> 2, key = rows + lane;
+      const uint32_t panel = tile + 2 * g * kPanel, pe = tile + kRopePanel * kPanel;
+      auto wait_all = [&](uint64_t* bar, uint32_t phase) {
+        return __all_sync(kFullMask, wait_for(bar, phase, dead));
+      };
+      bool more = w.seek(c0, c1, prefix, p);
+      int k = w.k0;
+      // The lane's row of tile k, found a tile ahead; this warp's part of it into L2.
+      auto find = [&]() {
+        const int j = k * kKeys + key;
+        const int32_t r = more && j < w.unit.end ? latent_key(p, w.row, j) : kNoRow;
+        if (r >= 0) {
+          const unsigned char* at = p.rows + r * p.row_stride;
+          prefetch_l2(at + g * 128);
+          prefetch_l2(at + g * 128 + 112);
+          if (g == 3) prefetch_l2(at + kRowBytes - 16);
+        }
+        return r;
+      };
+      int32_t row = find();
+      for (uint32_t n = 0; more; ++n) {
+        // ---- codes into the second panel of the quarter, 128 bytes a row, as soon as
+        // the last tile's values are used
+        if (!wait_all(&sh.empty[g], (n & 1) ^ 1)) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          const int32_t at = __shfl_sync(kFullMask, row, r);
+          cp_async_16_zfill(panel + kPanel + in_panel(rows + r, lane & 7),
+                            p.rows + max(at, 0) * p.row_stride + g * 128 + (lane & 7) * 16, at >= 0);
+        }
+        cp_async_commit();
+        // The row's 2^e, the power of two not below its largest scale, within what has a
+        // reciprocal; and this quarter's scale over it.
+        float e = kNoScale, sc = 0.f;
+        if (row >= 0) {
+          const uint4 x = ld_stream_v4(p.rows + row * p.row_stride + kLatent);
+          const uint32_t most = max(max(x.x & 0x7FFFFFFFu, x.y & 0x7FFFFFFFu), max(x.z & 0x7FFFFFFFu, x.w & 0x7FFFFFFFu));
+          e = __uint_as_float(min(max((most + 0x007FFFFFu) & 0x7F800000u, 0x0D800000u), 0x7E000000u));
+          sc = __uint_as_float(g < 2 ? (g == 0 ? x.x : x.y) : (g == 2 ? x.z : x.w)) * (1.0f / e);
+        }
+        const uint32_t f = pack2<false>(sc, sc);
+        const float left = sc <= 1.f ? sc - __half2float(__ushort_as_half(f & 0xFFFFu)) : 0.f;  // (inf stays)
+        const uint32_t f_lo = pack2<false>(left, left);
+        cp_async_wait_group<0>();
+        __syncwarp();
+        // ---- in place: a lane reads its row's codes, and writes their fp16 over them
+        // and into the first panel
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint4 c[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[i] = ld_shared_v4(panel + kPanel + in_panel(key, half * 4 + i));
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x[4] = {c[part * 2 + i].x, c[part * 2 + i].y, c[part * 2 + i].z, c[part * 2 + i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y[i * 8 + 2 * j] = scaled_pair(e4m3_to_f16(x[j]), f, f_lo);
+                y[i * 8 + 2 * j + 1] = scaled_pair(e4m3_to_f16(x[j] >> 16), f, f_lo);
+              }
+            }
+            if constexpr (kKeysApart)
+              tmem_st16(tmem + (static_cast<uint32_t>(rows) << 16) + kK + g * 64 + half * 32 + part * 16, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              st_shared_v4(panel + half * kPanel + in_panel(key, part * 4 + i),
+                           make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
+          }
+        }
+        if constexpr (kKeysApart) {
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[g]);
+        // ---- 16 of the rotary dims
+        if (!wait_all(&sh.empty[4], (n & 1) ^ 1)) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = i * 16 + (lane >> 1);
+          const int32_t at = __shfl_sync(kFullMask, row, r);
+          cp_async_16_zfill(pe + in_panel(rows + r, 2 * g + (lane & 1)),
+                            p.rows + max(at, 0) * p.row_stride + kLatent + 16 + g * 32 + (lane & 1) * 16, at >= 0);
+        }
+        if (g == 0) sh.row_scale[key] = row == kNoRow ? -1.f : e;
+        cp_async_commit_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[4]);
+        if (++k == w.k1) {
+          more = w.next(prefix, p);
+          k = w.k0;
+        }
+        row = find();
+      }
+      cp_async_wait_all();
+    }
+  } else {
+    // ---------------------------------------------------------------- products
+    if constexpr (kCodes) regs_shrink<product_regs(N)>();
+    if (warp == kProduct) {
+      // The whole warp walks along, so that addresses and descriptors stay in uniform
+      // registers; one elected lane issues.
+      constexpr uint32_t kQk = mma_shape(kBf16, kKeys, N, false), kQr = mma_shape(kRopeBf16, kKeys, N, false);
+      constexpr uint32_t kPv = mma_shape(kBf16, kKeys, N, true, true);
+      constexpr uint32_t kHi = mma_desc_hi(1024);
+      auto reached = [&](uint64_t* bar, uint32_t phase) {
+        const bool got = __all_sync(kFullMask, wait_for(bar, phase, dead));
+        tc_fence_after();
+        return got;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
+      };
+      uint32_t n = 0, u_n = 0;
+      bool ok = true;
+      bool more = w.seek(c0, c1, prefix, p);
+      if (lane == 0) {
+        // Where this run's start cuts a unit, and is the first to do so, the unit's parts
+        // are joined in this worker's name.
+        int4 j = make_int4(-1, 0, 0, 0);
+        if (more && w.k0 > 0 && split_worker(w.u0 + kUnitCost, total, workers) + 1 == me)
+          j = make_int4(w.b, w.x, static_cast<int>(split_worker(w.u0 + kUnitCost + w.unit.tiles - 1, total, workers)), 0);
+        ws.joins[me] = j;
+      }
+      for (; more && ok; more = w.next(prefix, p), ++u_n) {
+        if (!(ok = reached(&sh.q_full, u_n & 1))) break;
+        for (int k = w.k0; k < w.k1; ++k, ++n) {
+#pragma unroll 1
+          for (int g = 0; g < kQuarters; ++g) {
+            if (!(ok = reached(&sh.full[g], n & 1))) break;
+            const uint32_t a = mma_desc_lo(tile + 2 * g * kPanel, 16), b = mma_desc_lo(q_at + 2 * g * kQPanel, 16);
+            if (elect_one()) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const uint32_t bx = b + (((x / 4) * kQPanel + (x % 4) * 32) >> 4);
+                if constexpr (kKeysApart)
+                  mma_tmem<kHi>(tmem, tmem + kK + g * 64 + x * 8, bx, kQk, g > 0 || x > 0);
+                else
+                  mma_smem<kHi>(tmem, a + (((x / 4) * kPanel + (x % 4) * 32) >> 4), bx, kQk, g > 0 || x > 0);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok || !(ok = reached(&sh.full[4], n & 1))) break;
+          {
+            const uint32_t a = mma_desc_lo(tile + kRopePanel * kPanel, 16), b = mma_desc_lo(q_at + kRopePanel * kQPanel, 16);
+            if (elect_one()) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma_smem<kHi>(tmem + (kCodes ? N : 0), a + (x * 32 >> 4), b + (x * 32 >> 4), kCodes ? kQr : kQk,
+                              !kCodes || x > 0);
+            }
+            __syncwarp();
+          }
+          commit(&sh.s_full);
+          if (!(ok = reached(&sh.p_full, n & 1))) break;
+          const uint32_t b = mma_desc_lo(tile + kRopePanel * kPanel, kPanel);
+#pragma unroll 1
+          for (int g = 0; g < kQuarters; ++g) {
+            const uint32_t a = mma_desc_lo(tile + 2 * g * kPanel, kPanel);
+            if (elect_one()) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                mma_smem<kHi>(tmem + kO + g * N, a + x * 128, b + x * 128, kPv, k > w.k0 || x > 0);
+              mma_commit(&sh.empty[g]);
+            }
+            __syncwarp();
+          }
+          commit(&sh.empty[4]);
+          commit(&sh.o_done);
+        }
+      }
+      if (!ok) {
+        // Give what was issued a while to end before tensor memory is freed.
+        volatile int no = 0;
+        commit(&sh.drain);
+        wait_for(&sh.drain, 0, &no);
+      }
+    } else if constexpr (!kCodes) {
+      // ---- rows: a lane knows four neighbouring ones of a tile
+      const int rw = warp - kProduct - 1;
+      bool more = w.seek(c0, c1, prefix, p), ok = true;
+      auto reached = [&](uint64_t* bar, uint32_t phase) {
+        return __all_sync(kFullMask, wait_for(bar, phase, dead));
+      };
+      int k = w.k0;
+      auto advance = [&]() {
+        if (++k == w.k1) {
+          more = w.next(prefix, p);
+          k = w.k0;
+        }
+      };
+      uint32_t n = 0;  // tiles so far
+      // Straight into the panels, as soon as they are free: 16 rows that lie one behind
+      // the other, or four at a time.  Rows that are none read zeros.
+      int32_t found[4];
+      // The lane's rows of tile k, four neighbouring ones, found a tile ahead.
+      auto find = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = k * kKeys + lane * 4 + i;
+          found[i] = more && j < w.unit.end ? latent_key(p, w.row, j) : kNoRow;
+        }
+      };
+      find();
+      uint32_t stage = 0;
+      while (more && ok) {
+        int32_t row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = found[i];
+        advance();
+        find();
+        const int32_t first = __shfl_sync(kFullMask, row[0], lane & 28);
+        bool next = first >= 0 && row[0] == first + (lane & 3) * 4;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) next &= row[i] == row[0] + i;
+        const uint32_t dense = __ballot_sync(kFullMask, next);
+        const int chunks = (kChunks - rw + kRowWarps - 1) / kRowWarps;  // this warp's
+        for (stage = 0; stage < 5; ++stage) {
+          if (!(ok = reached(&sh.empty[stage], (n & 1) ^ 1))) break;
+          if (stage == 4 && rw == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sh.row_scale[lane * 4 + i] = row[i] == kNoRow ? -1.f : 1.f;
+          }
+          __syncwarp();
+          const int panels = stage < 4 ? 2 : 1;
+          if (elect_one()) mbar_arrive_expect_tx(&sh.full[stage], panels * chunks * kChunkRows * 128);
+          __syncwarp();
+#pragma unroll 1
+          for (int c = rw; c < kChunks; c += kRowWarps) {
+            const uint32_t to = tile + stage * 2 * kPanel + c * kChunkRows * 128;
+            if ((dense >> (c * 4) & 15) == 15) {
+              const int32_t r0 = __shfl_sync(kFullMask, row[0], c * 4);
+              if (elect_one())
+                for (int x = 0; x < panels; ++x)
+                  tensor_load_2d(to + x * kPanel, &box_map, (stage * 2 + x) * 64, r0, &sh.full[stage]);
+            } else if (lane >> 2 == c) {
+              const int4 r = make_int4(max(row[0], -1), max(row[1], -1), max(row[2], -1), max(row[3], -1));
+              for (int x = 0; x < panels; ++x)
+                tensor_gather_rows(to + x * kPanel + (lane & 3) * 512, &row_map, (stage * 2 + x) * 64, r, &sh.full[stage]);
+            }
+            __syncwarp();
+          }
+        }
+        if (ok) ++n;
+      }
+      // What is still on its way writes shared memory: see it in.
+      volatile int no = 0;
+      for (uint32_t i = 0; i < 5; ++i) {
+        const uint32_t issued = n + (!ok && i < stage ? 1 : 0);
+        if (issued > 0) wait_for(&sh.full[i], (issued - 1) & 1, &no);
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kProduct) tmem_free(tmem, kCols);
+  if (tid == 0) ws.failed[me] = *dead;
+}
+
+constexpr int kDimJoin = kLatent / 4;  // threads: four dims each
+
+// Joins the parts of one query row of the unit that worker w's boundary is the first to
+// cut: out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).  Blocks past the workers write
+// the status words.
+template <int kIn, int N>
+__global__ void __launch_bounds__(kDimJoin)
+    latent_tiles_join_kernel(const LatentTilesParams p, const TilesSpace ws) {
+  grid_dep_wait();  // in every block: this grid must not be done before the first kernel is
+  const uint32_t rows = ws.workers * N;
+  if (blockIdx.x >= rows) {
+    int late = 0;
+    for (uint32_t w = threadIdx.x; w < ws.workers; w += blockDim.x) late |= ws.failed[w];
+    late = __syncthreads_or(late);
+    latent_write_status(p, blockIdx.x - rows, late ? HS_ST_TIMEOUT : 0);
+    return;
+  }
+  const int w = blockIdx.x / N, m = blockIdx.x - w * N;
+  const int4 j = ws.joins[w];
+  if (j.x < 0) return;
+  const AttnRow row = latent_row(p, j.x);
+  const Unit u = unit_at<N>(p, row, j.y);
+  const int in = m / u.heads, head = u.head0 + m - in * u.heads;
+  if (in >= u.tokens) return;
+  const int w0 = w - 1, w1 = j.z;
+  auto part = [&](int x) { return ws.slots + static_cast<int64_t>(2 * x + (x == w0 ? 1 : 0)) * slot_floats(N); };
+  float top = -INFINITY, l = 0.f;
+  for (int x = w0; x <= w1; ++x) top = fmaxf(top, part(x)[N * kLatent + m]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int x = w0; x <= w1; ++x) {
+    const float* s = part(x);
+    const float add = fast_exp2(s[N * kLatent + m] - ref);
+    const float4 o = *reinterpret_cast<const float4*>(s + m * kLatent + threadIdx.x * 4);
+    l += add;
+    acc.x += add * o.x;
+    acc.y += add * o.y;
+    acc.z += add * o.z;
+    acc.w += add * o.w;
+  }
+  const float f = l == 0.f ? 0.f : 1.0f / l;  // (0: no row; NaN stays)
+  const int64_t tok = static_cast<int64_t>(row.q0) + u.i0 + in;
+  constexpr bool kB = kIn == HS_DT_BF16;
+  *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + threadIdx.x * 8) =
+      make_uint2(pack2<kB>(acc.x * f, acc.y * f), pack2<kB>(acc.z * f, acc.w * f));
+  if (threadIdx.x == 0 && p.lse) p.lse[tok * p.heads + head] = kLn2 * (top + log2f(l));
+}
+
+struct TilesKernels {
+  void (*main)(const LatentTilesParams, const TilesSpace, const CUtensorMap, const CUtensorMap);
+  void (*join)(const LatentTilesParams, const TilesSpace);
+  int smem;
+};
+template <int kIn, bool kCodes, int N>
+TilesKernels kernels() {
+  return TilesKernels{latent_tiles_kernel<kIn, kCodes, N>, latent_tiles_join_kernel<kIn, N>,
+                      kTileBytes + 9 * N * 128 + 1024};
+}
+template <int kIn, bool kCodes>
+TilesKernels pick_size(int n) {
+  return n == 16 ? kernels<kIn, kCodes, 16>() : (n == 32 ? kernels<kIn, kCodes, 32>() : kernels<kIn, kCodes, 64>());
+}
+TilesKernels pick(int in_dtype, bool codes, int n) {
+  if (in_dtype == HS_DT_BF16) return codes ? pick_size<HS_DT_BF16, true>(n) : pick_size<HS_DT_BF16, false>(n);
+  return codes ? pick_size<HS_DT_F16, true>(n) : pick_size<HS_DT_F16, false>(n);
+}
+
+// Query rows of a unit: as many as there are, up to 64, since every unit reads its latent rows
+// again (147 us for 64 at once over 16 tiles, four times 84.5 for 16 at a time); 32 where
+// the batch's running sums would not fit beside 64.
+int unit_rows(const LatentParams& p) {
+  const int64_t rows = static_cast<int64_t>(p.heads) * (p.indexed ? 1 : p.max_q);
+  if (rows <= 16) return 16;
+  return rows <= 32 || (!p.indexed && p.batch > 1024) ? 32 : 64;
+}
+
+constexpr int kMostSmem = 232448 - 4608;  // of a block, less what is not dynamic
+
+std::mutex g_mu;
+bool g_ready[64] = {false};
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+// Once per device: shared memory opt-in, and a check that the kernel was launched with
+// the registers that its warpgroups redistribute (a split of more than the launch's total
+// would wait for ever).
+hs_err tiles_setup(const DeviceInfo& dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (g_ready[dev.device]) return HS_OK;
+  for (int dt : {HS_DT_F16, HS_DT_BF16})
+    for (bool codes : {false, true})
+      for (int n : {16, 32, 64}) {
+        const TilesKernels k = pick(dt, codes, n);
+        const void* f = reinterpret_cast<const void*>(k.main);
+        cudaFuncAttributes at;
+        cudaError_t e = cudaFuncGetAttributes(&at, f);
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+        if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_latent_attention: %s", cudaGetErrorString(e));
+        if (codes && at.numRegs < static_cast<int>(kLaunchRegs))
+          return fail(HS_ERR_CUDA, "hs_latent_attention: built with %d registers a thread", at.numRegs);
+      }
+  if (g_encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got);
+    if (e != cudaSuccess || got != cudaDriverEntryPointSuccess || fn == nullptr)
+      return fail(HS_ERR_CUDA, "hs_latent_attention: cuTensorMapEncodeTiled is not available");
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  g_ready[dev.device] = true;
+  return HS_OK;
+}
+
+// 16-bit rows as [rows][dims], read 64 dims of `rows` at a time (1: gathered), swizzled as
+// the MMA wants them.
+bool encode_rows(CUtensorMap* map, const LatentParams& p, bool bf16, int rows) {
+  const cuuint64_t dims[2] = {kLatent + kRope, static_cast<cuuint64_t>(p.num_rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.row_stride)};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)}, steps[2] = {1, 1};
+  return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<unsigned char*>(p.rows), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Units of a call, at most, with the query heads' chunks.
+static int64_t most_units(const LatentParams& p) {
+  const int64_t n = unit_rows(p), chunks = (p.heads + n - 1) / n;
+  if (p.indexed) return p.batch * chunks;
+  const int64_t tokens = p.heads >= n ? 1 : n / p.heads;
+  return (p.n_tokens / tokens + p.batch) * chunks;
+}
+bool latent_tiles_fits(const LatentParams& p) {
+  // Whole numbers of 32 bits count the tiles, and the join's blocks.
+  const int64_t per = p.indexed ? (p.max_q + kKeys - 1) / kKeys + 1 + kUnitCost : 1 + kUnitCost;
+  return p.batch <= INT32_MAX - 2048 * 64 && most_units(p) * per <= INT32_MAX;
+}
+int64_t latent_tiles_max_len(const LatentParams& p) {
+  const int64_t units = most_units(p) > 0 ? most_units(p) : 1;
+  return (INT32_MAX / units - 1 - kUnitCost) * kKeys;
+}
+
+int64_t latent_tiles_workspace(const LatentParams& p, const DeviceInfo& dev) {
+  return kTilesHead + 2ll * dev.sm_count * slot_floats(unit_rows(p)) * 4;
+}
+
+hs_err latent_tiles_launch(const LatentParams& p, int in_dtype, bool codes, void* workspace, bool give_up,
+                           const DeviceInfo& dev, cudaStream_t stream) {
+  if (dev.sm_count > 2048) return fail(HS_ERR_UNSUPPORTED, "hs_latent_attention: %d SMs", dev.sm_count);
+  const hs_err err = tiles_setup(dev);
+  if (err != HS_OK) return err;
+  const int n = unit_rows(p);
+  const TilesKernels k = pick(in_dtype, codes, n);
+  TilesSpace ws;
+  unsigned char* at = static_cast<unsigned char*>(workspace);
+  ws.joins = reinterpret_cast<int4*>(at);
+  ws.failed = reinterpret_cast<int32_t*>(at + 2048 * sizeof(int4));
+  ws.slots = reinterpret_cast<float*>(at + kTilesHead);
+  ws.workers = static_cast<uint32_t>(dev.sm_count);
+  LatentTilesParams tp;
+  static_cast<LatentParams&>(tp) = p;
+  tp.tokens = p.indexed || p.heads >= n ? 1 : n / p.heads;
+  tp.chunks = (p.heads + n - 1) / n;
+  tp.give_up = give_up;
+  const int smem = k.smem + (p.indexed ? 0 : (p.batch + 1) * 4);
+  CUtensorMap maps[2] = {};
+  for (int i = 0; !codes && i < 2; ++i)
+    if (!encode_rows(&maps[i], p, in_dtype == HS_DT_BF16, i == 0 ? 1 : kChunkRows))
+      return fail(HS_ERR_ARG, "hs_latent_attention: rows %lld bytes apart", static_cast<long long>(p.row_stride));
+  k.main<<<dev.sm_count, block_threads(codes), smem, stream>>>(tp, ws, maps[0], maps[1]);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_latent_attention launch: %s", cudaGetErrorString(e));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count * n) + (p.status ? p.batch : 0));
+  cfg.blockDim = dim3(kDimJoin);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k.join, tp, ws);
+  if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_latent_attention join: %s", cudaGetErrorString(e));
+  return HS_OK;
+}
+
+}  // namespace hs

@@ -106,9 +106,10 @@ __host__ __device__ constexpr uint32_t mma_desc_hi(uint32_t group) {
   return group >> 4 | 1u << 14 | 2u << 29;
 }
 // Instruction descriptor: fp16 or bf16 operands, fp32 accumulator, M x N.
-__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int m, int n, bool b_across) {
+__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int m, int n, bool b_across,
+                                                bool a_across = false) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
-         ((b_across ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         ((a_across ? 1u : 0u) << 15) | ((b_across ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 // D (+)= A B^T with both operands in shared memory, or A in tensor memory.
@@ -139,6 +140,92 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
       : "memory");
 }
 
+// ------------------------------------------------------------------ operands and waits
+// Pairs of floats in 64-bit registers and the paired fp32 operations on them.
+__device__ __forceinline__ uint64_t two_words(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t two_floats(float lo, float hi) {
+  return two_words(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float low_float(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x));
+}
+__device__ __forceinline__ float high_float(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 16-byte chunk c (of 64 elements' eight) of row r of a panel.
+__device__ __forceinline__ uint32_t in_panel(int r, int c) {
+  return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2t(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+// Waits for phase `parity`, unless the block has given up; gives up itself
+// after kWaitNs.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((n & 15) == 15) {
+      if (*dead) return false;
+      const uint64_t now = global_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitNs) {
+        *dead = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ tiled loads
 // Box at (x0, x1, x2, x3); x0 times the element size is a multiple of 16 bytes.
 __device__ __forceinline__ void tensor_load_4d(uint32_t dst, const CUtensorMap* map, int x0, int x1,
@@ -156,6 +243,25 @@ __device__ __forceinline__ void tensor_load_3d(uint32_t dst, const CUtensorMap* 
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
       "[%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x0), "r"(x1), "r"(x2)
+      : "memory");
+}
+
+__device__ __forceinline__ void tensor_load_2d(uint32_t dst, const CUtensorMap* map, int x0, int x1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x0), "r"(x1)
+      : "memory");
+}
+// Four single rows of a two-dimensional map from x0 on, one behind the other; x0 times
+// the element size is a multiple of 16 bytes.  Rows outside the map read zeros.
+__device__ __forceinline__ void tensor_gather_rows(uint32_t dst, const CUtensorMap* map, int x0, int4 rows,
+                                                   uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x0), "r"(rows.x), "r"(rows.y), "r"(rows.z),
+      "r"(rows.w)
       : "memory");
 }
 

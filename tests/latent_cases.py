@@ -188,11 +188,11 @@ class LatentInputs:
         """Bounds on |out - plain| and |lse - plain|.  fp32 products and sums: a score is off by at
         most (dims + 8) units of 2^-24 of sum |q k| (a code's scale and its product with the value
         among them); the sums over n rows by n units; the exponentials by 4 units.  On the tensor
-        cores ("split") the weights are rounded to 16 bits (half a step; over codes they are fp16,
-        times the scales), bf16 queries over codes are taken as fp16, off by 2^-33 of the row's
-        largest, and outputs by half a step; fp16 weights have an absolute half step, at most 2^-29
-        of the largest value for each of n rows.  "tiles" also rounds what codes stand for to fp16,
-        half a step in keys and in values."""
+        cores ("tiles") the weights are rounded to 16 bits (half a step; over codes they are fp16,
+        times the scales), what codes stand for to fp16 (half a step in keys and in values), bf16
+        queries over codes are taken as fp16, off by 2^-33 of the row's largest, and outputs by half
+        a step; fp16 weights have an absolute half step, at most 2^-29 of the largest value for each
+        of n rows."""
         out, lse, size, unit, n, wide = ref
         dims = self.R + self.P
         es = (dims + 8) * U32 * unit
@@ -204,10 +204,8 @@ class LatentInputs:
                 v = self.held[:, : self.R].abs()
                 small = 2.0 ** -29 * float(v.max()) if v.numel() else 0.0
             if self.fmt == "fp8":
-                es = es + 2.0 ** -33 * wide
-                if kind == "tiles":
-                    es = es + half_step(torch.float16) * unit
-                    up += half_step(torch.float16)
+                es = es + 2.0 ** -33 * wide + half_step(torch.float16) * unit
+                up += half_step(torch.float16)
         u = half_step(self.dtype) if self.dtype != torch.float32 else U32
         rel = 2 * es + (2 * n[:, None] + 16) * U32 + up
         tiny = 2.0 ** -25 if self.dtype == torch.float16 else 0.0

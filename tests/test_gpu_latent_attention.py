@@ -12,6 +12,7 @@ from latent_cases import LatentInputs
 pytestmark = pytest.mark.gpu
 
 
+
 @pytest.fixture(scope="module")
 def hs(dev):
     import sparse_attention_kv_row_gb300
@@ -60,7 +61,7 @@ TYPES = [("bf16", "fp8"), ("f16", "fp8"), ("bf16", "same"), ("f16", "same")]
 def test_indexed(hs, dev, dtype, fmt, heads, T, top_k):
     a = LatentInputs(heads=heads, dtype=dtype, fmt=fmt, seed=T)
     a.indexed(T, top_k, 2 * top_k + 5, empty=[T // 2] if T > 2 else [], bad=[T - 1] if T > 1 else [])
-    a.check(hs, dev, "split")
+    a.check(hs, dev, "tiles")
 
 
 @pytest.mark.parametrize("dtype,fmt", TYPES)
@@ -70,4 +71,23 @@ def test_indexed(hs, dev, dtype, fmt, heads, T, top_k):
     [(i * 7 % 50, 1 + i % 2) for i in range(40)]])
 def test_paged(hs, dev, dtype, fmt, heads, page, lens):
     a = LatentInputs(heads=heads, dtype=dtype, fmt=fmt, seed=page)
-    a.paged(lens, page, gap=3).check(hs, dev, "split")
+    a.paged(lens, page, gap=3).check(hs, dev, "tiles")
+
+
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+@pytest.mark.parametrize("heads,T,top_k", [(17, 3, 200), (32, 2, 129), (64, 40, 260), (65, 3, 100), (128, 5, 700),
+                                           (128, 160, 140), (100, 2, 1), (20, 2, 5000)])
+def test_indexed_heads(hs, dev, dtype, fmt, heads, T, top_k):
+    a = LatentInputs(heads=heads, dtype=dtype, fmt=fmt, seed=T)
+    a.indexed(T, top_k, 2 * top_k + 5, empty=[T // 2] if T > 2 else [], bad=[T - 1])
+    a.check(hs, dev, "tiles")
+
+
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+@pytest.mark.parametrize("heads,page", [(16, 64), (128, 16), (12, 7), (64, 1)])
+@pytest.mark.parametrize("lens", [
+    [(0, 9)], [(120, 7), (128, 1), (200, 20)], [(700, 3), (None, 0), (3, 2), (0, 0), (0, 140)],
+    [(i * 37 % 290, 1 + i % 5) for i in range(30)]])
+def test_paged_chunks(hs, dev, dtype, fmt, heads, page, lens):
+    a = LatentInputs(heads=heads, dtype=dtype, fmt=fmt, seed=page)
+    a.paged(lens, page, gap=3).check(hs, dev, "tiles")
