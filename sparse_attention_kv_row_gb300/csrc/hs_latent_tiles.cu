@@ -861,52 +861,73 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
 }
 
 constexpr int kDimJoin = kLatent / 4;  // threads: four dims each
+// Query rows of a block, and parts of them, whose loads are on their way together.
+constexpr int join_rows(int n) { return n / 16; }
+constexpr int join_parts(int n) { return n == 16 ? 8 : 2; }
 
-// Joins the parts of one query row of the unit that worker w's boundary is the first to
-// cut: out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).  Blocks past the workers write
-// the status words.
+// Joins the parts of a few query rows of the unit that worker w's boundary is the first to
+// cut: out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M), with the running maximum M in
+// one pass.  Blocks past the workers write the status words.
 template <int kIn, int N>
 __global__ void __launch_bounds__(kDimJoin)
     latent_tiles_join_kernel(const LatentTilesParams p, const TilesSpace ws) {
   grid_dep_wait();  // in every block: this grid must not be done before the first kernel is
-  const uint32_t rows = ws.workers * N;
-  if (blockIdx.x >= rows) {
+  constexpr int kJoinRows = join_rows(N), kBlocks = N / kJoinRows;
+  const uint32_t blocks = ws.workers * kBlocks;
+  if (blockIdx.x >= blocks) {
     int late = 0;
     for (uint32_t w = threadIdx.x; w < ws.workers; w += blockDim.x) late |= ws.failed[w];
     late = __syncthreads_or(late);
-    latent_write_status(p, blockIdx.x - rows, late ? HS_ST_TIMEOUT : 0);
+    latent_write_status(p, blockIdx.x - blocks, late ? HS_ST_TIMEOUT : 0);
     return;
   }
-  const int w = blockIdx.x / N, m = blockIdx.x - w * N;
+  const int w = blockIdx.x / kBlocks, m0 = (blockIdx.x - w * kBlocks) * kJoinRows;
   const int4 j = ws.joins[w];
   if (j.x < 0) return;
+  const int w0 = w - 1, w1 = j.z;
+  float top[kJoinRows], l[kJoinRows];
+  float4 acc[kJoinRows];
+#pragma unroll
+  for (int i = 0; i < kJoinRows; ++i) {
+    top[i] = -INFINITY;
+    l[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll (join_parts(N))
+  for (int x = w0; x <= w1; ++x) {
+    const float* s = ws.slots + static_cast<int64_t>(2 * x + (x == w0 ? 1 : 0)) * slot_floats(N);
+    float4 o[kJoinRows];
+    float lse[kJoinRows];
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      o[i] = *reinterpret_cast<const float4*>(s + (m0 + i) * kLatent + threadIdx.x * 4);
+      lse[i] = s[N * kLatent + m0 + i];
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      const float most = fmaxf(top[i], lse[i]), ref = most == -INFINITY ? 0.f : most;
+      const float keep = fast_exp2(top[i] - ref), add = fast_exp2(lse[i] - ref);
+      top[i] = most;
+      l[i] = l[i] * keep + add;
+      acc[i].x = acc[i].x * keep + add * o[i].x;
+      acc[i].y = acc[i].y * keep + add * o[i].y;
+      acc[i].z = acc[i].z * keep + add * o[i].z;
+      acc[i].w = acc[i].w * keep + add * o[i].w;
+    }
+  }
   const AttnRow row = latent_row(p, j.x);
   const Unit u = unit_at<N>(p, row, j.y);
-  const int in = m / u.heads, head = u.head0 + m - in * u.heads;
-  if (in >= u.tokens) return;
-  const int w0 = w - 1, w1 = j.z;
-  auto part = [&](int x) { return ws.slots + static_cast<int64_t>(2 * x + (x == w0 ? 1 : 0)) * slot_floats(N); };
-  float top = -INFINITY, l = 0.f;
-  for (int x = w0; x <= w1; ++x) top = fmaxf(top, part(x)[N * kLatent + m]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int x = w0; x <= w1; ++x) {
-    const float* s = part(x);
-    const float add = fast_exp2(s[N * kLatent + m] - ref);
-    const float4 o = *reinterpret_cast<const float4*>(s + m * kLatent + threadIdx.x * 4);
-    l += add;
-    acc.x += add * o.x;
-    acc.y += add * o.y;
-    acc.z += add * o.z;
-    acc.w += add * o.w;
+#pragma unroll
+  for (int i = 0; i < kJoinRows; ++i) {
+    const int in = (m0 + i) / u.heads, head = u.head0 + m0 + i - in * u.heads;
+    if (in >= u.tokens) return;
+    const float f = l[i] == 0.f ? 0.f : 1.0f / l[i];  // (0: no row; NaN stays)
+    const int64_t tok = static_cast<int64_t>(row.q0) + u.i0 + in;
+    constexpr bool kB = kIn == HS_DT_BF16;
+    *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + threadIdx.x * 8) =
+        make_uint2(pack2<kB>(acc[i].x * f, acc[i].y * f), pack2<kB>(acc[i].z * f, acc[i].w * f));
+    if (threadIdx.x == 0 && p.lse) p.lse[tok * p.heads + head] = kLn2 * (top[i] + log2f(l[i]));
   }
-  const float f = l == 0.f ? 0.f : 1.0f / l;  // (0: no row; NaN stays)
-  const int64_t tok = static_cast<int64_t>(row.q0) + u.i0 + in;
-  constexpr bool kB = kIn == HS_DT_BF16;
-  *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + threadIdx.x * 8) =
-      make_uint2(pack2<kB>(acc.x * f, acc.y * f), pack2<kB>(acc.z * f, acc.w * f));
-  if (threadIdx.x == 0 && p.lse) p.lse[tok * p.heads + head] = kLn2 * (top + log2f(l));
 }
 
 struct TilesKernels {
@@ -1037,7 +1058,7 @@ hs_err latent_tiles_launch(const LatentParams& p, int in_dtype, bool codes, void
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(HS_ERR_CUDA, "hs_latent_attention launch: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count * n) + (p.status ? p.batch : 0));
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count * (n / join_rows(n))) + (p.status ? p.batch : 0));
   cfg.blockDim = dim3(kDimJoin);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
