@@ -66,6 +66,9 @@ constexpr int kRowWarps = 3;                      // that bring in 16-bit rows
 // those of 16-bit rows (over codes, as many without work).
 constexpr int product_warp(bool codes) { return codes ? 20 : 4; }
 constexpr int block_threads(bool codes) { return (product_warp(codes) + 4) * kWarp; }
+// Over codes, the weights of up to 32 query rows have a panel of their own, and the keys a
+// place in tensor memory.
+constexpr bool room_apart(bool codes, int n) { return codes && n <= 32; }
 // Registers over codes: of the launch, and of the warpgroups after they have shared them
 // out (softmax, four that convert, one of the products).
 constexpr uint32_t kLaunchRegs = 80;
@@ -77,7 +80,7 @@ static_assert(softmax_regs(64) + 4 * convert_regs(64) + product_regs(64) <= 6 * 
               "what the block was launched with");
 constexpr float kNoScale = 0x1p-100f;      // 2^e of a row of zeros
 constexpr float kRaise = 8.f;             // log2 of how far weights may exceed their reference
-constexpr int kUnitCost = 2;              // a unit's fixed cost in tiles
+constexpr int kUnitCost = 3;              // a unit's fixed cost in tiles
 
 struct LatentTilesParams : LatentParams {
   int tokens;      // of a unit, at most
@@ -254,21 +257,22 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
   // Keys that codes stand for go to tensor memory where there is room: the first product
   // then takes 12 clocks for 16 query rows and 18 for 32, 42 and 43 with keys in shared
   // memory, which is read and written by everything else.
-  constexpr bool kKeysApart = kCodes && N <= 32;
+  constexpr bool kApart = room_apart(kCodes, N);
   // Columns of tensor memory: the scores (the rotary dims' behind them), the outputs, and
   // those keys.
   constexpr int kO = 2 * N, kK = 6 * N;
-  constexpr uint32_t kCols = kKeysApart || N == 64 ? 512 : (N == 16 ? 128 : 256);
-  static_assert(kK + (kKeysApart ? kLatent / 2 : 0) <= kCols, "tensor memory");
+  constexpr uint32_t kCols = kApart || N == 64 ? 512 : (N == 16 ? 128 : 256);
+  static_assert(kK + (kApart ? kLatent / 2 : 0) <= kCols, "tensor memory");
   // fp16 weights reach 2^(6 + 8) and keep what is 2^-30 of the reference.
   constexpr float kBias = kBf16 ? 0.f : 6.f;
   constexpr int kStep = N < 32 ? N : 32;  // columns read at once
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + kTileBytes + 9 * kQPanel);
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + kTileBytes + 9 * kQPanel + (kApart ? kPanel : 0));
   __shared__ Shared<N> sh;
   const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
   const uint32_t tile = smem_addr(smem), q_at = tile + kTileBytes;
+  const uint32_t weights = kApart ? q_at + 9 * kQPanel : tile + kRopePanel * kPanel;
 
   if (tid == 0) {
     mbar_init(&sh.q_full, 4);
@@ -499,9 +503,8 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
           if (tid < N) sh.ref[tid] -= sh.most[0][tid];
           group_sync();
         }
-        // ---- weights, into the rotary panel: a row of up to 64 query rows
+        // ---- weights: a row of up to 64 query rows
         const float kn = kCodes ? (mine > 0.f ? mine * (1.0f / norm) : 0.f) : 1.f;
-        const uint32_t to = tile + kRopePanel * kPanel;
 #pragma unroll
         for (int q = 0; q < N; q += 8) {
           uint32_t v[4];
@@ -514,7 +517,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
             // operands: half a step off each, whose errors average out over the rows.
             v[i] = kCodes ? pack2<false>(e0 * kn, e1 * kn) : pack2<kBf16>(e0, e1);
           }
-          st_shared_v4(to + in_panel(tid, q / 8), make_uint4(v[0], v[1], v[2], v[3]));
+          st_shared_v4(weights + in_panel(tid, q / 8), make_uint4(v[0], v[1], v[2], v[3]));
         }
         fence_proxy_async_smem();  // the MMA reads through the async proxy
         tc_fence_before();
@@ -622,6 +625,20 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
           cp_async_16_zfill(panel + kPanel + in_panel(rows + r, lane & 7),
                             p.rows + max(at, 0) * p.row_stride + g * 128 + (lane & 7) * 16, at >= 0);
         }
+        // 16 of the rotary dims: now, if the weights leave their place alone.
+        auto send_rope = [&]() {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = i * 16 + (lane >> 1);
+            const int32_t at = __shfl_sync(kFullMask, row, r);
+            cp_async_16_zfill(pe + in_panel(rows + r, 2 * g + (lane & 1)),
+                              p.rows + max(at, 0) * p.row_stride + kLatent + 16 + g * 32 + (lane & 1) * 16, at >= 0);
+          }
+        };
+        if constexpr (kApart) {
+          if (!wait_all(&sh.empty[4], (n & 1) ^ 1)) break;
+          send_rope();
+        }
         cp_async_commit();
         // The row's 2^e, the power of two not below its largest scale, within what has a
         // reciprocal; and this quarter's scale over it.
@@ -656,7 +673,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
                 y[i * 8 + 2 * j + 1] = scaled_pair(e4m3_to_f16(x[j] >> 16), f, f_lo);
               }
             }
-            if constexpr (kKeysApart)
+            if constexpr (kApart)
               tmem_st16(tmem + (static_cast<uint32_t>(rows) << 16) + kK + g * 64 + half * 32 + part * 16, y);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -664,25 +681,22 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
                            make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
           }
         }
-        if constexpr (kKeysApart) {
+        if constexpr (kApart) {
           tmem_wait_st();
           tc_fence_before();
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.full[g]);
-        // ---- 16 of the rotary dims
-        if (!wait_all(&sh.empty[4], (n & 1) ^ 1)) break;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = i * 16 + (lane >> 1);
-          const int32_t at = __shfl_sync(kFullMask, row, r);
-          cp_async_16_zfill(pe + in_panel(rows + r, 2 * g + (lane & 1)),
-                            p.rows + max(at, 0) * p.row_stride + kLatent + 16 + g * 32 + (lane & 1) * 16, at >= 0);
+        if constexpr (!kApart) {
+          if (!wait_all(&sh.empty[4], (n & 1) ^ 1)) break;
+          send_rope();
         }
         if (g == 0) sh.row_scale[key] = row == kNoRow ? -1.f : e;
-        cp_async_commit_wait_all();
-        fence_proxy_async_smem();
+        if constexpr (!kApart) {
+          cp_async_commit_wait_all();
+          fence_proxy_async_smem();
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.full[4]);
         if (++k == w.k1) {
@@ -733,7 +747,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
                 const uint32_t bx = b + (((x / 4) * kQPanel + (x % 4) * 32) >> 4);
-                if constexpr (kKeysApart)
+                if constexpr (kApart)
                   mma_tmem<kHi>(tmem, tmem + kK + g * 64 + x * 8, bx, kQk, g > 0 || x > 0);
                 else
                   mma_smem<kHi>(tmem, a + (((x / 4) * kPanel + (x % 4) * 32) >> 4), bx, kQk, g > 0 || x > 0);
@@ -752,9 +766,10 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
             }
             __syncwarp();
           }
+          if constexpr (kApart) commit(&sh.empty[4]);
           commit(&sh.s_full);
           if (!(ok = reached(&sh.p_full, n & 1))) break;
-          const uint32_t b = mma_desc_lo(tile + kRopePanel * kPanel, kPanel);
+          const uint32_t b = mma_desc_lo(weights, kPanel);
 #pragma unroll 1
           for (int g = 0; g < kQuarters; ++g) {
             const uint32_t a = mma_desc_lo(tile + 2 * g * kPanel, kPanel);
@@ -766,7 +781,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
             }
             __syncwarp();
           }
-          commit(&sh.empty[4]);
+          if constexpr (!kApart) commit(&sh.empty[4]);
           commit(&sh.o_done);
         }
       }
@@ -938,7 +953,7 @@ struct TilesKernels {
 template <int kIn, bool kCodes, int N>
 TilesKernels kernels() {
   return TilesKernels{latent_tiles_kernel<kIn, kCodes, N>, latent_tiles_join_kernel<kIn, N>,
-                      kTileBytes + 9 * N * 128 + 1024};
+                      kTileBytes + 9 * N * 128 + (room_apart(kCodes, N) ? kPanel : 0) + 1024};
 }
 template <int kIn, bool kCodes>
 TilesKernels pick_size(int n) {
