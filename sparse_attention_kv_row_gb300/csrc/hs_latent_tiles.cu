@@ -10,8 +10,8 @@
 // A tile lies in shared memory once, as 9 panels of 64 dims (128 bytes a row, swizzled):
 // read along the dims as keys, across the rows as values, so that every latent row is
 // read, and widened where it is codes, once for all N query rows.  S and O stay in
-// tensor memory (6 N columns).  The weights take the place of the rotary panel, which is
-// done with by then.
+// tensor memory (6 N columns).  For more than 32 query rows, and over 16-bit rows, the
+// weights take the place of the rotary panel, which is done with by then.
 //
 // Codes become fp16 times the row's scales, each divided by a power of two 2^e of the
 // row (at least its largest scale): half a step of fp16 of every value.  2^e goes to the
@@ -34,14 +34,17 @@
 // What bounds it: the chain of a tile (its rows come in, four times the keys' product with
 // what has come, softmax, four times the values' product, and only then room for the next
 // rows), behind a start of some 8 us.  One unit an SM over codes takes, for 1, 2, 4, 8 and
-// 16 tiles, 12.6, 16.8, 25.2, 45.9 and 84.5 us with 16 query rows and 26, 34, 48, 84 and
-// 147 us with 64: 4.8 and 7.9 us a tile, 2.4 TB/s of rows and 0.29 PFLOP/s at 16 tiles.
+// 16 tiles, 13.0, 17.2, 25.6, 43.8 and 81.0 us with 16 query rows and 23.2, 30.0, 44.2,
+// 80.6 and 141.5 us with 64: 4.6 and 7.6 us a tile, 2.5 TB/s of rows and 0.31 PFLOP/s at
+// 16 tiles.  Nothing is full then (memory to 2.6 of 6.8 TB/s, shared memory to 37 %, the
+// tensor cores to 22 %, the issue of instructions to 31 %): the chain takes the time.
 // Measured against it, at 16 tiles: 16 query rows by 32 latent rows on mma.sync, eight warps
-// on their own (94 us, and 330 for 64 query rows, which it does 16 at a time); codes landing
-// in a buffer of their own ahead of their panels (83 to 92 us and 150 to 197: the room is
-// three quarters of a tile's codes at most, and the copies' and the conversion's accesses to
-// shared memory then meet); rows of codes by bulk copies (one row an instruction, 90 to 145
-// clocks each in its warp).
+// on their own (94 us, and 330 for 64 query rows, which it does 16 at a time); half of the
+// codes landing a tile ahead in buffers of their own (5 % slower in a decode batch); rows of
+// codes by bulk copies (one row an instruction, 90 to 145 clocks each in its warp); rotary
+// values and scales loaded into registers before their place is free (7 % slower).  A panel
+// of their own for the weights of up to 32 query rows, so that rotary values come in with
+// the codes, takes 3 to 5 % off.
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -80,7 +83,9 @@ static_assert(softmax_regs(64) + 4 * convert_regs(64) + product_regs(64) <= 6 * 
               "what the block was launched with");
 constexpr float kNoScale = 0x1p-100f;      // 2^e of a row of zeros
 constexpr float kRaise = 8.f;             // log2 of how far weights may exceed their reference
-constexpr int kUnitCost = 3;              // a unit's fixed cost in tiles
+// A unit's fixed cost (its queries, its outputs) in tiles.  Counted as 1, 2, 3 and 4 it makes a
+// batch of chunks take 110, 95, 87 and 89 us, others within 3 % of each other.
+constexpr int kUnitCost = 3;
 
 struct LatentTilesParams : LatentParams {
   int tokens;      // of a unit, at most
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
   constexpr bool kRopeBf16 = kIn == HS_DT_BF16;
   constexpr bool kHalve = kIn == HS_DT_BF16 && kCodes;  // the queries' latent dims become fp16
   constexpr int kQPanel = N * 128;
-  // Keys that codes stand for go to tensor memory where there is room: the first product
+  // Keys that codes stand for go to tensor memory too where there is room: the first product
   // then takes 12 clocks for 16 query rows and 18 for 32, 42 and 43 with keys in shared
   // memory, which is read and written by everything else.
   constexpr bool kApart = room_apart(kCodes, N);
@@ -876,7 +881,9 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
 }
 
 constexpr int kDimJoin = kLatent / 4;  // threads: four dims each
-// Query rows of a block, and parts of them, whose loads are on their way together.
+// Query rows of a block, and parts of them, whose loads are on their way together: few rows
+// are cut into many parts (18 of 2 tokens: 14.8 us with the kernel before it, 20.4 with four
+// rows of two parts), many rows into few (66.1 us for 64 rows of 2 or 3 parts, 70.3 a row at a time).
 constexpr int join_rows(int n) { return n / 16; }
 constexpr int join_parts(int n) { return n == 16 ? 8 : 2; }
 
@@ -965,7 +972,7 @@ TilesKernels pick(int in_dtype, bool codes, int n) {
 }
 
 // Query rows of a unit: as many as there are, up to 64, since every unit reads its latent rows
-// again (147 us for 64 at once over 16 tiles, four times 84.5 for 16 at a time); 32 where
+// again (142 us for 64 at once over 16 tiles, four times 81 for 16 at a time); 32 where
 // the batch's running sums would not fit beside 64.
 int unit_rows(const LatentParams& p) {
   const int64_t rows = static_cast<int64_t>(p.heads) * (p.indexed ? 1 : p.max_q);
