@@ -75,9 +75,9 @@ constexpr bool room_apart(bool codes, int n) { return codes && n <= 32; }
 // Registers over codes: of the launch, and of the warpgroups after they have shared them
 // out (softmax, four that convert, one of the products).
 constexpr uint32_t kLaunchRegs = 80;
-constexpr uint32_t softmax_regs(int n) { return n == 64 ? 184 : 128; }
-constexpr uint32_t convert_regs(int n) { return n == 64 ? 64 : 72; }
-constexpr uint32_t product_regs(int n) { return n == 64 ? 40 : 64; }
+constexpr uint32_t softmax_regs(int n) { return n == 64 ? 208 : 128; }
+constexpr uint32_t convert_regs(int n) { return n == 64 ? 56 : 72; }
+constexpr uint32_t product_regs(int n) { return n == 64 ? 48 : 64; }
 static_assert(softmax_regs(64) + 4 * convert_regs(64) + product_regs(64) <= 6 * kLaunchRegs &&
                   softmax_regs(32) + 4 * convert_regs(32) + product_regs(32) <= 6 * kLaunchRegs,
               "what the block was launched with");
@@ -198,11 +198,11 @@ struct alignas(16) Shared {
   // read four at a time
   alignas(16) float undo[2][N];  // what undoes the factors of the queries
   alignas(16) float ref[N];      // what scores are taken relative to, negated
-  float factor[N];               // what rescales O; then what outputs are multiplied by
-  float most[4][N];              // per warp: largest scores, then sums
+  alignas(16) float factor[N];   // what rescales O; then what outputs are multiplied by
+  alignas(16) float most[4][N];  // per warp: largest scores, then sums
   float row_scale[kKeys];        // 2^e, or -1 for a row that nobody sees
   int64_t to[N];                 // a query row's output's byte, -1: none
-  uint64_t q_full, full[5], empty[5], s_full, p_full, o_done, drain;
+  uint64_t q_full, q_empty, full[5], empty[5], s_full, p_full, o_done, drain;
   uint32_t scale_most[4];
   int vis[N];                    // rows [0, vis) that a query row sees; 0: no query row
   bool started[N];               // a query row has met a row that it sees
@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
   const uint32_t weights = kApart ? q_at + 9 * kQPanel : tile + kRopePanel * kPanel;
 
   if (tid == 0) {
-    mbar_init(&sh.q_full, 4);
+    mbar_init(&sh.q_full, kCodes ? 16 : 4);
+    mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 5; ++i) {
       mbar_init(&sh.full[i], kCodes ? (i < kQuarters ? 4 : 16) : kRowWarps);
       mbar_init(&sh.empty[i], 1);
@@ -309,6 +310,58 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
   const uint32_t c1 = me < workers ? split_begin(me + 1, total, workers) : 0;
   volatile int* dead = &sh.dead;
   Walk<N> w;
+  // The queries of a unit, zeros past the last, a row a warp at a time, by the softmax's or
+  // (over codes) the converting warps: on their way, and then ready.
+  constexpr int kQueryWarps = kCodes ? 16 : 4;
+  const int query_warp = kCodes ? warp - 4 : warp;
+  auto send_queries = [&](const Walk<N>& nx) {
+#pragma unroll 1
+    for (int m = query_warp; m < N; m += kQueryWarps) {
+      const int in = m / nx.unit.heads, h = m - in * nx.unit.heads;
+      const bool live = in < nx.unit.tokens;
+      const unsigned char* src = p.q + (static_cast<int64_t>(nx.row.q0) + (live ? nx.unit.i0 + in : 0)) * p.q_token +
+                                 static_cast<int64_t>(live ? nx.unit.head0 + h : 0) * p.q_head;
+#pragma unroll
+      for (int c = lane; c < (kLatent + kRope) / 8; c += kWarp)
+        cp_async_16_zfill(q_at + (c / 8) * kQPanel + in_panel(m, c % 8), src + c * 16, live);
+    }
+    cp_async_commit();
+  };
+  auto finish_queries = [&](uint32_t u_at) {
+    cp_async_wait_group<0>();
+    if constexpr (kHalve) {
+      // In place, a chunk in the lane that brought it: latent dims to fp16, times a
+      // power of two of the row.
+#pragma unroll 2
+      for (int m = query_warp; m < N; m += kQueryWarps) {
+        uint32_t at[2], top = 0;
+        uint4 v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = i * kWarp + lane;
+          at[i] = q_at + (c / 8) * kQPanel + in_panel(m, c % 8);
+          v[i] = ld_shared_v4(at[i]);
+          const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+        }
+        top = __reduce_max_sync(kFullMask, top);
+        const float up = f16_factor(top);
+        if (lane == 0) sh.undo[u_at & 1][m] = 1.0f / up;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = pack2<false>(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
+          st_shared_v4(at[i], make_uint4(x[0], x[1], x[2], x[3]));
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_full);
+  };
 
   if (warp < 4) {
     // ---------------------------------------------------------------- softmax, outputs
@@ -317,57 +370,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
     const float s2 = p.softmax_scale * kLog2e;
     uint32_t n = 0, u_n = 0;  // tiles and units so far
     bool ok = true, more = w.seek(c0, c1, prefix, p);
-    // The queries of a unit, zeros past the last, a row a warp at a time: on their way,
-    // and then ready.
-    auto send_queries = [&](const Walk<N>& nx) {
-#pragma unroll 1
-      for (int m = warp; m < N; m += 4) {
-        const int in = m / nx.unit.heads, h = m - in * nx.unit.heads;
-        const bool live = in < nx.unit.tokens;
-        const unsigned char* src = p.q + (static_cast<int64_t>(nx.row.q0) + (live ? nx.unit.i0 + in : 0)) * p.q_token +
-                                   static_cast<int64_t>(live ? nx.unit.head0 + h : 0) * p.q_head;
-#pragma unroll
-        for (int c = lane; c < (kLatent + kRope) / 8; c += kWarp)
-          cp_async_16_zfill(q_at + (c / 8) * kQPanel + in_panel(m, c % 8), src + c * 16, live);
-      }
-      cp_async_commit();
-    };
-    auto finish_queries = [&](uint32_t u_at) {
-      cp_async_wait_group<0>();
-      if constexpr (kHalve) {
-        // In place, a chunk in the lane that brought it: latent dims to fp16, times a
-        // power of two of the row.
-#pragma unroll 2
-        for (int m = warp; m < N; m += 4) {
-          uint32_t at[2], top = 0;
-          uint4 v[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = i * kWarp + lane;
-            at[i] = q_at + (c / 8) * kQPanel + in_panel(m, c % 8);
-            v[i] = ld_shared_v4(at[i]);
-            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
-          }
-          top = __reduce_max_sync(kFullMask, top);
-          const float up = f16_factor(top);
-          if (lane == 0) sh.undo[u_at & 1][m] = 1.0f / up;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = pack2<false>(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
-            st_shared_v4(at[i], make_uint4(x[0], x[1], x[2], x[3]));
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_full);
-    };
-    if (more) {
+    if (!kCodes && more) {
       send_queries(w);
       finish_queries(0);
     }
@@ -448,9 +451,14 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
         if (group_any(over) || fresh) {
           // ---- new reference points: where they are exceeded, and where there are none yet
 #pragma unroll
-          for (int h = 0; h < N; ++h) {
-            const int most = __reduce_max_sync(kFullMask, ordered(z[h]));
-            if (lane == (h & 31)) sh.most[warp][h] = from_ordered(most);
+          for (int q = 0; q < N; q += kStep) {
+            int mine_most = 0;
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+              const int most = __reduce_max_sync(kFullMask, ordered(z[q + i]));
+              if (lane == i) mine_most = most;
+            }
+            if (lane < kStep) sh.most[warp][q + lane] = from_ordered(mine_most);
           }
           const uint32_t sm = __reduce_max_sync(kFullMask, mine > 0.f ? __float_as_uint(mine) : 0u);
           if (lane == 0) sh.scale_most[warp] = sm;
@@ -479,9 +487,11 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
           }
           fresh = group_any(waits);
 #pragma unroll
-          for (int h = 0; h < N; ++h) {
-            z[h] -= sh.most[0][h];
-            l[h] *= sh.factor[h];
+          for (int h = 0; h < N; h += 4) {
+            const float4 up = *reinterpret_cast<const float4*>(&sh.most[0][h]);
+            const float4 f = *reinterpret_cast<const float4*>(&sh.factor[h]);
+            z[h] -= up.x, z[h + 1] -= up.y, z[h + 2] -= up.z, z[h + 3] -= up.w;
+            l[h] *= f.x, l[h + 1] *= f.y, l[h + 2] *= f.z, l[h + 3] *= f.w;
           }
           if (k > w.k0) {
             // O is whole once the last tile's products are.
@@ -529,12 +539,13 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
         mbar_arrive(&sh.p_full);
       }
       if (!ok) break;
-      // ---- the next unit's queries, whose place the last tile's scores have left free
+      // ---- (over 16-bit rows) the next unit's queries, whose place the last tile's scores
+      // have left free
       const Unit unit = w.unit;
       const int32_t q0 = w.row.q0;
       const bool from_start = w.k0 == 0;
       more = w.next(prefix, p);
-      if (more) send_queries(w);
+      if (!kCodes && more) send_queries(w);
       // ---- sums over the rows, 32 lanes and 4 warps
 #pragma unroll
       for (int h = 0; h < N; ++h) {
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
           p.lse[(static_cast<int64_t>(q0) + unit.i0 + in) * p.heads + unit.head0 + tid - in * unit.heads] = lse * kLn2;
         }
       }
-      if (more) finish_queries(u_n + 1);
+      if (!kCodes && more) finish_queries(u_n + 1);
       ok = __all_sync(kFullMask, wait_for(&sh.o_done, (n - 1) & 1, dead));
       if (group_any(!ok)) break;
       tc_fence_after();
@@ -570,14 +581,19 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
 #pragma unroll
         for (int g = 0; g < kQuarters; ++g) tmem_pin(o[g]);
         if (whole) {
+          // Neighbouring lanes swap, so that each writes two dims of every other query row.
+          const int odd = lane & 1;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int64_t to = sh.to[q + i];
-            const float f = sh.factor[q + i];
-            if (to >= 0) {
-              unsigned char* const out = p.out + to + tid * 2;
+          for (int i = 0; i < 16; i += 2) {
+            const int64_t to = sh.to[q + i + odd];
+            const float fa = sh.factor[q + i], fb = sh.factor[q + i + 1];
+            unsigned char* const out = p.out + to + (tid & ~1) * 2;
 #pragma unroll
-              for (int g = 0; g < kQuarters; ++g) attn_store<kIn>(out + g * 256, __uint_as_float(o[g][i]) * f);
+            for (int g = 0; g < kQuarters; ++g) {
+              const float a = __uint_as_float(o[g][i]) * fa, b = __uint_as_float(o[g][i + 1]) * fb;
+              const float got = __shfl_xor_sync(kFullMask, odd ? a : b, 1);
+              if (to >= 0)
+                *reinterpret_cast<uint32_t*>(out + g * 256) = pack2<kIn == HS_DT_BF16>(odd ? got : a, odd ? b : got);
             }
           }
         } else {
@@ -619,7 +635,13 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
         return r;
       };
       int32_t row = find();
-      for (uint32_t n = 0; more; ++n) {
+      for (uint32_t n = 0, u_n = 0; more; ++n) {
+        if (k == w.k0) {
+          // ---- a unit's queries, whose place is free once the last unit's last scores are there
+          if (!wait_all(&sh.q_empty, (u_n & 1) ^ 1)) break;
+          send_queries(w);
+          finish_queries(u_n++);
+        }
         // ---- codes into the second panel of the quarter, 128 bytes a row, as soon as
         // the last tile's values are used
         if (!wait_all(&sh.empty[g], (n & 1) ^ 1)) break;
@@ -772,6 +794,8 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
             __syncwarp();
           }
           if constexpr (kApart) commit(&sh.empty[4]);
+          if constexpr (kCodes)
+            if (k + 1 == w.k1) commit(&sh.q_empty);
           commit(&sh.s_full);
           if (!(ok = reached(&sh.p_full, n & 1))) break;
           const uint32_t b = mma_desc_lo(weights, kPanel);
