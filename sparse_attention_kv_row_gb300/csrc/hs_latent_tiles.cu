@@ -75,9 +75,9 @@ constexpr bool room_apart(bool codes, int n) { return codes && n <= 32; }
 // Registers over codes: of the launch, and of the warpgroups after they have shared them
 // out (softmax, four that convert, one of the products).
 constexpr uint32_t kLaunchRegs = 80;
-constexpr uint32_t softmax_regs(int n) { return n == 64 ? 208 : 128; }
+constexpr uint32_t softmax_regs(int n) { return n == 64 ? 208 : 136; }
 constexpr uint32_t convert_regs(int n) { return n == 64 ? 56 : 72; }
-constexpr uint32_t product_regs(int n) { return n == 64 ? 48 : 64; }
+constexpr uint32_t product_regs(int n) { return n == 64 ? 48 : 56; }
 static_assert(softmax_regs(64) + 4 * convert_regs(64) + product_regs(64) <= 6 * kLaunchRegs &&
                   softmax_regs(32) + 4 * convert_regs(32) + product_regs(32) <= 6 * kLaunchRegs,
               "what the block was launched with");
@@ -232,13 +232,6 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t c, uint32_t hi, uint32_
       : "r"(c), "r"(hi), "r"(lo));
   return r;
 }
-// Floats as whole numbers of the same order (NaN aside), and back.
-__device__ __forceinline__ int ordered(float x) {
-  const int b = __float_as_int(x);
-  return b ^ (b >> 31 & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b ^ (b >> 31 & 0x7FFFFFFF)); }
-
 // N columns of a warp's 32 lanes of tensor memory.
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t (&r)[N], uint32_t addr) {
@@ -248,6 +241,32 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t (&r)[N], uint32_t addr) {
     static_assert(N == 32, "16 or 32 columns");
     tmem_ld32(r, addr);
   }
+}
+
+// Folds N values of every lane over the 32 lanes, each step leaving half the values to half the
+// lanes (62 shuffles for 64 values, 320 one value at a time): lane i then has the values
+// i N / 32 (and the next, for 64; 16 values go to two lanes each) of the warp in `to`.
+template <int N, class Op>
+__device__ __forceinline__ void fold_lanes(const float (&v)[N], float* to, int lane, Op op) {
+  float r[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const bool up = lane & 16;
+    r[i] = op(up ? v[i + N / 2] : v[i], __shfl_xor_sync(kFullMask, up ? v[i] : v[i + N / 2], 16));
+  }
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) {
+    const int n = N * d / 32;
+    const bool up = lane & d;
+    if (n == 0) r[0] = op(r[0], __shfl_xor_sync(kFullMask, r[0], d));
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      r[i] = op(up ? r[i + n] : r[i], __shfl_xor_sync(kFullMask, up ? r[i] : r[i + n], d));
+  }
+  if constexpr (N == 64)
+    *reinterpret_cast<float2*>(to + lane * 2) = make_float2(r[0], r[1]);
+  else
+    to[lane * N / 32] = r[0];
 }
 
 template <int kIn, bool kCodes, int N>
@@ -450,16 +469,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
         if (kCodes) over |= mine > norm;
         if (group_any(over) || fresh) {
           // ---- new reference points: where they are exceeded, and where there are none yet
-#pragma unroll
-          for (int q = 0; q < N; q += kStep) {
-            int mine_most = 0;
-#pragma unroll
-            for (int i = 0; i < kStep; ++i) {
-              const int most = __reduce_max_sync(kFullMask, ordered(z[q + i]));
-              if (lane == i) mine_most = most;
-            }
-            if (lane < kStep) sh.most[warp][q + lane] = from_ordered(mine_most);
-          }
+          fold_lanes(z, sh.most[warp], lane, [](float x, float y) { return fmaxf(x, y); });
           const uint32_t sm = __reduce_max_sync(kFullMask, mine > 0.f ? __float_as_uint(mine) : 0u);
           if (lane == 0) sh.scale_most[warp] = sm;
           group_sync();
@@ -547,12 +557,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
       more = w.next(prefix, p);
       if (!kCodes && more) send_queries(w);
       // ---- sums over the rows, 32 lanes and 4 warps
-#pragma unroll
-      for (int h = 0; h < N; ++h) {
-#pragma unroll
-        for (int d = kWarp / 2; d > 0; d >>= 1) l[h] += __shfl_xor_sync(kFullMask, l[h], d);
-        if (lane == (h & 31)) sh.most[warp][h] = l[h];
-      }
+      fold_lanes(l, sh.most[warp], lane, [](float x, float y) { return x + y; });
       group_sync();
       float* part = ws.slots + static_cast<int64_t>(2 * me + (from_start ? 1 : 0)) * slot_floats(N);
       if (tid < N) {
