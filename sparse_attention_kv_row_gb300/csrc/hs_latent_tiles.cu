@@ -21,9 +21,10 @@
 // more than 2^8 above what it was; sums are in fp32, of unrounded weights.
 //
 // Roles: a warpgroup for the softmax and the outputs (a thread a row, then a thread a
-// dim; it also brings in the next unit's queries), a warp that issues the products, and
-// those that bring in rows: 16 warps that copy codes into a panel and turn them into fp16
-// in place, or three that issue tensor-map loads of 16-bit rows.  A quarter of a tile is
+// dim; over 16-bit rows it also brings in the next unit's queries), a warp that issues the
+// products, and those that bring in rows: 16 warps that copy codes into a panel and turn
+// them into fp16 in place, and bring in queries between two units (64 rows by the softmax's
+// warps took 10 us there), or three that issue tensor-map loads of 16-bit rows.  A quarter of a tile is
 // handed over as soon as it is there, and filled again as soon as its values are used;
 // the rows of the tile behind it are brought into L2 meanwhile.
 //
@@ -34,8 +35,8 @@
 // What bounds it: the chain of a tile (its rows come in, four times the keys' product with
 // what has come, softmax, four times the values' product, and only then room for the next
 // rows), behind a start of some 8 us.  One unit an SM over codes takes, for 1, 2, 4, 8 and
-// 16 tiles, 13.0, 17.2, 25.6, 43.8 and 81.0 us with 16 query rows and 23.2, 30.0, 44.2,
-// 80.6 and 141.5 us with 64: 4.6 and 7.6 us a tile, 2.5 TB/s of rows and 0.31 PFLOP/s at
+// 16 tiles, 12.8, 16.9, 25.5, 43.9 and 81.1 us with 16 query rows and 16.4, 22.6, 35.2,
+// 69.4 and 124.5 us with 64: 4.7 and 6.9 us a tile, 2.5 TB/s of rows and 0.35 PFLOP/s at
 // 16 tiles.  Nothing is full then (memory to 2.6 of 6.8 TB/s, shared memory to 37 %, the
 // tensor cores to 22 %, the issue of instructions to 31 %): the chain takes the time.
 // Measured against it, at 16 tiles: 16 query rows by 32 latent rows on mma.sync, eight warps
@@ -75,6 +76,7 @@ constexpr bool room_apart(bool codes, int n) { return codes && n <= 32; }
 // Registers over codes: of the launch, and of the warpgroups after they have shared them
 // out (softmax, four that convert, one of the products).
 constexpr uint32_t kLaunchRegs = 80;
+// Fewer spilled registers for 64 query rows came from the converting warps (56, not 64).
 constexpr uint32_t softmax_regs(int n) { return n == 64 ? 208 : 136; }
 constexpr uint32_t convert_regs(int n) { return n == 64 ? 56 : 72; }
 constexpr uint32_t product_regs(int n) { return n == 64 ? 48 : 56; }
@@ -1001,7 +1003,7 @@ TilesKernels pick(int in_dtype, bool codes, int n) {
 }
 
 // Query rows of a unit: as many as there are, up to 64, since every unit reads its latent rows
-// again (142 us for 64 at once over 16 tiles, four times 81 for 16 at a time); 32 where
+// again (125 us for 64 at once over 16 tiles, four times 81 for 16 at a time); 32 where
 // the batch's running sums would not fit beside 64.
 int unit_rows(const LatentParams& p) {
   const int64_t rows = static_cast<int64_t>(p.heads) * (p.indexed ? 1 : p.max_q);
