@@ -825,8 +825,8 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  * value.  Other calls hold everything in fp32.
  * A bounded wait inside a kernel that runs out (it cannot, short of a fault) ends the call
  * and sets HS_ST_TIMEOUT in every status word; out and lse are then not to be used.
- * Limits: R <= 512, rope_dim <= 256, batch <= 2048, num_rows, n_tokens, top_k and
- * max_q_len * num_heads < 2^31, R a multiple of 128 for HS_ROW_E4M3, which wants
+ * Limits: R <= 512, rope_dim <= 256, batch <= 2048, top_k <= 2^30, num_rows, n_tokens
+ * and max_q_len * num_heads < 2^31, R a multiple of 128 for HS_ROW_E4M3, which wants
  * 16-bit types (else HS_ERR_UNSUPPORTED).  Sequence lengths: up to 2^30, and as long as
  * the tiles of 128 rows that all query heads and tokens might see, 64 query rows a unit,
  * are fewer than 2^31 (HS_ST_BAD_STATE beyond).

@@ -138,10 +138,10 @@ hs_err check_args(const hs_latent_attention_args* a) {
     return fail(HS_ERR_UNSUPPORTED, "%s: rows of codes want 16-bit inputs and latent_dim a "
                                     "multiple of %d", who, kLatentGroup);
   if (a->latent_dim > kMaxLatent || a->rope_dim > kMaxRope || a->batch > kAttnMaxBatch ||
-      a->n_tokens > INT32_MAX || a->num_rows > INT32_MAX ||
+      a->n_tokens > INT32_MAX || a->num_rows > INT32_MAX || a->top_k > 1 << 30 ||
       (!indexed && static_cast<int64_t>(a->max_q_len) * a->num_heads > INT32_MAX))
-    return fail(HS_ERR_UNSUPPORTED, "%s: latent_dim <= %d, rope_dim <= %d, batch <= %d, n_tokens, "
-                                    "num_rows and max_q_len * num_heads <= INT32_MAX", who,
+    return fail(HS_ERR_UNSUPPORTED, "%s: latent_dim <= %d, rope_dim <= %d, batch <= %d, top_k <= "
+                                    "2^30, n_tokens, num_rows and max_q_len * num_heads <= INT32_MAX", who,
                 kMaxLatent, kMaxRope, kAttnMaxBatch);
   const int64_t esz = a->in_dtype == HS_DT_F32 ? 4 : 2;
   const int64_t bytes = (codes ? a->latent_dim + a->latent_dim / kLatentGroup * 4 : a->latent_dim * esz) +

@@ -209,6 +209,22 @@ def test_nothing_to_see(hs, dev, dtype, fmt):
     a.indexed(2, 5, 10, empty=[0, 1]).check(hs, dev, "general", rows=a.rows[:0].to(dev))
 
 
+@pytest.mark.parametrize("dtype,fmt,kind", [(*t, "tiles") for t in TYPES] + [("f32", "same", "general")])
+def test_more_new_tokens_than_rows(hs, dev, dtype, fmt, kind):
+    """The first tokens of a request that is shorter than what is new of it see nothing."""
+    a = LatentInputs(heads=16, dtype=dtype, fmt=fmt, seed=10)
+    a.paged([(-3, 5), (10, 2), (-4, 4), (-1, 140)], 16).check(hs, dev, kind)
+
+
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+def test_rows_listed_twice(hs, dev, dtype, fmt):
+    a = LatentInputs(heads=7, dtype=dtype, fmt=fmt, seed=11).indexed(3, 290, 600)
+    a.index[0] = np.repeat(a.index[0, :29], 10)
+    a.index[2, 1:200:2] = a.index[2, 0:199:2]
+    a.lists = [[int(e) for e in row if e >= 0] for row in a.index]
+    a.check(hs, dev, "tiles")
+
+
 # ------------------------------------------------------------------ streams, graphs, workspaces
 @pytest.mark.parametrize("fmt", ["fp8", "same"])
 @pytest.mark.parametrize("heads", [16, 64])

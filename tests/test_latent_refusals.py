@@ -100,7 +100,7 @@ INDEX = dict(flags=4, batch=0, row_index=4096, row_index_stride=8, top_k=8)
     (dict(row_stride=655), 1), (dict(row_stride=658), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(rows=None), 1),
     (dict(cu_q=None), 1), (dict(block_table=None), 1), (dict(q=4097), 1),
     (INDEX | dict(batch=1), 1), (INDEX | dict(row_index=None), 1), (INDEX | dict(row_index_stride=7), 1),
-    (INDEX | dict(top_k=-1), 1),
+    (INDEX | dict(top_k=-1), 1), (INDEX | dict(top_k=(1 << 30) + 1, row_index_stride=1 << 31), 2),
 ])
 def test_latent_attention(lib, kw, code):
     assert lib.hs_latent_attention(C.byref(_attn(**kw)), None) == code
