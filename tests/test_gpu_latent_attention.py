@@ -188,7 +188,7 @@ def test_rows_past_32_bits(hs, dev, fmt, n):
         assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("heads,batch", [(64, 1100), (16, 2048)])
+@pytest.mark.parametrize("heads,batch", [(64, 1024), (64, 1100), (16, 2048)])
 def test_many_requests(hs, dev, heads, batch):
     a = LatentInputs(heads=heads, dtype="bf16", fmt="fp8", seed=6)
     a.paged([(i % 7, 1) if i % 11 else (None, 0) for i in range(batch)], 4, gap=1).check(hs, dev, "tiles")
@@ -306,6 +306,29 @@ def test_captured(hs, dev, fmt, keep):
         torch.cuda.synchronize()
         assert bool((out[a.T:] == -7).all()) and bool((lse[a.T:] == -7).all())
         a.compare(out[: a.T], lse[: a.T], status, "tiles")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "same"])
+def test_graphs_that_share_a_workspace(hs, dev, fmt):
+    """Replayed in turn in one stream: what one left in the workspace is nothing to the other."""
+    two = [LatentInputs(heads=h, dtype="bf16", fmt=fmt, seed=40 + h).indexed(t, k, 2 * k) for h, t, k in
+           ((64, 9, 900), (16, 3, 2000))]
+    alone = [a.check(hs, dev, "tiles")[0] for a in two]
+    t = [(a.q.to(dev), a.rows.to(dev), torch.from_numpy(a.index).to(dev)) for a in two]
+    outs = [torch.zeros_like(x) for x in alone]
+    n = max(hs.latent_attention_workspace_bytes(*x, o) for x, o in zip(t, outs))
+    space = torch.full((n,), 0xFF, dtype=torch.uint8, device=dev)
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            hs.latent_attention(*t[i], outs[i], scale=two[i].scale, workspace=space)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], alone[i])
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "same"])
