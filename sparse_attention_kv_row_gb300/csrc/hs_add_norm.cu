@@ -82,6 +82,14 @@ __global__ void __launch_bounds__(kWarpRow ? kWarpRows * kWarp : 1024)
     r[i] = make_uint4(0, 0, 0, 0);
     if (c < chunks) r[i] = ld_once_v4(x + c * 16);
   }
+  uint4 weight[kC];  // on its way beside the token's values
+  if (p.weight != nullptr) {
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int c = i * threads + me;
+      if (c < chunks) weight[i] = __ldg(reinterpret_cast<const uint4*>(p.weight) + c);
+    }
+  }
   if (p.residual != nullptr) {
     const unsigned char* res = p.residual + t * p.res_row;
     uint4 add[kC];
@@ -136,7 +144,7 @@ __global__ void __launch_bounds__(kWarpRow ? kWarpRows * kWarp : 1024)
     unpack<kDtype>(r[i], y[i]);
     float w[E];
     if (p.weight != nullptr && c < chunks) {
-      unpack<kDtype>(__ldg(reinterpret_cast<const uint4*>(p.weight) + c), w);
+      unpack<kDtype>(weight[i], w);
     } else {
 #pragma unroll
       for (int j = 0; j < E; ++j) w[j] = 1.f;
