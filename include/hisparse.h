@@ -677,8 +677,8 @@ hs_err hs_paged_attention_timeout_selftest(const hs_paged_attention_args* args,
  * The sum is rounded to the inputs' type first, so that y belongs to the residual
  * stream that the next layers read; everything else is held in fp32 and rounded
  * once.  A NaN in a token makes all its y NaN, an infinity its own (the others become
- * zeros); a group that holds a NaN has NaN for scale and codes.  Defined by this library, beside hs_qk_norm_rope_store
- * (the norm) and hs_fp8_store_kv (the codes).
+ * zeros); a group that holds a NaN has NaN for scale and codes.  Defined by this
+ * library, beside hs_qk_norm_rope_store (the norm) and hs_fp8_store_kv (the codes).
  *
  *  x, residual, residual_out, out  dtype (HS_DT_F32 / F16 / BF16) [n_tokens, dim],
  *              strides in elements, dims contiguous.  residual_out may be residual
@@ -823,13 +823,15 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  * or 2^-25, and so counts in scores and outputs alike; a bf16 query's latent dims are
  * taken as fp16 over a power of two of the query row, exact within 2^-22 of its largest
  * value.  Other calls hold everything in fp32.
- * A bounded wait inside a kernel that runs out (it cannot, short of a fault) ends the call
- * and sets HS_ST_TIMEOUT in every status word; out and lse are then not to be used.
+ * Time-out: the waits of the tensor-core kernel are bounded.  If one runs out (the GPU did
+ * not complete a copy or a product within two seconds), every status word reports
+ * HS_ST_TIMEOUT and the outputs of the call are undefined; treat the context as suspect.
  * Limits: R <= 512, rope_dim <= 256, batch <= 2048, top_k <= 2^30, num_rows, n_tokens
  * and max_q_len * num_heads < 2^31, R a multiple of 128 for HS_ROW_E4M3, which wants
- * 16-bit types (else HS_ERR_UNSUPPORTED).  Sequence lengths: up to 2^30, and as long as
- * the tiles of 128 rows that all query heads and tokens might see, 64 query rows a unit,
- * are fewer than 2^31 (HS_ST_BAD_STATE beyond).
+ * 16-bit types (else HS_ERR_UNSUPPORTED); L at most 2^30, and so short that 32-bit whole
+ * numbers count the batch's tiles: with u = max(1, floor(16 / num_heads)) tokens a unit,
+ * (n_tokens / u + batch) * ceil(num_heads / 32) * (L + 512) <= 2^38 - 128 is enough
+ * (HS_ST_BAD_STATE for a longer row).
  */
 #define HS_LATENT_INDEX 4 /* beside HS_SEQ_LENS_I64 and HS_REQ_STATE_I64 in flags */
 typedef struct hs_latent_attention_args {
