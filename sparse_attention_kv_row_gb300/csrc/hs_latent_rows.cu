@@ -6,7 +6,7 @@
 // HBM bandwidth; a token's angles (4 rope_dim bytes) come from L1 after the first use.
 //
 // latent_rows_lanes: 16-bit types, 64 rotary dims, latents of 256 to 1024 in steps of
-// 256.  A warp takes a token's latent (chunk c of 16 bytes in lane c mod 32, so that a
+// 256 (over codes of 512, where the rotary values begin on 16 bytes).  A warp takes a token's latent (chunk c of 16 bytes in lane c mod 32, so that a
 // group of 128 lies in 16 lanes) with its rotary key in the first four lanes, or up to
 // 16 of its query heads, four lanes a head; such a lane holds both halves of every pair
 // that it turns.
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kRowThreads) latent_rows_lanes(const LatentRow
   }
   unsigned char* row = p.rows + loc * p.row_stride;
   constexpr int kLatent = kC * 256;
+  static_assert(!kCodes || (kLatent + kLatent / kGroup * 4) % 16 == 0, "rotary values on 16 bytes");
   float y[kC][8];
 #pragma unroll
   for (int i = 0; i < kC; ++i) unpack<kDtype>(x[i], y[i]);
@@ -287,10 +288,11 @@ __global__ void __launch_bounds__(kRowThreads) latent_rows_general(const LatentR
 using RowsFn = void (*)(const LatentRowsParams);
 template <int kDtype, bool kCodes, bool kInter>
 RowsFn lanes_of(int per) {
-  return per == 1   ? latent_rows_lanes<kDtype, kCodes, kInter, 1>
-         : per == 2 ? latent_rows_lanes<kDtype, kCodes, kInter, 2>
-                    : (per == 3 ? latent_rows_lanes<kDtype, kCodes, kInter, 3>
-                                : latent_rows_lanes<kDtype, kCodes, kInter, 4>);
+  if constexpr (!kCodes) {
+    if (per == 1) return latent_rows_lanes<kDtype, kCodes, kInter, 1>;
+    if (per == 3) return latent_rows_lanes<kDtype, kCodes, kInter, 3>;
+  }
+  return per == 2 ? latent_rows_lanes<kDtype, kCodes, kInter, 2> : latent_rows_lanes<kDtype, kCodes, kInter, 4>;
 }
 template <int kDtype>
 RowsFn rows_of(bool lanes, bool codes, bool inter, int per) {
@@ -386,7 +388,9 @@ extern "C" hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* a, hs_str
   if (heads > 0)
     al |= static_cast<uintptr_t>(p.q_token) | static_cast<uintptr_t>(p.q_head) |
           static_cast<uintptr_t>(p.out_token) | static_cast<uintptr_t>(p.out_head);
-  const bool lanes = esz == 2 && a->rope_dim == 64 && a->latent_dim % 256 == 0 && al % 16 == 0;
+  // (latent_bytes: where a row's rotary values begin, in chunks of 16 bytes as well)
+  const bool lanes = esz == 2 && a->rope_dim == 64 && a->latent_dim % 256 == 0 && al % 16 == 0 &&
+                     latent_bytes % 16 == 0;
   const int per_unit = kHeadsAtOnce * kHeadRounds;
   const uint32_t per_token =
       1 + static_cast<uint32_t>(lanes ? (heads + per_unit - 1) / per_unit : heads);

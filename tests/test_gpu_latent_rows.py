@@ -129,6 +129,15 @@ def test_alignment(dev):
     run(dev, 9, 3, "f16", "same", pad=1, shift=3)
 
 
+@pytest.mark.parametrize("R,pad", [(256, 8), (256, 56), (768, 8), (768, 24), (512, 16), (1024, 16)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_padded_rows_of_codes(dev, R, pad, dtype):
+    """Rows that begin on 16 bytes; their rotary values do so for multiples of 512 only."""
+    assert (row_bytes(R, 64) + pad) % 16 == 0
+    run(dev, 9, 5, dtype, "fp8", R=R, pad=pad)
+    run(dev, 9, 0, dtype, "fp8", R=R, pad=pad, inter=True)
+
+
 def test_options(dev):
     run(dev, 9, 4, "bf16", "fp8", pow2=True)
     run(dev, 9, 4, "bf16", "fp8", weight=False, rotate=False)
