@@ -819,10 +819,12 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  * q, out and rows are multiples of 16.  There the weights are rounded to the type of the
  * values before their product with them (the sums that they are divided by are not).
  * Over codes that type is fp16: a value becomes code * scale / 2^e, with 2^e the power of
- * two not below the row's largest scale (within 2^-100 .. 2^125), half a step of fp16 off
- * or 2^-25, and so counts in scores and outputs alike; a bf16 query's latent dims are
- * taken as fp16 over a power of two of the query row, exact within 2^-22 of its largest
- * value.  Other calls hold everything in fp32.
+ * two not below the row's largest scale (within 2^-80 .. 2^113), half a step of fp16 off
+ * or 2^-25, and so counts in scores and outputs alike; a weight times 2^e is kept over a
+ * power of two of its token and head, half a step off or 2^-30 of the largest such product;
+ * a bf16 query's latent dims are taken as fp16 over a power of two of the query row, exact
+ * within 2^-22 of its largest value.  Weights below 2^-126 of the largest are 0.  Other
+ * calls hold everything in fp32.
  * Time-out: the waits of the tensor-core kernel are bounded.  If one runs out (the GPU did
  * not complete a copy or a product within two seconds), every status word reports
  * HS_ST_TIMEOUT and the outputs of the call are undefined; treat the context as suspect.

@@ -15,10 +15,13 @@
 //
 // Codes become fp16 times the row's scales, each divided by a power of two 2^e of the
 // row (at least its largest scale): half a step of fp16 of every value.  2^e goes to the
-// row's scores (a thread has one row, all query rows) and, over a running power of two
-// of the unit, to its weights.  The rotary dims have a product of their own then, in
-// their own type.  The running maximum is only raised, and O rescaled, when a score is
-// more than 2^8 above what it was; sums are in fp32, of unrounded weights.
+// row's scores (a thread has one row, all query rows) and to its weights.  The rotary dims
+// have a product of their own then, in their own type.  The running maximum is only raised,
+// and O rescaled, when a score is more than 2^8 above what it was; sums are in fp32, of
+// unrounded weights.  Over codes every query row has a second running power of two, that of
+// its largest weight times 2^e: O is kept relative to it, so that the fp16 weights of a
+// query row keep 2^-30 of its own largest share, and rows that it does not see, or that
+// have no weight, change no bit of it however large their scales are.
 //
 // Roles: a warpgroup for the softmax and the outputs (a thread a row, then a thread a
 // dim; over 16-bit rows it also brings in the next unit's queries), a warp that issues the
@@ -76,15 +79,16 @@ constexpr bool room_apart(bool codes, int n) { return codes && n <= 32; }
 // Registers over codes: of the launch, and of the warpgroups after they have shared them
 // out (softmax, four that convert, one of the products).
 constexpr uint32_t kLaunchRegs = 80;
-// Fewer spilled registers for 64 query rows came from the converting warps (56, not 64).
-constexpr uint32_t softmax_regs(int n) { return n == 64 ? 208 : 136; }
+// 216, 56 and 40 for 64 query rows spill none (208, 56 and 48 did: 2 % slower in chunks).
+constexpr uint32_t softmax_regs(int n) { return n == 64 ? 216 : 136; }
 constexpr uint32_t convert_regs(int n) { return n == 64 ? 56 : 72; }
-constexpr uint32_t product_regs(int n) { return n == 64 ? 48 : 56; }
+constexpr uint32_t product_regs(int n) { return n == 64 ? 40 : 56; }
 static_assert(softmax_regs(64) + 4 * convert_regs(64) + product_regs(64) <= 6 * kLaunchRegs &&
                   softmax_regs(32) + 4 * convert_regs(32) + product_regs(32) <= 6 * kLaunchRegs,
               "what the block was launched with");
-constexpr float kNoScale = 0x1p-100f;      // 2^e of a row of zeros
+constexpr float kNoScale = 0x1p-80f;       // 2^e of a row of zeros, and the least there is
 constexpr float kRaise = 8.f;             // log2 of how far weights may exceed their reference
+constexpr float kF16Bias = 6.f;           // log2 of that reference in fp16: what is 2^-30 of it stays
 // A unit's fixed cost (its queries, its outputs) in tiles.  Counted as 1, 2, 3 and 4 it makes a
 // batch of chunks take 110, 95, 87 and 89 us, others within 3 % of each other.
 constexpr int kUnitCost = 3;
@@ -201,11 +205,13 @@ struct alignas(16) Shared {
   alignas(16) float undo[2][N];  // what undoes the factors of the queries
   alignas(16) float ref[N];      // what scores are taken relative to, negated
   alignas(16) float factor[N];   // what rescales O; then what outputs are multiplied by
+  alignas(16) float share[N];    // over codes: weights are stored as w * 2^e * share, a power of two
+  float reach;                   // log2 of the largest share
   alignas(16) float most[4][N];  // per warp: largest scores, then sums
+  float shares[4][N];            // per warp: largest weights times 2^e (as powers)
   float row_scale[kKeys];        // 2^e, or -1 for a row that nobody sees
   int64_t to[N];                 // a query row's output's byte, -1: none
   uint64_t q_full, q_empty, full[5], empty[5], s_full, p_full, o_done, drain;
-  uint32_t scale_most[4];
   int vis[N];                    // rows [0, vis) that a query row sees; 0: no query row
   bool started[N];               // a query row has met a row that it sees
   uint32_t tmem;
@@ -214,6 +220,10 @@ struct alignas(16) Shared {
 static_assert(offsetof(Shared<16>, ref) % 16 == 0 && offsetof(Shared<32>, undo[1]) % 16 == 0 &&
                   offsetof(Shared<64>, to) % 8 == 0, "alignment of vector reads");
 
+// Of a power of two in fp32's normal range.
+__device__ __forceinline__ float log2_of(float x) {
+  return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127);
+}
 __device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool group_any(bool x) {
   uint32_t r;
@@ -248,13 +258,14 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t (&r)[N], uint32_t addr) {
 // Folds N values of every lane over the 32 lanes, each step leaving half the values to half the
 // lanes (62 shuffles for 64 values, 320 one value at a time): lane i then has the values
 // i N / 32 (and the next, for 64; 16 values go to two lanes each) of the warp in `to`.
-template <int N, class Op>
-__device__ __forceinline__ void fold_lanes(const float (&v)[N], float* to, int lane, Op op) {
+// `take` is what a lane does to its values first.
+template <int N, class Take, class Op>
+__device__ __forceinline__ void fold_lanes(const float (&v)[N], float* to, int lane, Take take, Op op) {
   float r[N / 2];
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
     const bool up = lane & 16;
-    r[i] = op(up ? v[i + N / 2] : v[i], __shfl_xor_sync(kFullMask, up ? v[i] : v[i + N / 2], 16));
+    r[i] = op(take(up ? v[i + N / 2] : v[i]), __shfl_xor_sync(kFullMask, take(up ? v[i] : v[i + N / 2]), 16));
   }
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) {
@@ -289,8 +300,8 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
   constexpr int kO = 2 * N, kK = 6 * N;
   constexpr uint32_t kCols = kApart || N == 64 ? 512 : (N == 16 ? 128 : 256);
   static_assert(kK + (kApart ? kLatent / 2 : 0) <= kCols, "tensor memory");
-  // fp16 weights reach 2^(6 + 8) and keep what is 2^-30 of the reference.
-  constexpr float kBias = kBf16 ? 0.f : 6.f;
+  // fp16 weights reach 2^(6 + 8); over codes they have a reference of their own.
+  constexpr float kBias = kBf16 || kCodes ? 0.f : kF16Bias;
   constexpr int kStep = N < 32 ? N : 32;  // columns read at once
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -389,6 +400,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
     if constexpr (kCodes) regs_grow<softmax_regs(N)>();
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const float s2 = p.softmax_scale * kLog2e;
+    const auto as_is = [](float x) { return x; };
     uint32_t n = 0, u_n = 0;  // tiles and units so far
     bool ok = true, more = w.seek(c0, c1, prefix, p);
     if (!kCodes && more) {
@@ -407,12 +419,13 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
                           : -1;
         sh.ref[tid] = kBias;
         sh.started[tid] = sh.vis[tid] == 0;
+        sh.share[tid] = 0.f;  // none yet
+        sh.reach = -INFINITY;
       }
       const int all_end = latent_end(p, w.row, w.unit.i0);  // rows that every query row sees
       float l[N];
 #pragma unroll
       for (int h = 0; h < N; ++h) l[h] = 0.f;
-      float norm = 0.f;   // a power of two that no row's 2^e so far exceeds
       bool fresh = true;  // some query row has not met a row that it sees
       group_sync();
       for (int k = w.k0; k < w.k1; ++k, ++n) {
@@ -463,38 +476,36 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
           for (int h = 0; h < N; ++h)
             if (mine < 0.f || j >= sh.vis[h]) z[h] = -INFINITY;
         }
+        const float e = kCodes ? log2_of(mine) : 0.f;
         float top = z[0];
 #pragma unroll
         for (int h = 1; h + 1 < N; h += 2) top = fmaxf(top, fmaxf(z[h], z[h + 1]));
         top = fmaxf(top, z[N - 1]);
         bool over = top > kRaise + kBias;
-        if (kCodes) over |= mine > norm;
+        if (kCodes) over |= top + e + sh.reach > kRaise + kF16Bias;
         if (group_any(over) || fresh) {
-          // ---- new reference points: where they are exceeded, and where there are none yet
-          fold_lanes(z, sh.most[warp], lane, [](float x, float y) { return fmaxf(x, y); });
-          const uint32_t sm = __reduce_max_sync(kFullMask, mine > 0.f ? __float_as_uint(mine) : 0u);
-          if (lane == 0) sh.scale_most[warp] = sm;
+          // ---- new reference points: where they are exceeded, and where there are none yet.
+          // Each query row's are its own affair: another's leave its bits alone.
+          const auto larger = [](float x, float y) { return fmaxf(x, y); };
+          const auto of_warps = [&](const float (&x)[4][N]) {
+            return fmaxf(fmaxf(x[0][tid], x[1][tid]), fmaxf(x[2][tid], x[3][tid]));
+          };
+          fold_lanes(z, sh.most[warp], lane, as_is, larger);
           group_sync();
-          float back = 1.f;
-          if constexpr (kCodes) {
-            const float to = __uint_as_float(max(max(max(sh.scale_most[0], sh.scale_most[1]),
-                                                     max(sh.scale_most[2], sh.scale_most[3])), 0x0D800000u));
-            if (to > norm) {
-              back = norm / to;
-              norm = to;
-            }
-          }
-          bool waits = false;
+          bool waits = false, first = false;
+          float by = 0.f;
           if (tid < N) {
-            const float most = fmaxf(fmaxf(sh.most[0][tid], sh.most[1][tid]), fmaxf(sh.most[2][tid], sh.most[3][tid]));
-            float up = 0.f, f = 1.f;
-            if (most > kRaise + kBias || (!sh.started[tid] && most > -INFINITY)) {
-              up = most - kBias;
-              f = sh.started[tid] ? fast_exp2(-up) : 0.f;
+            const float most = of_warps(sh.most);
+            float f = 1.f;
+            first = !sh.started[tid];
+            if (most > kRaise + kBias || (first && most > -INFINITY)) {
+              by = kCodes ? ceilf(most) : most - kBias;
+              f = first ? 0.f : fast_exp2(-by);
               sh.started[tid] = true;
             }
-            sh.most[0][tid] = up;
+            sh.most[0][tid] = by;
             sh.factor[tid] = f;
+            sh.ref[tid] -= by;  // (everyone has read this tile's)
             waits = !sh.started[tid];
           }
           fresh = group_any(waits);
@@ -505,7 +516,34 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
             z[h] -= up.x, z[h + 1] -= up.y, z[h + 2] -= up.z, z[h + 3] -= up.w;
             l[h] *= f.x, l[h + 1] *= f.y, l[h + 2] *= f.z, l[h + 3] *= f.w;
           }
-          if (k > w.k0) {
+          bool rescale = true;
+          if constexpr (kCodes) {
+            // The same for the weights times 2^e, whose unit a new maximum leaves as it is.
+            fold_lanes(z, sh.shares[warp], lane, [&](float x) { return x + e; }, larger);
+            group_sync();  // (the factors of the sums are read, too)
+            float f = 1.f;
+            if (tid < N) {
+              const float most = of_warps(sh.shares);
+              float share = log2_of(sh.share[tid]) + by;
+              if (most > -INFINITY && (first || most + share > kRaise + kF16Bias)) {
+                const float to = kF16Bias - ceilf(most);
+                f = first ? 0.f : fast_exp2(to - share);
+                share = to;
+              }
+              sh.factor[tid] = f;
+              if (sh.started[tid] && sh.vis[tid] > 0)
+                sh.share[tid] = __int_as_float((static_cast<int>(fminf(fmaxf(share, -126.f), 127.f)) + 127) << 23);
+            }
+            rescale = group_any(f != 1.f);
+            if (warp == 0) {
+              float largest = 0.f;
+#pragma unroll
+              for (int h = lane; h < N; h += kWarp) largest = fmaxf(largest, sh.share[h]);
+              const uint32_t bits = __reduce_max_sync(kFullMask, __float_as_uint(largest));
+              if (lane == 0 && bits != 0) sh.reach = log2_of(__uint_as_float(bits));
+            }
+          }
+          if (rescale && k > w.k0) {
             // O is whole once the last tile's products are.
             ok = __all_sync(kFullMask, wait_for(&sh.o_done, (n - 1) & 1, dead));
             if (group_any(!ok)) {
@@ -521,20 +559,30 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
               tmem_pin(o);
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * (sh.factor[(q + i) % N] * back));
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.factor[(q + i) % N]);
               tmem_st16(tmem + lanes + kO + q, o);
             }
             tmem_wait_st();
           }
-          group_sync();
-          if (tid < N) sh.ref[tid] -= sh.most[0][tid];
-          group_sync();
+          if constexpr (!kCodes) group_sync();  // sh.most is written again
         }
         // ---- weights: a row of up to 64 query rows
-        const float kn = kCodes ? (mine > 0.f ? mine * (1.0f / norm) : 0.f) : 1.f;
+        // Times 2^e first: at least 2^-80 of a weight, at most 2^(113 + 8), is in fp32's range,
+        // and what falls below it is nothing beside the query row's largest.
+        const float to_e = fmaxf(mine, 0.f);
+        const uint64_t to_e2 = two_floats(to_e, to_e);
+        ulonglong2 own[2], then[2];  // shares, read a step ahead of the stores
+        auto read_shares = [&](ulonglong2 (&to)[2], int q) {
+          if constexpr (kCodes) {
+            to[0] = *reinterpret_cast<const ulonglong2*>(&sh.share[q]);
+            to[1] = *reinterpret_cast<const ulonglong2*>(&sh.share[q + 4]);
+          }
+        };
+        read_shares(own, 0);
 #pragma unroll
         for (int q = 0; q < N; q += 8) {
           uint32_t v[4];
+          if (q + 8 < N) read_shares(then, q + 8);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float e0 = fast_exp2(z[q + 2 * i]), e1 = fast_exp2(z[q + 2 * i + 1]);
@@ -542,9 +590,15 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
             l[q + 2 * i + 1] += e1;
             // The weights take the type of the values, as one product wants of its
             // operands: half a step off each, whose errors average out over the rows.
-            v[i] = kCodes ? pack2<false>(e0 * kn, e1 * kn) : pack2<kBf16>(e0, e1);
+            if constexpr (kCodes) {
+              const uint64_t y = mul2(mul2(two_floats(e0, e1), to_e2), i & 1 ? own[i / 2].y : own[i / 2].x);
+              v[i] = pack2<false>(low_float(y), high_float(y));
+            } else {
+              v[i] = pack2<kBf16>(e0, e1);
+            }
           }
           st_shared_v4(weights + in_panel(tid, q / 8), make_uint4(v[0], v[1], v[2], v[3]));
+          own[0] = then[0], own[1] = then[1];
         }
         fence_proxy_async_smem();  // the MMA reads through the async proxy
         tc_fence_before();
@@ -559,13 +613,13 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
       more = w.next(prefix, p);
       if (!kCodes && more) send_queries(w);
       // ---- sums over the rows, 32 lanes and 4 warps
-      fold_lanes(l, sh.most[warp], lane, [](float x, float y) { return x + y; });
+      fold_lanes(l, sh.most[warp], lane, as_is, [](float x, float y) { return x + y; });
       group_sync();
       float* part = ws.slots + static_cast<int64_t>(2 * me + (from_start ? 1 : 0)) * slot_floats(N);
       if (tid < N) {
         const float sum = (sh.most[0][tid] + sh.most[1][tid]) + (sh.most[2][tid] + sh.most[3][tid]);
         // A sum of 0 is that of a token without rows: zeros, and -inf.
-        sh.factor[tid] = sum == 0.f ? 0.f : (kCodes ? norm : 1.f) / sum;
+        sh.factor[tid] = sum == 0.f ? 0.f : (kCodes ? 1.0f / sh.share[tid] : 1.f) / sum;
         const float lse = log2f(sum) - sh.ref[tid];
         if (!whole) {
           part[N * kLatent + tid] = lse;
@@ -675,16 +729,16 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
         }
         cp_async_commit();
         // The row's 2^e, the power of two not below its largest scale, within what has a
-        // reciprocal; and this quarter's scale over it.
+        // reciprocal and leaves room for a weight; and this quarter's scale over it.
         float e = kNoScale, sc = 0.f;
         if (row >= 0) {
           const uint4 x = ld_stream_v4(p.rows + row * p.row_stride + kLatent);
           const uint32_t most = max(max(x.x & 0x7FFFFFFFu, x.y & 0x7FFFFFFFu), max(x.z & 0x7FFFFFFFu, x.w & 0x7FFFFFFFu));
-          e = __uint_as_float(min(max((most + 0x007FFFFFu) & 0x7F800000u, 0x0D800000u), 0x7E000000u));
+          e = __uint_as_float(min(max((most + 0x007FFFFFu) & 0x7F800000u, 0x17800000u), 0x78000000u));
           sc = __uint_as_float(g < 2 ? (g == 0 ? x.x : x.y) : (g == 2 ? x.z : x.w)) * (1.0f / e);
         }
         const uint32_t f = pack2<false>(sc, sc);
-        const float left = sc <= 1.f ? sc - __half2float(__ushort_as_half(f & 0xFFFFu)) : 0.f;  // (inf stays)
+        const float left = fabsf(sc) <= 32768.f ? sc - __half2float(__ushort_as_half(f & 0xFFFFu)) : 0.f;  // (inf stays)
         const uint32_t f_lo = pack2<false>(left, left);
         cp_async_wait_group<0>();
         __syncwarp();
@@ -1011,7 +1065,7 @@ int unit_rows(const LatentParams& p) {
   return rows <= 32 || (!p.indexed && p.batch > 1024) ? 32 : 64;
 }
 
-constexpr int kMostSmem = 232448 - 4608;  // of a block, less what is not dynamic
+constexpr int kMostSmem = 232448 - 5120;  // of a block, less what is not dynamic
 
 std::mutex g_mu;
 bool g_ready[64] = {false};
