@@ -818,9 +818,10 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  * rope_dim = 64 run on the tensor cores, where the addresses and strides in bytes of
  * q, out and rows are multiples of 16.  There the weights are rounded to the type of the
  * values before their product with them (the sums that they are divided by are not).
- * Over codes that type is fp16: a value becomes code * scale / 2^e, with 2^e the power of
- * two not below the row's largest scale (within 2^-80 .. 2^113), half a step of fp16 off
- * or 2^-25, and so counts in scores and outputs alike; a weight times 2^e is kept over a
+ * Over codes that type is fp16: a value becomes code * scale / 2^e, with 2^e a 128th of the
+ * power of two not below the row's largest scale (within 2^-80 .. 2^113), half a step of
+ * fp16 off or, in groups of far smaller scales, 2^-25 for each unit of the code and one
+ * more, and so counts in scores and outputs alike; a weight times 2^e is kept over a
  * power of two of its token and head, half a step off or 2^-30 of the largest such product;
  * a bf16 query's latent dims are taken as fp16 over a power of two of the query row, exact
  * within 2^-22 of its largest value.  Weights below 2^-126 of the largest are 0.  Other

@@ -14,7 +14,8 @@
 // weights take the place of the rotary panel, which is done with by then.
 //
 // Codes become fp16 times the row's scales, each divided by a power of two 2^e of the
-// row (at least its largest scale): half a step of fp16 of every value.  2^e goes to the
+// row (the one not below its largest scale, over 128, so that values fill fp16's range):
+// half a step of fp16 of every value, and of the factors of small groups.  2^e goes to the
 // row's scores (a thread has one row, all query rows) and to its weights.  The rotary dims
 // have a product of their own then, in their own type.  The running maximum is only raised,
 // and O rescaled, when a score is more than 2^8 above what it was; sums are in fp32, of
@@ -728,13 +729,15 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
           send_rope();
         }
         cp_async_commit();
-        // The row's 2^e, the power of two not below its largest scale, within what has a
-        // reciprocal and leaves room for a weight; and this quarter's scale over it.
+        // The row's 2^e, a 128th of the power of two not below its largest scale (448 of
+        // that are in fp16's range), within what has a reciprocal and leaves room for a
+        // weight; and this quarter's scale over it.
         float e = kNoScale, sc = 0.f;
         if (row >= 0) {
           const uint4 x = ld_stream_v4(p.rows + row * p.row_stride + kLatent);
           const uint32_t most = max(max(x.x & 0x7FFFFFFFu, x.y & 0x7FFFFFFFu), max(x.z & 0x7FFFFFFFu, x.w & 0x7FFFFFFFu));
-          e = __uint_as_float(min(max((most + 0x007FFFFFu) & 0x7F800000u, 0x17800000u), 0x78000000u));
+          const int over = static_cast<int>((min(most, 0x7F800000u) + 0x007FFFFFu) & 0x7F800000u) - (7 << 23);
+          e = __int_as_float(min(max(over, 0x17800000), 0x78000000));
           sc = __uint_as_float(g < 2 ? (g == 0 ? x.x : x.y) : (g == 2 ? x.z : x.w)) * (1.0f / e);
         }
         const uint32_t f = pack2<false>(sc, sc);

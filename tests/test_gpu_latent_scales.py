@@ -178,6 +178,28 @@ def test_equal_scores_of_rows_far_apart(dev, heads):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("heads", [3, 20, 64])
+@pytest.mark.parametrize("apart", [8, 14, 17, 20, 24])
+@pytest.mark.parametrize("seen", [1, 250])
+def test_small_groups(dev, dtype, heads, apart, seen):
+    """A group 2^-apart of its row's largest, with scales that are no powers of two; a single row's
+    outputs are its values."""
+    dt = TORCH[dtype]
+    g = torch.Generator().manual_seed(apart)
+    n = 260
+    codes, scales, pe = some(g, n, dt, 1.0)
+    scales[:, 2] *= 2.0 ** -apart
+    scales *= 0.5 + 0.5 * torch.rand(n, GROUPS, generator=g).double()
+    scales = scales.float().double()
+    rows, held = rows_of(codes, scales, pe)
+    q = (0.05 * torch.randn(2, heads, R + P, generator=g)).to(dt)
+    if seen == 1:
+        q.zero_()
+    index = torch.stack([torch.randperm(n, generator=g)[:seen] for _ in range(2)]).tolist()
+    indexed(dev, q, rows, held, scales, index, (R + P) ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("heads,new", [(1, 5), (4, 4), (5, 5), (8, 6), (16, 3), (64, 2), (20, 3)])
 @pytest.mark.parametrize("ctx", [3, 126, 500])
 def test_rows_of_later_tokens(dev, dtype, heads, new, ctx):
