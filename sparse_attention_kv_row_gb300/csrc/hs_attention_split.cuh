@@ -126,11 +126,13 @@ __device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t two) {
 
 // The power of two that brings a row of bf16 queries to fp16, where `top` is
 // the bits of its largest magnitude: to [2^8, 2^9), which keeps everything above
-// 2^-22 of it exact (2^62 at most: what is still small then scores nothing).  An
-// infinity or NaN passes through any factor.
+// 2^-22 of it exact.  An infinity or NaN passes through any factor.  kLeast is the biased
+// exponent from which on: 73 makes the factor 2^62 at most (what is still small then scores
+// nothing against cached values over one scale), 10 makes it 2^125, and all there are exact.
+template <int kLeast = 73>
 __device__ __forceinline__ float f16_factor(uint32_t top) {
   const int e = static_cast<int>(top >> 7);  // biased exponent
-  return __uint_as_float(static_cast<uint32_t>(262 - min(max(e, 73), 254)) << 23);
+  return __uint_as_float(static_cast<uint32_t>(262 - min(max(e, kLeast), 254)) << 23);
 }
 
 // Turns a row of bf16 queries, held by the four lanes of a row group in the

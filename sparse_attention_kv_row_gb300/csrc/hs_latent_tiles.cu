@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
           for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
         }
         top = __reduce_max_sync(kFullMask, top);
-        const float up = f16_factor(top);
+        const float up = f16_factor<10>(top);  // (rows may be as large as queries are small)
         if (lane == 0) sh.undo[u_at & 1][m] = 1.0f / up;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -151,7 +151,7 @@ def test_large_row_of_small_weight(dev, dtype, heads, power, apart):
 
 
 @pytest.mark.parametrize("heads", [3, 20, 64])
-@pytest.mark.parametrize("power", [-66, -40, 40])
+@pytest.mark.parametrize("power", [-66, -40, 40, 60, 100])
 def test_all_rows_small_or_large(dev, heads, power):
     g = torch.Generator().manual_seed(abs(power))
     codes, scales, pe = some(g, 700, torch.bfloat16, 2.0 ** power)
