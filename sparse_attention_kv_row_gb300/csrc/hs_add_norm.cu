@@ -134,8 +134,9 @@ __global__ void __launch_bounds__(kWarpRow ? kWarpRows * kWarp : 1024)
       return block_all(ss, part, add_op);
     }
   };
-  const float inv = inverse_rms(sum_of(1.f, s_sum[0]), p.inv_dim, p.eps,
-                                [&](float f) { return sum_of(f, s_sum[1]); });
+  const InverseRms by = inverse_rms(sum_of(1.f, s_sum[0]), p.inv_dim, p.eps,
+                                    [&](float f) { return sum_of(f, s_sum[1]); });
+  const uint64_t pre2 = pair(by.pre, by.pre), inv2 = pair(by.inv, by.inv);
   float y[kC][E];
   uint32_t top[kC];
 #pragma unroll
@@ -151,8 +152,15 @@ __global__ void __launch_bounds__(kWarpRow ? kWarpRows * kWarp : 1024)
     }
     top[i] = 0;
 #pragma unroll
+    for (int j = 0; j < E; j += 2) {
+      // (in pairs, 83.6 us for the 16384 tokens and 9.9 for the 4097; 84.3 and 10.3 singly)
+      const uint64_t z = mul2(mul2(pair(y[i][j], y[i][j + 1]), pre2), inv2);
+      const float2 f = unpair(mul2(z, pair(w[j], w[j + 1])));
+      y[i][j] = f.x;
+      y[i][j + 1] = f.y;
+    }
+#pragma unroll
     for (int j = 0; j < E; ++j) {
-      y[i][j] = y[i][j] * inv * w[j];
       // (chunks past the token hold zeros; with an infinite sum they would not)
       if (c < chunks) top[i] = larger_bits(top[i], y[i][j]);
     }
@@ -225,13 +233,13 @@ __global__ void __launch_bounds__(kGenThreads) add_norm_general(const AddNormPar
   ss = block_all(ss, s_sum[0], add_op);
   __syncthreads();  // (what was kept is read by other threads; residual_out may be x)
   auto stream = [&](int64_t d) { return kept != nullptr ? T::load(kept + d * T::kBytes) : sum(d); };
-  const float inv = inverse_rms(ss, p.inv_dim, p.eps, [&](float f) {
+  const InverseRms by = inverse_rms(ss, p.inv_dim, p.eps, [&](float f) {
     float again = 0.f;
     for (int d = tid; d < p.dim; d += kGenThreads) again = fmaf(stream(d) * f, stream(d) * f, again);
     return block_all(again, s_sum[1], add_op);
   });
   auto value = [&](int64_t d) {
-    return stream(d) * inv * (p.weight != nullptr ? T::load(p.weight + d * T::kBytes) : 1.f);
+    return stream(d) * by.pre * by.inv * (p.weight != nullptr ? T::load(p.weight + d * T::kBytes) : 1.f);
   };
   if (p.codes != nullptr) {
     unsigned char* codes = p.codes + t * p.codes_row;

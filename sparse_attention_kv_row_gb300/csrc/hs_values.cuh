@@ -109,17 +109,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// 1 / sqrt(mean square + eps); 0 where both are zero, so that zeros stay zero without
-// eps too (0 times infinity would be NaN).  Where the squares leave fp32's range, or all
-// but do, sum_of(f) is asked for the sum of squares of the values times the power of two f.
+// 1 / sqrt(mean square + eps) as two factors, for values are multiplied by one after the
+// other: the inverse of a subnormal root is past fp32's range.  0 where both are zero, so
+// that zeros stay zero without eps too (0 times infinity would be NaN).  Where the squares
+// leave fp32's range, or all but do, sum_of(f) is asked for the sum of squares of the
+// values times the power of two f: 2^96 takes the least of them (2^-149) to 2^-53, and
+// those of a mean square below 2^-100 to 2^54 at most.
+struct InverseRms {
+  float pre, inv;
+};
 template <typename Sum>
-__device__ __forceinline__ float inverse_rms(float sum_sq, float inv_dim, float eps, Sum sum_of) {
-  float ms = sum_sq * inv_dim + eps, f = 1.f;
-  if (ms < 0x1p-100f || (ms > 0x1p127f && eps < 0x1p126f)) {
-    f = ms < 1.f ? 0x1p63f : 0x1p-80f;
-    ms = sum_of(f) * inv_dim + eps * f * f;
+__device__ __forceinline__ InverseRms inverse_rms(float sum_sq, float inv_dim, float eps, Sum sum_of) {
+  float ms = sum_sq * inv_dim + eps;
+  InverseRms r{1.f, 1.f};
+  if (ms < 0x1p-100f) {
+    r.pre = 0x1p96f;
+    ms = sum_of(r.pre) * inv_dim + eps * r.pre * r.pre;
+  } else if (ms > 0x1p127f && eps < 0x1p126f) {
+    r = InverseRms{0x1p-40f, 0x1p-40f};  // (what that makes subnormal ends below 2^-149)
+    ms = sum_of(0x1p-80f) * inv_dim + eps * 0x1p-80f * 0x1p-80f;
   }
-  return ms == 0.f ? 0.f : rsqrtf(ms) * f;
+  r.inv = ms == 0.f ? 0.f : rsqrtf(ms) * r.inv;
+  return r;
 }
 
 // The larger of `top` and the magnitude of x, as bits: they order like the values, and

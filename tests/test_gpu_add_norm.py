@@ -135,6 +135,21 @@ def test_squares_out_of_range(dev, size, T, D):
     run(dev, T, D, "f32", x=x, residual=False, eps=0.0, group=128)
 
 
+@pytest.mark.parametrize("size", [2.0 ** -148, 2.0 ** -140, 1e-40, 2.0 ** -128, 1e-37, 8e37])
+@pytest.mark.parametrize("T,D", [(3, 512), (400, 256), (3, 1001)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_subnormal_and_largest_values(dev, size, T, D, dtype):
+    """Roots whose inverse leaves fp32's range; some of the values, and a whole token, are zeros."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(T, D, generator=g).clamp(-4, 4).double() * size
+    x[torch.rand(T, D, generator=g) < 0.2] = 0.0
+    x[-1] = 0.0
+    x[1, :-1] = 0.0  # one value alone
+    x[1, -1] = size
+    run(dev, T, D, dtype, x=x.to(TORCH[dtype]), residual=False, eps=0.0, group=128)
+    run(dev, T, D, dtype, x=x.to(TORCH[dtype]), residual=False, eps=0.0, group=0, out=False, pow2=True)
+
+
 def test_nan_and_infinity(dev):
     import sparse_attention_kv_row_gb300 as hs
 

@@ -158,6 +158,34 @@ def test_zero_latent(dev):
         assert bool((rows[[0, 2]] == 0).all()) and bool((rows[[1, 3]] == 9).all())
 
 
+@pytest.mark.parametrize("R", [512, 384])
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "fp8"), ("bf16", "same"), ("f32", "same")])
+@pytest.mark.parametrize("size", [2.0 ** -133, 2.0 ** -128, 1e-37, 8e37])
+def test_subnormal_and_largest_latents(dev, R, dtype, fmt, size):
+    """Latents whose root's inverse leaves fp32's range, zeros among them, without eps."""
+    import sparse_attention_kv_row_gb300 as hs
+
+    dt = TORCH[dtype]
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(6, R, generator=g).clamp(-4, 4).double() * size
+    x[torch.rand(6, R, generator=g) < 0.2] = 0.0
+    x[2, 1:] = 0.0  # one value alone
+    x[2, 0] = size
+    x[5] = 0.0
+    x = x.to(dt)
+    w = (1 + 0.2 * torch.randn(R, generator=g)).to(dt)
+    rows = torch.zeros(8, row_bytes(R, 64), dtype=torch.uint8, device=dev) if fmt == "fp8" else \
+        torch.zeros(8, R + 64, dtype=dt, device=dev)
+    hs.latent_norm_rope_store(x.to(dev), torch.zeros(6, 64, dtype=dt, device=dev), w.to(dev), None, None, rows,
+                              torch.arange(6, device=dev), eps=0.0)
+    y, got = norm_plain(x, w, 0.0), rows[:6].cpu()
+    if fmt == "fp8":
+        check_codes(y, norm_error(R), got[:, :R].contiguous(), got[:, R:R + R // 32].contiguous().view(torch.float32),
+                    GROUP, False)
+    else:
+        close(got[:, :R], y, norm_error(R), dt, y.abs())
+
+
 def test_long_offsets(dev):
     """Rows whose offsets pass 32 bits."""
     import sparse_attention_kv_row_gb300 as hs
