@@ -686,8 +686,8 @@ hs_err hs_paged_attention_timeout_selftest(const hs_paged_attention_args* args,
  *              they may not be the same
  *  weight      dtype [dim] or NULL
  *  codes       E4M3 bytes [n_tokens, dim], stride in bytes, or NULL
- *  scales      fp32, strides in elements for tokens and groups (either order);
- *              NULL iff codes is
+ *  scales      fp32, strides in elements for tokens and groups (either order; each
+ *              scale has a place of its own); NULL iff codes is
  * out or codes must be given (or both); residual_out needs residual.  A token whose
  * r are all zero gives zeros, with eps = 0 too.  The sum of squares is held in fp32,
  * of scaled values where it would leave its range.  A scale below fp32's smallest

@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <numeric>
 
 #include "hs_device.cuh"
 #include "hs_host.h"
@@ -273,6 +274,17 @@ __global__ void __launch_bounds__(kGenThreads) add_norm_general(const AddNormPar
   }
 }
 
+// Whether two places t * a + g * b with t in [0, tokens) and g in [0, groups) are the same:
+// the least steps that make up for each other are b / gcd and a / gcd.
+bool places_shared(int64_t tokens, int64_t a, int64_t groups, int64_t b) {
+  if ((tokens > 1 && a == 0) || (groups > 1 && b == 0)) return true;
+  if (tokens <= 1 || groups <= 1) return false;
+  a = a < 0 ? -a : a;
+  b = b < 0 ? -b : b;
+  const int64_t d = std::gcd(a, b);
+  return b / d < tokens && a / d < groups;
+}
+
 using AddFn = void (*)(const AddNormParams);
 template <int kDtype>
 AddFn rows_fn(int per, bool warp_row) {
@@ -311,6 +323,9 @@ extern "C" hs_err hs_add_rms_norm(const hs_add_rms_norm_args* a, hs_stream_t str
                           (a->residual_out && a->residual_out_stride < a->dim) ||
                           (a->codes && a->codes_stride < a->dim)))
     return fail(HS_ERR_ARG, "%s: strides of outputs must cover dim", who);
+  if (a->scales && places_shared(a->n_tokens, a->scales_stride_token,
+                                 a->group > 0 ? (a->dim - 1ll) / a->group + 1 : 1, a->scales_stride_group))
+    return fail(HS_ERR_ARG, "%s: two scales have the same place", who);
   // Aliases are of whole tensors only: a token's bytes are read before they are written.
   if (a->out && a->out == a->residual_out)
     return fail(HS_ERR_ARG, "%s: out and residual_out are the same", who);

@@ -166,3 +166,16 @@ def test_python_checks():
             (lambda: hs.paged_latent_attention(q, rows, t, i, cu, i.float(), out, **kw), TypeError)):
         with pytest.raises(err):
             bad()
+
+
+@pytest.mark.parametrize("tokens,group,strides", [
+    (3, 16, (0, 1)), (3, 16, (4, 0)), (3, 16, (0, 0)), (3, 16, (1, 1)), (3, 16, (3, 1)), (3, 16, (1, 2)), (3, 16, (2, 2)),
+    (3, 16, (-2, 1)), (3, 16, (1 << 40, 0)), (2, 0, (0, 1)), (1, 16, (4, 0))])
+def test_scales_strides(lib, tokens, group, strides):
+    """Two scales in one place would race."""
+    places = [t * strides[0] + g * strides[1] for t in range(tokens) for g in range(64 // group if group else 1)]
+    assert len(set(places)) < len(places)
+    a = _norm(n_tokens=tokens, group=group, codes=16384, codes_stride=64, scales=4096, scales_stride_token=strides[0],
+              scales_stride_group=strides[1])
+    assert lib.hs_add_rms_norm(C.byref(a), None) == 1
+    assert b"scales" in lib.hs_last_error()
