@@ -743,7 +743,8 @@ hs_err hs_add_rms_norm(const hs_add_rms_norm_args* args, hs_stream_t stream);
  *              positions is NULL too)
  *  positions   int64 [n_tokens]
  *  q_pe, q_out in_dtype [n_tokens, num_heads, rope_dim], token and head strides in
- *              elements; num_heads 0 and NULL: no queries.  q_out may be q_pe itself
+ *              elements; num_heads 0 and NULL: no queries.  q_out may be q_pe itself;
+ *              two tokens that have the same place in it are refused
  *  rows        [num_rows] rows of row_format, row_stride bytes apart
  *  loc         int64 [n_tokens]
  *  status      int32 [1] or NULL: HS_ST_BAD_INDEX is OR-ed in when a token's loc is
@@ -812,7 +813,8 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  *  scale       positive
  *  status      int32, overwritten, or NULL: [n_tokens] with HS_LATENT_INDEX, else [batch]
  *  workspace   as in hs_paged_attention, hs_latent_attention_workspace_bytes of it
- * out and lse overlap no other buffer (not checked).  Rows of q that belong to no
+ * out and lse overlap no other buffer (not checked); two tokens whose outputs have the
+ * same place are refused.  Rows of q that belong to no
  * request are left as they were in out and lse.
  * Scores, sums and outputs are accumulated in fp32.  16-bit calls with R = 512 and
  * rope_dim = 64 run on the tensor cores, where the addresses and strides in bytes of

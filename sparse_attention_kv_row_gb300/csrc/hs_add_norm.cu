@@ -16,7 +16,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <numeric>
 
 #include "hs_device.cuh"
 #include "hs_host.h"
@@ -272,17 +271,6 @@ __global__ void __launch_bounds__(kGenThreads) add_norm_general(const AddNormPar
     for (int d = tid; d < p.dim; d += kGenThreads)
       T::store(p.out + t * p.out_row + static_cast<int64_t>(d) * T::kBytes, value(d));
   }
-}
-
-// Whether two places t * a + g * b with t in [0, tokens) and g in [0, groups) are the same:
-// the least steps that make up for each other are b / gcd and a / gcd.
-bool places_shared(int64_t tokens, int64_t a, int64_t groups, int64_t b) {
-  if ((tokens > 1 && a == 0) || (groups > 1 && b == 0)) return true;
-  if (tokens <= 1 || groups <= 1) return false;
-  a = a < 0 ? -a : a;
-  b = b < 0 ? -b : b;
-  const int64_t d = std::gcd(a, b);
-  return b / d < tokens && a / d < groups;
 }
 
 using AddFn = void (*)(const AddNormParams);

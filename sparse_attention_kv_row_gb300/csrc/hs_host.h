@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <numeric>
 
 #include "../../include/hisparse.h"
 
@@ -43,5 +44,16 @@ class CallRange {
 // Lemire-Kaser-Kurz divider constant for 1 <= d < 2^32 (d == 1 gives magic 0
 // and the device side short-circuits it).
 inline uint64_t fastdiv_magic(uint32_t d) { return d <= 1 ? 0ull : (~0ull) / d + 1ull; }
+
+// Whether two places t * a + g * b with t in [0, tokens) and g in [0, groups) are the same:
+// the least steps that make up for each other are b / gcd and a / gcd.
+inline bool places_shared(int64_t tokens, int64_t a, int64_t groups, int64_t b) {
+  if ((tokens > 1 && a == 0) || (groups > 1 && b == 0)) return true;
+  if (tokens <= 1 || groups <= 1) return false;
+  a = a < 0 ? -a : a;
+  b = b < 0 ? -b : b;
+  const int64_t d = std::gcd(a, b);
+  return b / d < tokens && a / d < groups;
+}
 
 }  // namespace hs

@@ -150,6 +150,10 @@ hs_err check_args(const hs_latent_attention_args* a) {
       a->row_stride < bytes)
     return fail(HS_ERR_ARG, "%s: head strides must cover their dims, row_stride a row of %lld bytes",
                 who, static_cast<long long>(bytes));
+  if (a->n_tokens > 1 &&
+      ((a->out_stride_token < a->latent_dim && a->out_stride_token > -a->latent_dim) ||
+       places_shared(a->n_tokens, a->out_stride_token, a->num_heads, a->out_stride_head)))
+    return fail(HS_ERR_ARG, "%s: two tokens' outputs have the same place", who);
   return HS_OK;
 }
 

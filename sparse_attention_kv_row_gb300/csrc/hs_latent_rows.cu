@@ -348,6 +348,9 @@ extern "C" hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* a, hs_str
                      a->q_stride_token < 0 || a->out_stride_token < 0)))
     return fail(HS_ERR_ARG, "%s: row_stride must cover a row, head strides rope_dim, token strides "
                             "be >= 0", who);
+  if (heads > 0 && a->n_tokens > 1 &&
+      (a->out_stride_token < a->rope_dim || places_shared(a->n_tokens, a->out_stride_token, heads, a->out_stride_head)))
+    return fail(HS_ERR_ARG, "%s: two tokens have the same place in q_out", who);
   if (heads > 0 && a->q_out == a->q_pe && a->n_tokens > 0 &&
       (a->out_stride_head != a->q_stride_head || a->out_stride_token != a->q_stride_token))
     return fail(HS_ERR_ARG, "%s: q_out may be q_pe itself, with its strides", who);

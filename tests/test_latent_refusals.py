@@ -179,3 +179,17 @@ def test_scales_strides(lib, tokens, group, strides):
               scales_stride_group=strides[1])
     assert lib.hs_add_rms_norm(C.byref(a), None) == 1
     assert b"scales" in lib.hs_last_error()
+
+
+@pytest.mark.parametrize("tokens,heads,strides", [
+    (2, 1, (0, 64)), (2, 2, (0, 64)), (3, 2, (63, 64)), (2, 2, (64, 64)), (3, 4, (128, 64)), (2, 3, (128, 128)), (4, 3, (192, 288))])
+def test_outputs_that_share_places(lib, tokens, heads, strides):
+    """Two tokens' outputs in one place would race."""
+    a = _rows(n_tokens=tokens, num_heads=heads, out_stride_token=strides[0], out_stride_head=strides[1])
+    assert lib.hs_latent_norm_rope_store(C.byref(a), None) == 1
+    assert b"q_out" in lib.hs_last_error()
+    for kw in ({}, INDEX):
+        a = _attn(**kw | dict(n_tokens=tokens, num_heads=heads, out_stride_token=strides[0] * 8, out_stride_head=strides[1] * 8,
+                              q_stride_token=9216))
+        assert lib.hs_latent_attention(C.byref(a), None) == 1
+        assert b"outputs" in lib.hs_last_error()
