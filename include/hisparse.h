@@ -814,8 +814,8 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  *  status      int32, overwritten, or NULL: [n_tokens] with HS_LATENT_INDEX, else [batch]
  *  workspace   as in hs_paged_attention, hs_latent_attention_workspace_bytes of it
  * out and lse overlap no other buffer (not checked); two tokens whose outputs have the
- * same place are refused.  Rows of q that belong to no
- * request are left as they were in out and lse.
+ * same place are refused.  Rows of q that belong to no request are left as they were in
+ * out and lse.
  * Scores, sums and outputs are accumulated in fp32.  16-bit calls with R = 512 and
  * rope_dim = 64 run on the tensor cores, where the addresses and strides in bytes of
  * q, out and rows are multiples of 16.  There the weights are rounded to the type of the
@@ -834,9 +834,9 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  * Limits: R <= 512, rope_dim <= 256, batch <= 2048, top_k <= 2^30, num_rows, n_tokens
  * and max_q_len * num_heads < 2^31, R a multiple of 128 for HS_ROW_E4M3, which wants
  * 16-bit types (else HS_ERR_UNSUPPORTED); L at most 2^30, and so short that 32-bit whole
- * numbers count the batch's tiles: with u = max(1, floor(16 / num_heads)) tokens a unit,
- * (n_tokens / u + batch) * ceil(num_heads / 32) * (L + 512) <= 2^38 - 128 is enough
- * (HS_ST_BAD_STATE for a longer row).
+ * numbers count the batch's tiles: with u = max(1, floor(16 / num_heads)) tokens a unit
+ * and L rounded up to a multiple of 128, (n_tokens / u + batch) * ceil(num_heads / 32) *
+ * (L + 512) <= 2^38 - 128 is enough (HS_ST_BAD_STATE for a longer row).
  */
 #define HS_LATENT_INDEX 4 /* beside HS_SEQ_LENS_I64 and HS_REQ_STATE_I64 in flags */
 typedef struct hs_latent_attention_args {

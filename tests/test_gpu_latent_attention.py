@@ -225,6 +225,29 @@ def test_rows_listed_twice(hs, dev, dtype, fmt):
     a.check(hs, dev, "tiles")
 
 
+def test_longest_row(hs, dev):
+    """The longest row that the limit's formula allows is served, one past it is refused: rows
+    outside the pool, so that every score is 0."""
+    T, L = 16 * 1023, 128 * ((2 ** 31 - 1) // 1024 - 4)
+    assert 1024 * (L + 512) <= 2 ** 38 - 128 < 1024 * (L + 128 + 512)
+    f = dict(device=dev)
+    q = torch.zeros(T, 1, 576, dtype=torch.bfloat16, **f)
+    out, lse = torch.zeros(T, 1, 512, dtype=torch.bfloat16, **f), torch.zeros(T, 1, **f)
+    rows, status = torch.zeros(16, 656, dtype=torch.uint8, **f), torch.zeros(1, dtype=torch.int32, **f)
+    for n, want in ((L, 64), (L + 1, 32), (L + 127, 32)):
+        out.fill_(-7)
+        lse.fill_(-7)
+        hs.paged_latent_attention(q, rows, torch.zeros(1, 1, dtype=torch.int32, **f), torch.zeros(1, dtype=torch.int64, **f),
+                                  torch.tensor([0, 1], dtype=torch.int32, **f), torch.tensor([n], **f), out, max_q_len=1,
+                                  page_size=1 << 28, scale=1.0, lse=lse, status=status)
+        assert int(status) == want
+        assert bool((out[1:] == -7).all()) and bool((lse[1:] == -7).all())
+        if want == 64:
+            assert bool((out[0] == 0).all()) and abs(float(lse[0, 0]) - math.log(n)) < 1e-3
+        else:
+            assert bool((out[0] == -7).all()) and bool((lse[0] == -7).all())
+
+
 # ------------------------------------------------------------------ streams, graphs, workspaces
 @pytest.mark.parametrize("fmt", ["fp8", "same"])
 @pytest.mark.parametrize("heads", [16, 64])
