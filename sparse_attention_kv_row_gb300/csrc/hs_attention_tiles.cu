@@ -275,7 +275,7 @@ struct Loader {
     uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      v[j] = pack2t<false>(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
+      v[j] = pack2<false>(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
     return make_uint4(v[0], v[1], v[2], v[3]);
   }
   // The larger of `top` and the magnitudes (as bits) of eight bf16 values.
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const uint64_t sc2 = two_floats(sc, sc), ref2 = two_floats(-ref, -ref);
+        const uint64_t sc2 = pair(sc, sc), ref2 = pair(-ref, -ref);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -513,11 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 16; ++c) {
             const uint64_t x = fma2(two_words(s[q][2 * c], s[q][2 * c + 1]), sc2, ref2);
             const float a = fast_exp2(low_float(x)), b = fast_exp2(high_float(x));
-            sum[c & 1] = add2(sum[c & 1], two_floats(a, b));
+            sum[c & 1] = add2(sum[c & 1], pair(a, b));
             // The weights take the type of V, as one product wants of its operands:
             // half a step off each, whose errors average out over the keys.  The sum
             // keeps them whole, for the log-sum.
-            w16[c] = pack2t<kBf16>(a, b);
+            w16[c] = pack2<kBf16>(a, b);
           }
           tmem_st16(s_at + q * 16, w16);
           if (q == 1) {
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_pin(o);
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            x[c] = pack2t<kIn == HS_DT_BF16>(__uint_as_float(o[2 * c]) * f, __uint_as_float(o[2 * c + 1]) * f);
+            x[c] = pack2<kIn == HS_DT_BF16>(__uint_as_float(o[2 * c]) * f, __uint_as_float(o[2 * c + 1]) * f);
           send(x, d * 2);
         }
       } else {
@@ -998,7 +998,7 @@ __global__ void __launch_bounds__(kTilesJoinThreads)
     const int64_t tok = row.q0 + i;
     constexpr bool kB = kIn == HS_DT_BF16;
     *reinterpret_cast<uint2*>(p.out + tok * p.out_token + head * p.out_head + lane * 8) =
-        make_uint2(pack2t<kB>(acc.x * f, acc.y * f), pack2t<kB>(acc.z * f, acc.w * f));
+        make_uint2(pack2<kB>(acc.x * f, acc.y * f), pack2<kB>(acc.z * f, acc.w * f));
     if (lane == 0 && p.lse)
       p.lse[tok * p.heads + head] = kLn2 * (top + log2f(l));
   }

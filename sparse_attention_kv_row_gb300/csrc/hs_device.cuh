@@ -1,6 +1,6 @@
-// hs_device.cuh -- device helpers for the swap-in and mover kernels (sm_103a):
-// cache-hinted loads/stores as inline PTX, LDGSTS staging into shared memory,
-// warp scans, and a 32-bit divider by multiply-high.
+// hs_device.cuh -- device helpers that the kernels share (sm_103a): cache-hinted
+// loads/stores as inline PTX, LDGSTS staging into shared memory, warp scans, a 32-bit
+// divider by multiply-high, and paired fp32 operations.
 #pragma once
 
 #include <cstdint>
@@ -289,6 +289,49 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv f) {
 // floor(n / f.d), also for d == 1 (whose multiplier is not representable).
 __device__ __forceinline__ uint32_t div_any(uint32_t n, FastDiv f) {
   return f.d == 1 ? n : fast_div(n, f);
+}
+
+// ------------------------------------------------------------------ pairs of values
+// Pairs of fp32 values and the paired operations on them.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Two fp32 values rounded to 16 bits.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 }  // namespace hs

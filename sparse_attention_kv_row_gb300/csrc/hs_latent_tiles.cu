@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
         const int j = k * kKeys + tid;
         // Scores over their reference points, two query rows at a time.
         uint64_t z2[N / 2];
-        const uint64_t c2 = two_floats(c, c), s22 = two_floats(s2, s2);
+        const uint64_t c2 = pair(c, c), s22 = pair(s2, s2);
 #pragma unroll
         for (int q = 0; q < N; q += kStep) {
           uint32_t a[kStep];
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
         // Times 2^e first: at least 2^-80 of a weight, at most 2^(113 + 8), is in fp32's range,
         // and what falls below it is nothing beside the query row's largest.
         const float to_e = fmaxf(mine, 0.f);
-        const uint64_t to_e2 = two_floats(to_e, to_e);
+        const uint64_t to_e2 = pair(to_e, to_e);
         ulonglong2 own[2], then[2];  // shares, read a step ahead of the stores
         auto read_shares = [&](ulonglong2 (&to)[2], int q) {
           if constexpr (kCodes) {
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
             // The weights take the type of the values, as one product wants of its
             // operands: half a step off each, whose errors average out over the rows.
             if constexpr (kCodes) {
-              const uint64_t y = mul2(mul2(two_floats(e0, e1), to_e2), i & 1 ? own[i / 2].y : own[i / 2].x);
+              const uint64_t y = mul2(mul2(pair(e0, e1), to_e2), i & 1 ? own[i / 2].y : own[i / 2].x);
               v[i] = pack2<false>(low_float(y), high_float(y));
             } else {
               v[i] = pack2<kBf16>(e0, e1);

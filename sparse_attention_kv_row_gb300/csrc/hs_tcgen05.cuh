@@ -141,14 +141,11 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // ------------------------------------------------------------------ operands and waits
-// Pairs of floats in 64-bit registers and the paired fp32 operations on them.
+// Words and halves of a pair of floats (hs_device.cuh has the operations on pairs).
 __device__ __forceinline__ uint64_t two_words(uint32_t lo, uint32_t hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
   return r;
-}
-__device__ __forceinline__ uint64_t two_floats(float lo, float hi) {
-  return two_words(__float_as_uint(lo), __float_as_uint(hi));
 }
 __device__ __forceinline__ float low_float(uint64_t x) {
   return __uint_as_float(static_cast<uint32_t>(x));
@@ -156,22 +153,6 @@ __device__ __forceinline__ float low_float(uint64_t x) {
 __device__ __forceinline__ float high_float(uint64_t x) {
   return __uint_as_float(static_cast<uint32_t>(x >> 32));
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // 16-byte chunk c (of 64 elements' eight) of row r of a panel.
 __device__ __forceinline__ uint32_t in_panel(int r, int c) {
   return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
@@ -189,16 +170,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                : "memory");
   return v;
 }
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack2t(float lo, float hi) {
-  uint32_t r;
-  if constexpr (kBf16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 constexpr uint64_t kWaitNs = 2000000000ull;
 // Waits for phase `parity`, unless the block has given up; gives up itself
 // after kWaitNs.

@@ -1,5 +1,5 @@
 // hs_values.cuh -- element types of the norm kernels: single values and 16-byte
-// chunks to and from fp32, E4M3 codes, and paired fp32 operations.
+// chunks to and from fp32, E4M3 codes, and the inverse of a norm.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "../../include/hisparse.h"
+#include "hs_device.cuh"
 
 namespace hs {
 
@@ -80,33 +81,6 @@ __device__ __forceinline__ uint4 pack(const float* x) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Pairs of fp32 values and the paired operations on them.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 // 1 / sqrt(mean square + eps) as two factors, for values are multiplied by one after the
