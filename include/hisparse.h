@@ -827,7 +827,8 @@ hs_err hs_latent_norm_rope_store(const hs_latent_rows_args* args, hs_stream_t st
  * power of two of its token and head, half a step off or 2^-30 of the largest such product;
  * a bf16 query's latent dims are taken as fp16 over a power of two of the query row, exact
  * within 2^-22 of its largest value.  Weights below 2^-126 of the largest are 0.  Other
- * calls hold everything in fp32.
+ * calls (fp32, other dims, other alignments) hold everything in fp32, in a kernel for
+ * correctness that is hundreds of times slower.
  * Time-out: the waits of the tensor-core kernel are bounded.  If one runs out (the GPU did
  * not complete a copy or a product within two seconds), every status word reports
  * HS_ST_TIMEOUT and the outputs of the call are undefined; treat the context as suspect.

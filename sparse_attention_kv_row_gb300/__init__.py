@@ -1015,7 +1015,8 @@ def latent_attention(q, rows, row_index, out, *, scale, lse=None, status=None, w
     ``rows`` (layouts as in ``latent_norm_rope_store``; see include/hisparse.h).  ``lse`` [T, heads]
     gets the softmax's log-sum-exp, ``status`` [T] the HS_ST_* bits.  ``workspace`` (uint8, 256-byte
     aligned, ``latent_attention_workspace_bytes`` of it) may be passed to keep one for a captured
-    graph; otherwise one is allocated for the call."""
+    graph; otherwise one is allocated for the call.  16-bit calls with R = 512, P = 64 and 16-byte
+    aligned addresses and strides run on the tensor cores, all others hundreds of times slower."""
     dev, fields = _indexed_fields(q, rows, row_index, out, scale, lse, status)
     _latent_attend("hs_latent_attention", _lib().hs_latent_attention, q, dev, fields, workspace,
                    stream)

@@ -9,8 +9,9 @@
 // thread c mod threads), as r in its own type; a group of codes lies in neighbouring
 // lanes, so that its maximum is a few shuffles.  A block per token, or a warp for
 // short ones.
-// Measured: 16384 bf16 tokens of 4096 with codes of 128 (472 MB) 84 us, 5.6 TB/s of 6.8
-// for a copy; 4097 tokens of 2304 10.0 us; 32 tokens 2.5 us, a launch.
+// Measured: 16384 bf16 tokens of 4096 with codes of 128 (472 MB) 83 us, 5.7 TB/s of 6.8
+// for a copy, with an instruction issued in 75 % of the cycles; 4097 tokens of 2304 9.9 us;
+// 32 tokens 2.5 us, a launch.
 // add_norm_general: any size, alignment and group; a block per token that reads it
 // again for each step.
 #include <cuda_runtime.h>
@@ -371,7 +372,7 @@ extern "C" hs_err hs_add_rms_norm(const hs_add_rms_norm_args* a, hs_stream_t str
   const bool rows = al % 16 == 0 && cal % E == 0 && a->dim % E == 0 && (!p.codes || groups) &&
                     chunks <= 4 * 1024;
   // Few chunks a thread where there are few tokens (the call is as long as one of
-  // them), four where there are many (84 us for the 16384; one 92, two 92, eight 112).
+  // them), four where there are many (83 us for the 16384; one 92, two 92, eight 112).
   const bool warp_row = rows && chunks <= 4 * kWarp && a->n_tokens >= 2 * dev.sm_count;
   int per = warp_row ? (chunks + kWarp - 1) / kWarp : (a->n_tokens >= 2 * dev.sm_count ? 4 : 1);
   if (warp_row && per == 3) per = 4;

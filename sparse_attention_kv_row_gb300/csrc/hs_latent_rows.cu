@@ -11,7 +11,8 @@
 // 16 of its query heads, four lanes a head; such a lane holds both halves of every pair
 // that it turns.
 // Measured: 4097 tokens with 128 query heads to codes 28 us (142 MB, 5.0 TB/s of 6.8 for
-// a copy), 16384 with 16 to 16-bit rows 22 us; 32 tokens 2.7 us, a launch.
+// a copy; the warps wait for their loads, 46 % of an SM's place for warps taken in so short
+// a run), 16384 with 16 to 16-bit rows 22 us; 32 tokens 2.7 us, a launch.
 // latent_rows_general: any type, size and alignment; a warp per latent row or head,
 // staged in shared memory.
 #include <cuda_runtime.h>

@@ -39,10 +39,10 @@
 // What bounds it: the chain of a tile (its rows come in, four times the keys' product with
 // what has come, softmax, four times the values' product, and only then room for the next
 // rows), behind a start of some 8 us.  One unit an SM over codes takes, for 1, 2, 4, 8 and
-// 16 tiles, 12.8, 16.9, 25.5, 43.9 and 81.1 us with 16 query rows and 16.4, 22.6, 35.2,
-// 69.4 and 124.5 us with 64: 4.7 and 6.9 us a tile, 2.5 TB/s of rows and 0.35 PFLOP/s at
-// 16 tiles.  Nothing is full then (memory to 2.6 of 6.8 TB/s, shared memory to 37 %, the
-// tensor cores to 22 %, the issue of instructions to 31 %): the chain takes the time.
+// 16 tiles, 12.8, 17.1, 26.1, 45.2 and 83.3 us with 16 query rows and 16.9, 23.5, 36.7,
+// 72.2 and 130.5 us with 64: 4.8 and 7.3 us a tile, 2.5 TB/s of rows and 0.33 PFLOP/s at
+// 16 tiles.  Nothing is full then (memory to 2.7 of 6.8 TB/s, L2 to 40 %, shared memory to
+// 38 %, the tensor cores to 22 %, the issue of instructions to 32 %): the chain takes the time.
 // Measured against it, at 16 tiles: 16 query rows by 32 latent rows on mma.sync, eight warps
 // on their own (94 us, and 330 for 64 query rows, which it does 16 at a time); half of the
 // codes landing a tile ahead in buffers of their own (5 % slower in a decode batch); rows of
@@ -90,8 +90,10 @@ static_assert(softmax_regs(64) + 4 * convert_regs(64) + product_regs(64) <= 6 * 
 constexpr float kNoScale = 0x1p-80f;       // 2^e of a row of zeros, and the least there is
 constexpr float kRaise = 8.f;             // log2 of how far weights may exceed their reference
 constexpr float kF16Bias = 6.f;           // log2 of that reference in fp16: what is 2^-30 of it stays
-// A unit's fixed cost (its queries, its outputs) in tiles.  Counted as 1, 2, 3 and 4 it makes a
-// batch of chunks take 110, 95, 87 and 89 us, others within 3 % of each other.
+// A unit's fixed cost (its queries, its outputs) in tiles, one number for all kernels.  Counted
+// as 1, 2, 3 and 4 it made a batch of chunks take 110, 95, 87 and 89 us when it was chosen, and
+// makes it 82.0, 79.2, 83.2 and 87.0 now; decode of 32 requests 74.7, 75.5, 77.4 and 78.2, drafts
+// over 16-bit rows 48.0, 47.4, 47.3 and 49.6.
 constexpr int kUnitCost = 3;
 
 struct LatentTilesParams : LatentParams {
@@ -969,9 +971,10 @@ __global__ void __launch_bounds__(block_threads(kCodes), 1)
 }
 
 constexpr int kDimJoin = kLatent / 4;  // threads: four dims each
-// Query rows of a block, and parts of them, whose loads are on their way together: few rows
-// are cut into many parts (18 of 2 tokens: 14.8 us with the kernel before it, 20.4 with four
-// rows of two parts), many rows into few (66.1 us for 64 rows of 2 or 3 parts, 70.3 a row at a time).
+// Query rows of a block, and parts of them, whose loads are on their way together.  Units of
+// few rows may be cut into many parts (18 for each of 2 tokens: 15.0 us with the kernel before
+// it, 20.8 with four rows of two parts), those of 64 rows seldom are (58.5 us for 32 tokens of
+// 128 heads in 2 or 3 parts, 60.5 a row at a time).
 constexpr int join_rows(int n) { return n / 16; }
 constexpr int join_parts(int n) { return n == 16 ? 8 : 2; }
 
@@ -1060,7 +1063,7 @@ TilesKernels pick(int in_dtype, bool codes, int n) {
 }
 
 // Query rows of a unit: as many as there are, up to 64, since every unit reads its latent rows
-// again (125 us for 64 at once over 16 tiles, four times 81 for 16 at a time); 32 where
+// again (131 us for 64 at once over 16 tiles, four times 83 for 16 at a time); 32 where
 // the batch's running sums would not fit beside 64.
 int unit_rows(const LatentParams& p) {
   const int64_t rows = static_cast<int64_t>(p.heads) * (p.indexed ? 1 : p.max_q);
